@@ -281,12 +281,167 @@ mlora_status mlora_linear_noalloc(const void *x, const void *W, int64_t T, int64
                                   hipStream_t stream);
 
 /*
+ * ---- The attention step after a merged QKV layer -------------------------------------------
+ *
+ * A serving step runs mlora_linear on the merged layer, mlora_qk_rope on its rows (norms,
+ * rotation, K and V into the paged cache), then mlora_attention (whole prompts) or
+ * mlora_paged_attention (new tokens over the cache: one token a sequence when decoding).
+ * head_dim is 64 or 128; query head i reads kv head i / (n_q_heads / n_kv_heads).
+ */
+
+/* Limits of the attention entry points. */
+#define MLORA_CACHE_BF16 0        /* dtype of mlora_cache: bfloat16 values                     */
+#define MLORA_CACHE_E4M3 1        /* 8-bit e4m3 codes with an fp32 scale per token and head    */
+#define MLORA_MAX_PAGE 256        /* page_size: a power of two from 16 to 256                  */
+#define MLORA_MAX_HEADS 1024      /* query heads                                               */
+
+/* scaling of mlora_rope_turns */
+#define MLORA_ROPE_PLAIN 0
+#define MLORA_ROPE_LINEAR 1       /* every pair slowed down by factor                          */
+#define MLORA_ROPE_PARTS 2        /* slow pairs by factor, fast ones kept, a ramp between      */
+
+/*
+ * A paged cache of one layer's keys and values.  Token `slot` sits in page slot / page_size at
+ * offset slot % page_size; one kv head of a page is contiguous.  In e4m3 a vector is
+ * code * scale, scale = max(amax, 2^-90) / 448 of the vector.
+ */
+typedef struct {
+    void *k, *v;              /* bf16 or e4m3 [n_pages][n_kv_heads][page_size][head_dim]       */
+    float *k_scale, *v_scale; /* fp32 [n_pages][n_kv_heads][page_size]; e4m3 only, else NULL   */
+    int32_t n_pages, n_kv_heads, page_size, head_dim;
+    int32_t dtype;            /* MLORA_CACHE_BF16 or MLORA_CACHE_E4M3                          */
+} mlora_cache;
+
+/*
+ * Rotation by position of the first rot_dim values of a head (rot_dim a multiple of 16, at most
+ * head_dim; 0: none, turns unused).  Pair i turns by frac(pos * turns[i] / 2^64) of a circle:
+ * integer arithmetic modulo 2^64, exact at any position, so no table over positions is kept.
+ * Pairs are (i, i + rot_dim / 2), or (2 i, 2 i + 1) when `interleaved` is non-zero; cosine and
+ * sine are multiplied by `magnitude` (1, or what the scaling for long contexts asks for).
+ */
+typedef struct {
+    const uint64_t *turns;    /* uint64 [rot_dim / 2] device (mlora_rope_turns)                */
+    int32_t rot_dim;
+    int32_t interleaved;
+    float magnitude;
+} mlora_rope;
+
+/*
+ * Host helper: turns[i] (host, rot_dim / 2 values) = 2^64 * f_i, f_i = base^(-2 i / rot_dim) /
+ * (2 pi) turns per position, computed in long double.  MLORA_ROPE_LINEAR divides f_i by factor.
+ * MLORA_ROPE_PARTS keeps pairs with at least `fast` turns in orig_len positions, divides those
+ * with at most `slow` by factor, and ramps linearly in the number of turns between.
+ * MLORA_ERR_ARG on NULL, rot_dim not a positive even number, base <= 1, factor < 1, unknown
+ * scaling, or (PARTS) orig_len < 1 or fast <= slow.
+ */
+mlora_status mlora_rope_turns(int32_t rot_dim, double base, int32_t scaling, double factor,
+                              int64_t orig_len, double fast, double slow, uint64_t *turns);
+
+/* Host helper: bytes of a cache's k and v buffers (and scales) together; -1 on arguments outside
+ * the limits above. */
+int64_t mlora_cache_bytes(int64_t n_pages, int32_t n_kv_heads, int32_t page_size,
+                          int32_t head_dim, int32_t dtype);
+
+/*
+ * Norm, rotation and cache write of T rows of a merged QKV layer.  Row t holds n_q_heads query
+ * heads, then n_kv_heads key heads, then n_kv_heads value heads of head_dim values:
+ *   n = x * (mean(x^2) + eps)^(-1/2) * weight   (queries and keys with a weight; else n = x)
+ *   o = n rotated by pos[t]
+ * in fp32, rounded once: queries to q_out, keys to k_out and to the cache, values (unchanged) to
+ * the cache.
+ *   qkv      bf16 [T] rows, row_stride elements apart
+ *   pos      int32 [T]
+ *   q_weight, k_weight  bf16 [head_dim], each may be NULL (no norm)
+ *   q_out    bf16 [T][n_q_heads * head_dim], rows q_stride elements apart
+ *   k_out    bf16 [T][n_kv_heads * head_dim], rows k_stride elements apart, or NULL
+ *   cache, slot  where K and V go: slot int32 [T], a token whose slot is outside
+ *            [0, n_pages * page_size) (-1: padding) is not stored; both NULL: no cache.  Two
+ *            tokens of one call must not name the same slot.
+ * q_out and k_out may be the rows' own query and key parts (in place) but overlap qkv in no
+ * other way.  Strides are multiples of 8.  T = 0 is a no-op.
+ */
+mlora_status mlora_qk_rope(const void *qkv, int64_t T, int64_t row_stride, int32_t n_q_heads,
+                           int32_t n_kv_heads, int32_t head_dim, const int32_t *pos,
+                           const mlora_rope *rope, const void *q_weight, const void *k_weight,
+                           float eps, void *q_out, int64_t q_stride, void *k_out,
+                           int64_t k_stride, const mlora_cache *cache, const int32_t *slot,
+                           hipStream_t stream);
+
+/*
+ * Cached tokens back as bf16 (e4m3: code * scale, rounded once):
+ *   k, v  bf16 [T][n_kv_heads][head_dim] (either may be NULL);  slot int32 [T], tokens whose
+ *   slot is outside [0, n_pages * page_size) give zeros.
+ */
+mlora_status mlora_cache_read(const mlora_cache *cache, const int32_t *slot, int64_t T, void *k,
+                              void *v, hipStream_t stream);
+
+/*
+ * Attention over whole prompts, packed: sequence b owns query rows [cu_q[b], cu_q[b+1]) and key
+ * rows [cu_k[b], cu_k[b+1]) (cu_k NULL: the same as cu_q).  With n queries and L keys, query i
+ * stands at p = L - n + i and sees key j when j < L, j <= p (if causal) and j > p - window (if
+ * window > 0):
+ *   out = sum_j softmax_j(scale q . k_j) v_j    over the keys it sees, fp32 softmax
+ *   lse = ln sum_j exp(scale q . k_j)
+ * A query that sees no key gives zeros and lse = -inf; what it does not see has no effect on it,
+ * infinities and NaN included.  Probabilities are rounded to bf16 for the product with V.
+ *   q   bf16 [T_q][n_q_heads * head_dim], rows q_stride elements apart (k, v: T_k rows of
+ *       n_kv_heads * head_dim; strides multiples of 8, so views of a merged row will do)
+ *   out bf16 like q, rows out_stride apart;  lse fp32 [T_q][n_q_heads], or NULL
+ *   cu_q, cu_k  int32 [n_seqs + 1] device, ascending from 0; entries beyond the T given are read
+ *       as T.  max_q: an upper bound of the sequences' query counts (host; sizes the launch).
+ *   scale  of the scores; 0 means head_dim^(-1/2)
+ */
+mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, int64_t T_q, int64_t T_k,
+                             int32_t n_seqs, const int32_t *cu_q, const int32_t *cu_k,
+                             int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                             int64_t max_q, int32_t causal, int32_t window, float scale,
+                             void *out, int64_t out_stride, float *lse, hipStream_t stream);
+
+/*
+ * Attention of new tokens over a paged cache that already holds them (mlora_qk_rope first):
+ * sequence b owns query rows [cu_q[b], cu_q[b+1]) and kv_len[b] cached tokens, token j in page
+ * page_table[b][j / page_size].  Semantics as mlora_attention with L = kv_len[b]; decode is one
+ * query row a sequence, and decode rows and prefill chunks may share a call.
+ *   page_table int32 [n_seqs][table_stride] device; kv_len int32 [n_seqs] device, read as at
+ *       most table_stride * page_size and max_kv
+ *   max_q, max_kv  host upper bounds of the query counts and of kv_len (they size the launch;
+ *       sequences with more queries than max_q are left unanswered)
+ *   ws  mlora_paged_workspace_size() bytes for the same sizes
+ * A page number outside the cache is read as its nearest valid page (no fault; such sequences'
+ * results are meaningless): mlora_validate_pages checks a batch's tables on the host.
+ */
+size_t mlora_paged_workspace_size(int64_t T, int32_t n_seqs, int32_t n_q_heads,
+                                  int32_t n_kv_heads, int32_t head_dim, int64_t max_q,
+                                  int64_t max_kv);
+mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads,
+                                   const mlora_cache *cache, const int32_t *page_table,
+                                   int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
+                                   const int32_t *kv_len, int64_t max_q, int64_t max_kv,
+                                   int32_t causal, int32_t window, float scale, void *out,
+                                   int64_t out_stride, float *lse, void *ws, size_t ws_bytes,
+                                   hipStream_t stream);
+
+/*
+ * Host check of a paged batch before its arrays are copied to the GPU (all pointers host):
+ * cu_q ascending from 0 to T, 0 <= kv_len[b] <= min(table_stride * page_size, max_kv), query
+ * counts at most max_q, and every page that a sequence's kv_len reaches in [0, n_pages).
+ * MLORA_ERR_SHAPE for the lengths, MLORA_ERR_INDEX for a page; the offending value in *bad_value
+ * (may be NULL).
+ */
+mlora_status mlora_validate_pages(const mlora_cache *cache, const int32_t *page_table,
+                                  int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
+                                  const int32_t *kv_len, int64_t T, int64_t max_q,
+                                  int64_t max_kv, int64_t *bad_value);
+
+/*
  * Profiling hook (not part of the computation).  mlora_trace_start creates 2*capacity HIP
  * events (no device memory); from then on every mlora_linear call records one event on its
  * stream right before and one right after each launch of its main product kernel (the decode
  * GEMM or the tiled GEMM), every mlora_shrink / mlora_expand call around its one kernel, and
- * every mlora_plan call around its kernels (one duration for the one or three), for the first
- * `capacity` launches.
+ * every mlora_plan call around its kernels (one duration for the one or three), and the calls
+ * of the attention step around theirs (one duration a call), for the first `capacity`
+ * launches.
  * mlora_trace_stop waits for the recorded events, writes the duration of launch i in
  * milliseconds to ms[i] (host array of `capacity` floats; NULL discards them), releases the
  * events and returns the number of durations written (-1 on a HIP error).

@@ -1,6 +1,6 @@
 """Build libmlora.so in-tree with hipcc for gfx950 (CDNA4).
 
-Every .hip file and api.cpp is compiled to an object in parallel, then linked into
+Every .hip and .cpp file of csrc/ is compiled to an object in parallel, then linked into
 lora_serving_amd/libmlora.so.  All device code is built with the packed-FP32 feature switched
 off (the host pass warns that it does not know the feature; that is harmless).
 """
@@ -26,7 +26,8 @@ FLAGS = [f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + [os.path.join(CSRC, "api.cpp")]
+    return (sorted(glob.glob(os.path.join(CSRC, "*.hip"))) +
+            sorted(glob.glob(os.path.join(CSRC, "*.cpp"))))
 
 
 def _compile(src: str) -> str:

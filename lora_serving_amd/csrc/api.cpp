@@ -13,6 +13,7 @@
 #include <mutex>
 #include <vector>
 
+#include "abi.h"
 #include "kernels.h"
 
 using namespace mlora;
@@ -21,8 +22,6 @@ namespace {
 
 constexpr int64_t DECODE_MAX_T = 512;         // tokens per decode launch (8 chunks of 64)
 constexpr int64_t PREFILL_MAX_T = 4096 * 256; // token chunk of the tiled kernels
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
 
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
@@ -113,15 +112,6 @@ Layout make_layout(int64_t T, int32_t K, int64_t n_in, int64_t n_out, int32_t S,
 
 thread_local char g_last_error[256] = "";
 
-mlora_status hip_status(hipError_t e, const char *where = "launch")
-{
-    if (e == hipSuccess)
-        return MLORA_OK;
-    std::snprintf(g_last_error, sizeof g_last_error, "%s: %s (%d)", where, hipGetErrorString(e),
-                  (int)e);
-    return MLORA_ERR_HIP;
-}
-
 // Profiling hook: event pairs around the main product kernel of each mlora_linear call.
 struct Trace {
     std::mutex mu;
@@ -145,6 +135,15 @@ void trace_release()
 }  // namespace
 
 namespace mlora {
+
+mlora_status hip_status(hipError_t e, const char *where)
+{
+    if (e == hipSuccess)
+        return MLORA_OK;
+    std::snprintf(g_last_error, sizeof g_last_error, "%s: %s (%d)", where, hipGetErrorString(e),
+                  (int)e);
+    return MLORA_ERR_HIP;
+}
 
 void trace_mark(hipStream_t stream, bool begin)
 {

@@ -1,0 +1,67 @@
+// Device-side helpers shared by the attention kernels.
+//
+// Both kernels compute transposed scores S^T = K Q^T and transposed outputs O^T = V^T P^T, so a
+// query is a column: it stays in one lane (and the lanes that share its column), its running
+// maximum is a per-lane value, and the accumulator of S^T is the B operand of the second
+// product without moving a value across lanes.  The second product may take its keys in any
+// order as long as both operands agree, so its k index is simply numbered the way the first
+// product's accumulator holds the keys, and V^T is read from LDS in that order with transposing
+// reads (ds_read_b64_tr_b16: 16 lanes read 4 keys x 16 values and get 4 keys of one value each).
+#pragma once
+
+#include "common.h"
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+namespace mlora {
+
+constexpr float ATTN_LOG2E = 1.4426950408889634f;
+// Start of the running maximum: finite, so that a masked score (-inf) minus it is -inf, never NaN.
+constexpr float ATTN_LOWEST = -3.0e38f;
+// The running maximum follows a new one only past this many powers of two: below it the
+// probabilities (at most 2^6) and their fp32 sums lose nothing, and the accumulators are not
+// rescaled for every small rise.
+constexpr float ATTN_SLACK = 6.f;
+
+// two floats as packed bf16, rounded to nearest even (one v_cvt_pk_bf16_f32)
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi)
+{
+    const f32x2 v = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// 4 x 16 values of 16 bits, transposed over 16 lanes (see above); p: this lane's 8 bytes
+__device__ __forceinline__ u32x2 lds_read_tr(const uint16_t *p)
+{
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p));
+}
+
+__device__ __forceinline__ bf16x8 as_bf16x8(u32x4 v) { return __builtin_bit_cast(bf16x8, v); }
+
+// 8 e4m3 codes as bf16, exactly (e4m3's 4 significant bits fit bf16's 8)
+__device__ __forceinline__ u32x4 e4m3_to_bf16x8(uint32_t a, uint32_t b)
+{
+    u32x4 r;
+    r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, false));
+    r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.f, true));
+    r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, false));
+    r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.f, true));
+    return r;
+}
+
+// Bits of `acc` at 0x80008000 get set where a bf16 of w is infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite(uint32_t acc, uint32_t w)
+{
+    return acc | ((w & 0x7f807f80u) + 0x00800080u);
+}
+
+__device__ __forceinline__ int clamp_page(int page, int n_pages)
+{
+    return min(max(page, 0), n_pages - 1);
+}
+
+}  // namespace mlora

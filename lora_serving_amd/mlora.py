@@ -33,12 +33,22 @@ MLORA_PATH_TILED = 4
 MLORA_W_PACKED = 8
 MLORA_PATH_GROUPED = 16
 MLORA_NOALLOC_SCRATCH_BYTES = 64 << 20
+MLORA_CACHE_BF16 = 0
+MLORA_CACHE_E4M3 = 1
+MLORA_MAX_PAGE = 256
+MLORA_MAX_HEADS = 1024
+MLORA_ROPE_PLAIN = 0
+MLORA_ROPE_LINEAR = 1
+MLORA_ROPE_PARTS = 2
 
 EXPORTS = ("mlora_status_string", "mlora_last_error", "mlora_factor", "mlora_slot_bytes",
            "mlora_workspace_size", "mlora_slot_load", "mlora_packed_weight_bytes",
            "mlora_pack_weight",
            "mlora_validate", "mlora_plan", "mlora_shrink", "mlora_expand", "mlora_linear",
-           "mlora_linear_path", "mlora_linear_noalloc", "mlora_trace_start", "mlora_trace_stop")
+           "mlora_linear_path", "mlora_linear_noalloc", "mlora_rope_turns", "mlora_cache_bytes",
+           "mlora_qk_rope", "mlora_cache_read", "mlora_attention", "mlora_paged_workspace_size",
+           "mlora_paged_attention", "mlora_validate_pages", "mlora_trace_start",
+           "mlora_trace_stop")
 
 _P = ctypes.c_void_p
 _i64 = ctypes.c_int64
@@ -51,7 +61,20 @@ class mlora_slots(ctypes.Structure):
                 ("rank", _P)]
 
 
+class mlora_cache(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("n_pages", _i32),
+                ("n_kv_heads", _i32), ("page_size", _i32), ("head_dim", _i32), ("dtype", _i32)]
+
+
+class mlora_rope(ctypes.Structure):
+    _fields_ = [("turns", _P), ("rot_dim", _i32), ("interleaved", _i32),
+                ("magnitude", ctypes.c_float)]
+
+
 _SLOTS_P = ctypes.POINTER(mlora_slots)
+_CACHE_P = ctypes.POINTER(mlora_cache)
+_ROPE_P = ctypes.POINTER(mlora_rope)
+_f32 = ctypes.c_float
 
 _lib.mlora_status_string.restype = ctypes.c_char_p
 _lib.mlora_status_string.argtypes = [ctypes.c_int]
@@ -87,6 +110,28 @@ _lib.mlora_linear_path.argtypes = [_i64, _i64, _i64, _SLOTS_P, _i32, ctypes.c_ui
 _lib.mlora_linear_noalloc.restype = ctypes.c_int
 _lib.mlora_linear_noalloc.argtypes = [_P, _P, _i64, _i64, _i64, _SLOTS_P, _P, _i32, _P, _P,
                                       ctypes.c_uint32, _P]
+_lib.mlora_rope_turns.restype = ctypes.c_int
+_lib.mlora_rope_turns.argtypes = [_i32, ctypes.c_double, _i32, ctypes.c_double, _i64,
+                                  ctypes.c_double, ctypes.c_double, _P]
+_lib.mlora_cache_bytes.restype = _i64
+_lib.mlora_cache_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32]
+_lib.mlora_qk_rope.restype = ctypes.c_int
+_lib.mlora_qk_rope.argtypes = [_P, _i64, _i64, _i32, _i32, _i32, _P, _ROPE_P, _P, _P, _f32, _P,
+                               _i64, _P, _i64, _CACHE_P, _P, _P]
+_lib.mlora_cache_read.restype = ctypes.c_int
+_lib.mlora_cache_read.argtypes = [_CACHE_P, _P, _i64, _P, _P, _P]
+_lib.mlora_attention.restype = ctypes.c_int
+_lib.mlora_attention.argtypes = [_P, _i64, _P, _i64, _P, _i64, _i64, _i64, _i32, _P, _P, _i32,
+                                 _i32, _i32, _i64, _i32, _i32, _f32, _P, _i64, _P, _P]
+_lib.mlora_paged_workspace_size.restype = ctypes.c_size_t
+_lib.mlora_paged_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _i32, _i64, _i64]
+_lib.mlora_paged_attention.restype = ctypes.c_int
+_lib.mlora_paged_attention.argtypes = [_P, _i64, _i64, _i32, _CACHE_P, _P, _i64, _i32, _P, _P,
+                                       _i64, _i64, _i32, _i32, _f32, _P, _i64, _P, _P,
+                                       ctypes.c_size_t, _P]
+_lib.mlora_validate_pages.restype = ctypes.c_int
+_lib.mlora_validate_pages.argtypes = [_CACHE_P, _P, _i64, _i32, _P, _P, _i64, _i64, _i64,
+                                      ctypes.POINTER(_i64)]
 _lib.mlora_trace_start.restype = ctypes.c_int
 _lib.mlora_trace_start.argtypes = [_i32]
 _lib.mlora_trace_stop.restype = _i32
@@ -326,6 +371,210 @@ def mlora_linear_noalloc(x, W, slots: Slots | None, idx, scale, y, flags: int = 
                                      None if slots is None else slots.ref, _ptr(idx), K,
                                      _ptr(scale), _ptr(y), flags, _stream(stream)),
            "mlora_linear_noalloc")
+
+
+# ---- the attention step after a merged QKV layer ---------------------------------------------
+class Cache:
+    """A paged cache: k, v bf16 or float8_e4m3fn [n_pages][n_kv_heads][page_size][head_dim]
+    device tensors; e4m3 caches also take k_scale, v_scale fp32 [n_pages][n_kv_heads][page_size]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        import torch
+        kinds = (torch.bfloat16, torch.float8_e4m3fn)
+        self.k, self.v = _need(k, kinds, "k"), _need(v, kinds, "v")
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("k and v must have one 4-dimensional shape and one dtype")
+        e4m3 = k.dtype == torch.float8_e4m3fn
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if e4m3:
+                _need(t, (torch.float32,), name)
+                if t.shape != k.shape[:3]:
+                    raise ValueError(f"{name} must have shape {tuple(k.shape[:3])}")
+            elif t is not None:
+                raise ValueError(f"{name} belongs to e4m3 caches only")
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.n_pages, self.n_kv_heads, self.page_size, self.head_dim = (int(n) for n in k.shape)
+        self.struct = mlora_cache(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), self.n_pages,
+                                  self.n_kv_heads, self.page_size, self.head_dim,
+                                  MLORA_CACHE_E4M3 if e4m3 else MLORA_CACHE_BF16)
+        self.ref = ctypes.byref(self.struct)
+
+
+class Rope:
+    """Rotation by position: turns int64 [rot_dim / 2] device tensor (mlora_rope_turns)."""
+
+    def __init__(self, turns, rot_dim: int, interleaved: bool = False, magnitude: float = 1.0):
+        import torch
+        self.turns = None if rot_dim == 0 else _need(turns, (torch.int64,), "turns")
+        self.rot_dim = int(rot_dim)
+        if self.turns is not None and self.turns.numel() != self.rot_dim // 2:
+            raise ValueError("turns must hold rot_dim / 2 values")
+        self.struct = mlora_rope(_ptr(self.turns), self.rot_dim, int(bool(interleaved)),
+                                 float(magnitude))
+        self.ref = ctypes.byref(self.struct)
+
+
+def mlora_rope_turns(rot_dim: int, base: float = 10000.0, scaling: int = MLORA_ROPE_PLAIN,
+                     factor: float = 1.0, orig_len: int = 0, fast: float = 32.0,
+                     slow: float = 1.0):
+    """int64 host tensor [rot_dim / 2] of the pairs' turns per position (2^64 = one turn)."""
+    import torch
+    turns = torch.empty(max(int(rot_dim), 0) // 2, dtype=torch.int64)
+    _check(_lib.mlora_rope_turns(int(rot_dim), float(base), int(scaling), float(factor),
+                                 int(orig_len), float(fast), float(slow), _ptr(turns)),
+           "mlora_rope_turns")
+    return turns
+
+
+def mlora_cache_bytes(n_pages: int, n_kv_heads: int, page_size: int, head_dim: int,
+                      dtype: int = MLORA_CACHE_BF16) -> int:
+    return int(_lib.mlora_cache_bytes(n_pages, n_kv_heads, page_size, head_dim, dtype))
+
+
+def _rows(t, name, shape=None):
+    """Row stride of a bf16 [T][heads][head_dim] device tensor whose rows may lie apart."""
+    import torch
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be bf16 [T][heads][head_dim]")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    n, h, d = t.shape
+    st = t.stride()
+    if n > 0 and (st[2] != 1 or (h > 1 and st[1] != d)):
+        raise ValueError(f"the heads of a row of {name} must be contiguous")
+    return st[0] if n > 1 else h * d
+
+
+def _ints(t, n, name):
+    import torch
+    _need(t, (torch.int32,), name)
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} values, expected {n}")
+    return t.data_ptr()
+
+
+def _lse(lse, T, heads):
+    import torch
+    if lse is None:
+        return None
+    _need(lse, (torch.float32,), "lse")
+    if lse.shape != (T, heads):
+        raise ValueError(f"lse must have shape {(T, heads)}")
+    return lse.data_ptr()
+
+
+def mlora_qk_rope(qkv, n_q_heads: int, n_kv_heads: int, head_dim: int, pos, rope: Rope, q_out,
+                  k_out=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                  cache: Cache | None = None, slot=None, stream=None):
+    """qkv bf16 [T][(n_q_heads + 2 n_kv_heads) * head_dim]; q_out, k_out bf16
+    [T][heads][head_dim], also views of qkv's own query and key parts."""
+    import torch
+    if qkv.dtype != torch.bfloat16 or not qkv.is_cuda or qkv.dim() != 2:
+        raise ValueError("qkv must be a bf16 [T][width] device tensor")
+    T = qkv.shape[0]
+    width = (n_q_heads + 2 * n_kv_heads) * head_dim
+    if qkv.shape[1] != width or (T > 0 and qkv.stride(1) != 1):
+        raise ValueError(f"rows of qkv must hold {width} contiguous values")
+    q_stride = _rows(q_out, "q_out", (T, n_q_heads, head_dim))
+    k_stride = 0 if k_out is None else _rows(k_out, "k_out", (T, n_kv_heads, head_dim))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and _bf16(w, name).numel() != head_dim:
+            raise ValueError(f"{name} must hold head_dim values")
+    _check(_lib.mlora_qk_rope(qkv.data_ptr(), T, qkv.stride(0) if T > 1 else width, n_q_heads,
+                              n_kv_heads, head_dim, _ints(pos, T, "pos"), rope.ref,
+                              _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), q_stride,
+                              _ptr(k_out), k_stride, None if cache is None else cache.ref,
+                              None if slot is None else _ints(slot, T, "slot"),
+                              _stream(stream)), "mlora_qk_rope")
+
+
+def mlora_cache_read(cache: Cache, slot, k, v, stream=None):
+    """Tokens slot[0..T) of the cache into k, v bf16 [T][n_kv_heads][head_dim] (either None)."""
+    import torch
+    T = slot.numel()
+    for t, name in ((k, "k"), (v, "v")):
+        if t is not None:
+            _need(t, (torch.bfloat16,), name)
+            if t.shape != (T, cache.n_kv_heads, cache.head_dim):
+                raise ValueError(f"{name} must have shape "
+                                 f"{(T, cache.n_kv_heads, cache.head_dim)}")
+    _check(_lib.mlora_cache_read(cache.ref, _ints(slot, T, "slot"), T, _ptr(k), _ptr(v),
+                                 _stream(stream)), "mlora_cache_read")
+
+
+def mlora_attention(q, k, v, cu_q, out, cu_k=None, max_q: int | None = None, causal: bool = True,
+                    window: int = 0, scale: float = 0.0, lse=None, stream=None):
+    """q, out bf16 [T_q][n_q_heads][head_dim], k, v bf16 [T_k][n_kv_heads][head_dim], rows of any
+    stride (views of a merged row); cu_q, cu_k int32 [n_seqs + 1] device.  max_q: the longest
+    sequence's queries (None: T_q)."""
+    T, hq, d = q.shape
+    hkv = k.shape[1]
+    n = cu_q.numel() - 1
+    _check(_lib.mlora_attention(q.data_ptr(), _rows(q, "q"), k.data_ptr(),
+                                _rows(k, "k", (k.shape[0], hkv, d)), v.data_ptr(),
+                                _rows(v, "v", k.shape), T, k.shape[0], n,
+                                _ints(cu_q, n + 1, "cu_q"),
+                                None if cu_k is None else _ints(cu_k, n + 1, "cu_k"), hq, hkv, d,
+                                T if max_q is None else max_q, int(causal), window, scale,
+                                out.data_ptr(), _rows(out, "out", q.shape), _lse(lse, T, hq),
+                                _stream(stream)), "mlora_attention")
+
+
+def mlora_paged_workspace_size(T: int, n_seqs: int, n_q_heads: int, n_kv_heads: int,
+                               head_dim: int, max_q: int, max_kv: int) -> int:
+    return int(_lib.mlora_paged_workspace_size(T, n_seqs, n_q_heads, n_kv_heads, head_dim, max_q,
+                                               max_kv))
+
+
+def paged_workspace(T: int, n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                    max_q: int, max_kv: int, device="cuda"):
+    """A workspace of mlora_paged_workspace_size() bytes."""
+    import torch
+    n = mlora_paged_workspace_size(T, n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_kv)
+    if n == 0:
+        raise MloraError(MLORA_ERR_ARG, "mlora_paged_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mlora_paged_attention(q, cache: Cache, page_table, cu_q, kv_len, out, max_q: int,
+                          max_kv: int, causal: bool = True, window: int = 0, scale: float = 0.0,
+                          lse=None, ws=None, stream=None):
+    """q, out bf16 [T][n_q_heads][head_dim] (rows of any stride); page_table int32
+    [n_seqs][pages], cu_q int32 [n_seqs + 1], kv_len int32 [n_seqs], device."""
+    T, hq, d = q.shape
+    n = kv_len.numel()
+    if page_table.dim() != 2 or page_table.shape[0] != n:
+        raise ValueError("page_table must be [n_seqs][pages]")
+    if d != cache.head_dim:
+        raise ValueError("q and the cache must have one head_dim")
+    _check(_lib.mlora_paged_attention(q.data_ptr(), _rows(q, "q"), T, hq, cache.ref,
+                                      _ints(page_table, page_table.numel(), "page_table"),
+                                      page_table.shape[1], n, _ints(cu_q, n + 1, "cu_q"),
+                                      _ints(kv_len, n, "kv_len"), max_q, max_kv, int(causal),
+                                      window, scale, out.data_ptr(), _rows(out, "out", q.shape),
+                                      _lse(lse, T, hq), None if ws is None else ws.data_ptr(),
+                                      0 if ws is None else ws.numel() * ws.element_size(),
+                                      _stream(stream)), "mlora_paged_attention")
+
+
+def mlora_validate_pages(cache: Cache, page_table, cu_q, kv_len, T: int, max_q: int,
+                         max_kv: int):
+    """Host check of a paged batch (host int32 tensors or arrays); returns (status, offending
+    value)."""
+    import numpy as np
+    table = np.ascontiguousarray(page_table, dtype=np.int32)
+    cu = np.ascontiguousarray(cu_q, dtype=np.int32)
+    lens = np.ascontiguousarray(kv_len, dtype=np.int32)
+    if table.ndim != 2 or table.shape[0] != lens.size or cu.size != lens.size + 1:
+        raise ValueError("page_table [n_seqs][pages], cu_q [n_seqs + 1] and kv_len [n_seqs] "
+                         "do not agree")
+    bad = _i64(0)
+    code = _lib.mlora_validate_pages(cache.ref, table.ctypes.data_as(_P), table.shape[1],
+                                     lens.size, cu.ctypes.data_as(_P), lens.ctypes.data_as(_P),
+                                     T, max_q, max_kv, ctypes.byref(bad))
+    return code, int(bad.value)
 
 
 def mlora_trace_start(capacity: int):
