@@ -12,7 +12,9 @@ using namespace mlora;
 
 namespace {
 
-constexpr int64_t MAX_ROWS = INT64_C(1) << 31;   // query rows x heads, key rows: 32-bit row numbers
+constexpr int64_t MAX_ROWS = INT64_C(1) << 31;   // query rows x heads: 32-bit row numbers
+constexpr int64_t MAX_KEYS = INT64_C(1) << 30;   // tokens: positions and windows add up within 32 bits
+constexpr int64_t MAX_STRIDE = INT64_C(1) << 26; // K and V rows: 16 of them within a 32-bit byte offset
 
 bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
 
@@ -63,6 +65,10 @@ mlora_status check_cache(const mlora_cache *c, CacheGeom *g)
 }
 
 bool rows_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
+
+// A window that no sequence is longer than hides nothing (and is left out, so that positions minus the window
+// stay within 32 bits).
+int32_t seen_window(int32_t window, int64_t max_keys) { return window >= max_keys ? 0 : window; }
 
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
@@ -242,7 +248,8 @@ mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int
                              int64_t max_q, int32_t causal, int32_t window, float scale, void *out,
                              int64_t out_stride, float *lse, hipStream_t stream)
 {
-    if (T_q < 0 || T_k < 0 || n_seqs < 0 || max_q < 0 || window < 0 || std::isnan(scale))
+    if (T_q < 0 || T_k < 0 || n_seqs < 0 || max_q < 0 || window < 0 || !(scale >= 0.f) ||
+        std::isinf(scale))
         return MLORA_ERR_ARG;
     const mlora_status st = check_heads(n_q_heads, n_kv_heads, head_dim);
     if (st != MLORA_OK)
@@ -251,7 +258,8 @@ mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int
     if (!rows_ok(q_stride, qw) || !rows_ok(out_stride, qw) || !rows_ok(k_stride, kw) || !rows_ok(v_stride, kw) ||
         (cu_k == nullptr && T_k != T_q))
         return MLORA_ERR_SHAPE;
-    if (T_q * n_q_heads >= MAX_ROWS || T_q >= MAX_ROWS || T_k >= MAX_ROWS)
+    if (T_q >= MAX_KEYS || T_k >= MAX_KEYS || T_q * n_q_heads >= MAX_ROWS || k_stride >= MAX_STRIDE ||
+        v_stride >= MAX_STRIDE)
         return MLORA_ERR_UNSUPPORTED;
     if (T_q == 0 || n_seqs == 0 || max_q == 0)
         return MLORA_OK;
@@ -276,7 +284,7 @@ mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int
     a.cu_k = cu_k;
     a.max_q = std::min(max_q, T_q);
     a.causal = causal;
-    a.window = window;
+    a.window = seen_window(window, T_k);
     a.scale = scale == 0.f ? (float)(1.0 / std::sqrt((double)head_dim)) : scale;
     a.out = (uint16_t *)out;
     a.lse = lse;
@@ -304,7 +312,8 @@ mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, i
                                    int64_t max_kv, int32_t causal, int32_t window, float scale, void *out,
                                    int64_t out_stride, float *lse, void *ws, size_t ws_bytes, hipStream_t stream)
 {
-    if (T < 0 || n_seqs < 0 || max_q < 0 || max_kv < 0 || table_stride < 0 || window < 0 || std::isnan(scale))
+    if (T < 0 || n_seqs < 0 || max_q < 0 || max_kv < 0 || table_stride < 0 || window < 0 || !(scale >= 0.f) ||
+        std::isinf(scale))
         return MLORA_ERR_ARG;
     AttnArgs a{};
     mlora_status st = check_cache(cache, &a.cache);
@@ -316,7 +325,7 @@ mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, i
         return st;
     if (!rows_ok(q_stride, (int64_t)n_q_heads * d) || !rows_ok(out_stride, (int64_t)n_q_heads * d))
         return MLORA_ERR_SHAPE;
-    if (T >= MAX_ROWS || T * n_q_heads >= MAX_ROWS || max_kv >= (INT64_C(1) << 30) ||
+    if (T >= MAX_KEYS || T * n_q_heads >= MAX_ROWS || max_kv >= MAX_KEYS ||
         (int64_t)n_seqs * cache->n_kv_heads >= MAX_ROWS || table_stride >= MAX_ROWS)
         return MLORA_ERR_UNSUPPORTED;
     if (T == 0 || n_seqs == 0 || max_q == 0)
@@ -346,7 +355,7 @@ mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, i
     a.max_q = max_q;
     a.max_kv = max_kv;
     a.causal = causal;
-    a.window = window;
+    a.window = seen_window(window, max_kv);
     a.scale = scale == 0.f ? (float)(1.0 / std::sqrt((double)d)) : scale;
     a.out = (uint16_t *)out;
     a.lse = lse;

@@ -59,6 +59,9 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t acc, uint32_t w)
     return acc | ((w & 0x7f807f80u) + 0x00800080u);
 }
 
+// a value that is the same in all lanes, as a scalar
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 __device__ __forceinline__ int clamp_page(int page, int n_pages)
 {
     return min(max(page, 0), n_pages - 1);

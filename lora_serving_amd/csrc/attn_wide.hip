@@ -9,6 +9,7 @@
 // tile.  e4m3 tiles are converted to bf16 (exactly) on their way into LDS, their scales applied to
 // the scores and the probabilities.  Bound by the matrix cores together with the exponentials.
 #include <algorithm>
+#include <type_traits>
 
 #include "attention.h"
 #include "attention_device.h"
@@ -18,10 +19,85 @@ namespace mlora {
 constexpr int AW_BN = 64;      // keys a tile
 enum { AW_ROWS = 0, AW_PAGES = 1, AW_PAGES_E4M3 = 2 };
 
-// One 16-byte copy per lane from global memory straight into LDS (64 lanes: 1 KB at lds).
-__device__ __forceinline__ void aw_dma(const void *g, uint16_t *lds)
+// One 16-byte copy a lane from global memory (a scalar base and a byte offset of the lane) straight into
+// LDS: 64 lanes fill 1 KB at lds.  In asm, so that the compiler does not drain the copies in flight
+// before each LDS read (it cannot tell the buffers apart); every copy is waited for by hand.
+__device__ __forceinline__ void aw_dma(const void *base, uint32_t off, uint16_t *lds)
 {
-    __builtin_amdgcn_global_load_lds(g, (void __attribute__((address_space(3))) *)lds, 16, 0, 0);
+    const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds;
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(uniform((int)to)) : "memory");    // (nothing else here uses m0)
+}
+
+// Swizzle of the 16-byte pieces of a row by its key, a bijection for reads of one piece over 16 keys
+// (K, ds_read_b128) that also spreads a transposing read's 4 keys x 64 bytes (V) over all banks.
+template <int D>
+__device__ __forceinline__ int aw_swz(int key)
+{
+    return D == 128 ? ((key & 3) << 2) | ((key >> 2) & 3) : (((key >> 1) & 1) << 2) | ((key >> 2) & 3);
+}
+
+// The sequence and row block of an item: the longest row blocks (the last ones of a causal prompt) first, of
+// all sequences up to 64 of them (they start first, so that the launch ends on short ones: 8 prompts of 2048
+// tokens), in each sequence where there are more (short prompts, or one chunk among many single tokens).
+template <int BM>
+__device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, int *seq, int *block)
+{
+    auto blocks = [&](int s) {
+        if (s >= a.n_seqs)
+            return 0;
+        const int64_t lo = min((int64_t)max(a.cu_q[s], 0), a.T), hi = min((int64_t)max(a.cu_q[s + 1], 0), a.T);
+        const int64_t rows = (hi - lo) * a.group;
+        const bool mine = hi > lo && hi - lo <= a.max_q && rows >= a.min_rows && rows <= a.max_rows;
+        return mine ? (int)((rows + BM - 1) / BM) : 0;
+    };
+    if (a.n_seqs <= 64) {
+        const int nb = blocks(lane);
+        int most = nb;
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1)
+            most = max(most, __shfl_xor(most, off, 64));
+        // items of block numbers >= r
+        auto count = [&](int r) {
+            int c = max(nb - r, 0);
+#pragma unroll
+            for (int off = 32; off >= 1; off >>= 1)
+                c += __shfl_xor(c, off, 64);
+            return uniform(c);
+        };
+        if (item >= count(0))
+            return false;
+        int lo = 0, hi = uniform(most);                  // count(lo) > item >= count(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (count(mid) > item)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int nth = item - count(hi);       // among the sequences of more than lo blocks
+        const uint64_t have = ballot64(nb > lo);
+        const int rank = __popcll(have & ((UINT64_C(1) << lane) - 1));
+        const uint64_t hit = ballot64(nb > lo && rank == nth);
+        *seq = uniform(__ffsll((unsigned long long)hit) - 1);
+        *block = uniform(lo);
+        return true;
+    }
+    for (int s0 = 0, base = 0; s0 < a.n_seqs; s0 += 64) {
+        const int nb = blocks(s0 + lane);
+        int total;
+        const int ex = wave_exclusive_scan(nb, &total);
+        total = uniform(total);
+        if (item < base + total) {
+            const uint64_t hit = ballot64(item >= base + ex && item < base + ex + nb);
+            const int src = __ffsll((unsigned long long)hit) - 1;
+            *seq = uniform(s0 + src);
+            *block = uniform(__shfl(nb, src, 64) - 1 - (item - base - __shfl(ex, src, 64)));
+            return true;
+        }
+        base += total;
+    }
+    return false;
 }
 
 template <int D, int NW, int SRC>
@@ -36,50 +112,28 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_wide_kernel(AttnArgs a)
     constexpr int RPI = 64 / LPR;           // rows a copy instruction
     constexpr int IPW = BN / RPI / NW > 0 ? BN / RPI / NW : 1;  // copies a wave, for K and for V each
     constexpr int COPIERS = BN / RPI / IPW; // waves that copy
-    __shared__ __attribute__((aligned(1024))) uint16_t kl[2][BN * D];
-    __shared__ __attribute__((aligned(1024))) uint16_t vl[2][BN * D];
+    constexpr int TILE = BN * D;
+    __shared__ __attribute__((aligned(4 * TILE))) uint16_t kl[2 * TILE];
+    __shared__ __attribute__((aligned(4 * TILE))) uint16_t vl[2 * TILE];
     __shared__ __attribute__((aligned(16))) float sc[FP8 ? 2 : 1][2][FP8 ? BN : 4];
 
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wave = uniform(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, col = lane & 31, hh = lane >> 5;
     const int item = (int)(blockIdx.x / a.hkv), h = (int)(blockIdx.x - (unsigned)item * a.hkv);
 
     // the item's sequence and row block
-    int b = -1, rb = 0;
-    for (int s0 = 0, base = 0; s0 < a.n_seqs; s0 += 64) {
-        const int s = s0 + lane;
-        int nb = 0;
-        if (s < a.n_seqs) {
-            const int64_t lo = min((int64_t)max(a.cu_q[s], 0), a.T), hi = min((int64_t)max(a.cu_q[s + 1], 0), a.T);
-            const int64_t rows = (hi - lo) * a.group;
-            if (hi > lo && hi - lo <= a.max_q && rows >= a.min_rows && rows <= a.max_rows)
-                nb = (int)((rows + BM - 1) / BM);
-        }
-        int total;
-        const int ex = wave_exclusive_scan(nb, &total);
-        if (item < base + total) {
-            const uint64_t hit = ballot64(item >= base + ex && item < base + ex + nb);
-            const int src = __ffsll((unsigned long long)hit) - 1;
-            b = s0 + src;
-            rb = __shfl(nb, src, 64) - 1 - (item - base - __shfl(ex, src, 64));   // the longest rows first
-            break;
-        }
-        base += total;
-    }
-    if (b < 0)
+    int b, rb;
+    if (!aw_item<BM>(a, item, lane, &b, &rb))
         return;
-    b = __builtin_amdgcn_readfirstlane(b);
-    rb = __builtin_amdgcn_readfirstlane(rb);
-    const int q0 = (int)min((int64_t)max(a.cu_q[b], 0), a.T);
-    const int n = (int)min((int64_t)max(a.cu_q[b + 1], 0), a.T) - q0;
-    int L;
-    int64_t key0 = 0;
+    const int q0 = uniform((int)min((int64_t)max(a.cu_q[b], 0), a.T));
+    const int n = uniform((int)min((int64_t)max(a.cu_q[b + 1], 0), a.T)) - q0;
+    int L, key0 = 0;
     if (SRC == AW_ROWS) {
         const int32_t *cu = a.cu_k ? a.cu_k : a.cu_q;
-        key0 = min((int64_t)max(cu[b], 0), a.Tk);
-        L = (int)max(min((int64_t)max(cu[b + 1], 0), a.Tk) - key0, (int64_t)0);
+        key0 = uniform((int)min((int64_t)max(cu[b], 0), a.Tk));
+        L = max(uniform((int)min((int64_t)max(cu[b + 1], 0), a.Tk)) - key0, 0);
     } else {
-        L = (int)min((int64_t)max(a.kv_len[b], 0), min(a.max_kv, a.table_stride << a.cache.ps));
+        L = uniform((int)min((int64_t)max(a.kv_len[b], 0), min(a.max_kv, a.table_stride << a.cache.ps)));
     }
     const int rows = n * a.group;
 
@@ -96,9 +150,10 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_wide_kernel(AttnArgs a)
         return;
     const int wrow = rb * BM + wave * 32;
     const int wmin = first_key(wrow), wmax = wrow < rows ? end_key(wrow + 31) : 0;
-    // keys from wfull on, and before wfree, are seen by some of the wave's rows only
-    const int wfull = end_key(wrow), wfree = first_key(wrow + 31);
     const int t0 = kmin / BN, t1 = kmax > kmin ? (kmax + BN - 1) / BN : t0;
+    // tiles [f0, f1): every row of the workgroup sees every key
+    const int f0 = max(t0, (first_key(rb * BM + BM - 1) + BN - 1) / BN);
+    const int f1 = max(min(t1, min(kmax, end_key(rb * BM)) / BN), f0);
 
     u32x4 qf[KS];
     {
@@ -120,221 +175,324 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_wide_kernel(AttnArgs a)
     const int crow = lane / LPR, cpiece = lane % LPR;
     const int32_t *__restrict__ table = SRC == AW_ROWS ? nullptr : a.table + (int64_t)b * a.table_stride;
     const int ps = a.cache.ps, pm = (1 << ps) - 1;
-    int pg[IPW];
+    int pgk[IPW], pgv[IPW];
     u32x4 kr[IPW], vr[IPW];
     float scr = 0.f;
-    // pages of the tile's rows that this wave copies (a copy's rows lie in one page)
+    // pages of the rows of tile t that this wave copies (a copy's rows lie in one page)
     auto lookup = [&](int t) {
         if (SRC == AW_ROWS)
             return;
 #pragma unroll
         for (int i = 0; i < IPW; ++i)
-            pg[i] = clamp_page(table[min(t * BN + (wave * IPW + i) * RPI, L - 1) >> ps], a.cache.n_pages);
+            pgk[i] = clamp_page(table[min(t * BN + (wave * IPW + i) * RPI, L - 1) >> ps], a.cache.n_pages);
     };
-    auto stage = [&](int t, int buf) {
-        if (wave >= COPIERS)
+    // (one scalar base and a 32-bit offset a lane: row strides are below 2^26 elements)
+    auto copy = [&](int t, const uint16_t *rowbase, int64_t stride, const uint8_t *pages, const int *pg, uint16_t *lds, u32x4 *regs) {
+        if (COPIERS < NW && wave >= COPIERS)
             return;
 #pragma unroll
         for (int i = 0; i < IPW; ++i) {
-            const int r0 = (wave * IPW + i) * RPI, r = r0 + crow;
-            const int key = min(t * BN + r, L - 1);     // rows past the end: the last key again
+            const int r0 = (wave * IPW + i) * RPI;
+            const int key = min(t * BN + r0, L - 1);
+            const uint32_t cr = (uint32_t)min(crow, L - 1 - key);    // rows past the end: the last key again
+            const uint32_t piece = 16 * (cpiece ^ aw_swz<D>(r0 + crow));
             if (SRC == AW_ROWS) {
-                const int64_t at = key0 + key;
-                const int piece = 8 * (cpiece ^ (r & (CPR - 1)));
-                aw_dma(a.k + at * a.k_stride + (int64_t)h * D + piece, kl[buf] + r0 * D);
-                aw_dma(a.v + at * a.v_stride + (int64_t)h * D + piece, vl[buf] + r0 * D);
+                const uint16_t *base = rowbase + ((int64_t)key0 + key) * stride + (int64_t)h * D;
+                aw_dma(base, cr * (uint32_t)(2 * stride) + piece, lds + r0 * D);
             } else {
-                const int64_t at = (((int64_t)pg[i] * a.cache.hkv + h) << ps) + (key & pm);
-                if (!FP8) {
-                    const int piece = 16 * (cpiece ^ (r & (CPR - 1)));
-                    aw_dma(a.cache.k + at * D * 2 + piece, kl[buf] + r0 * D);
-                    aw_dma(a.cache.v + at * D * 2 + piece, vl[buf] + r0 * D);
-                } else {
-                    kr[i] = *(const u32x4 *)(a.cache.k + at * D + 16 * cpiece);
-                    vr[i] = *(const u32x4 *)(a.cache.v + at * D + 16 * cpiece);
-                }
+                const int64_t at = (((int64_t)uniform(pg[i]) * a.cache.hkv + h) << ps) + (key & pm);
+                if (!FP8)
+                    aw_dma(pages + at * D * 2, cr * (uint32_t)(2 * D) + piece, lds + r0 * D);
+                else
+                    regs[i] = *(const u32x4 *)(pages + at * D + (cr * (uint32_t)D + 16 * cpiece));
             }
         }
-        if (FP8 && threadIdx.x < 2 * BN) {
-            const int key = min(t * BN + (int)(threadIdx.x & (BN - 1)), L - 1);
+    };
+    // K of tile t + 1 and V of tile t on their way (pgk: the pages of tile t + 1, pgv: of tile t)
+    auto issue = [&](int t) {
+        const int nb = (t + 1) & 1;
+        if (t + 1 < t1)
+            copy(t + 1, a.k, a.k_stride, a.cache.k, pgk, kl + nb * TILE, kr);
+        if (t >= t0)
+            copy(t, a.v, a.v_stride, a.cache.v, pgv, vl + (nb ^ 1) * TILE, vr);
+        if (FP8 && threadIdx.x < 2 * BN) {      // scales of K and of V, both of tile t + 1
+            const int key = min((t + 1) * BN + (int)(threadIdx.x & (BN - 1)), L - 1);
             const int page = clamp_page(table[key >> ps], a.cache.n_pages);
-            const float *src = threadIdx.x < BN ? a.cache.k_scale : a.cache.v_scale;
-            scr = src[(((int64_t)page * a.cache.hkv + h) << ps) + (key & pm)];
+            scr = (threadIdx.x < BN ? a.cache.k_scale : a.cache.v_scale)[(((int64_t)page * a.cache.hkv + h) << ps) + (key & pm)];
         }
-    };
-    // e4m3: the loaded tile into LDS
-    auto deposit = [&](int buf) {
-        if (!FP8)
-            return;
-        if (wave < COPIERS)
+        if (SRC != AW_ROWS) {
 #pragma unroll
-            for (int i = 0; i < IPW; ++i) {
-                const int r = (wave * IPW + i) * RPI + crow;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int piece = 8 * ((2 * cpiece + e) ^ (r & (CPR - 1)));
-                    *(u32x4 *)(kl[buf] + r * D + piece) = e4m3_to_bf16x8(kr[i][2 * e], kr[i][2 * e + 1]);
-                    *(u32x4 *)(vl[buf] + r * D + piece) = e4m3_to_bf16x8(vr[i][2 * e], vr[i][2 * e + 1]);
-                }
-            }
-        if (threadIdx.x < 2 * BN)
-            sc[FP8 ? buf : 0][threadIdx.x / BN][FP8 ? threadIdx.x & (BN - 1) : 0] = scr;
-    };
-
-    if (t0 < t1) {
-        lookup(t0);
-        stage(t0, 0);
-        deposit(0);
-        if (t0 + 1 < t1)
-            lookup(t0 + 1);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1, kb = t * BN;
-        if (t + 1 < t1) {
-            stage(t + 1, buf ^ 1);
+            for (int i = 0; i < IPW; ++i)
+                pgv[i] = pgk[i];
             if (t + 2 < t1)
                 lookup(t + 2);
         }
-        if (kb < wmax && kb + BN > wmin) {
-            const uint16_t *kt = kl[buf], *vt = vl[buf];
-            const bool edge = kb + BN > wfull || kb < wfree;
-            // S^T: rows = keys 32 u + 8 (i / 4) + 4 hh + i % 4, column = query
-            f32x16 st[2];
+    };
+    // what issue(t) started has arrived in LDS (this wave's part; a barrier makes it the workgroup's)
+    auto land = [&](int t) {
+        if (FP8) {
+            const int nb = (t + 1) & 1;
+            if (wave < COPIERS)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+                for (int i = 0; i < IPW; ++i) {
+                    const int r = (wave * IPW + i) * RPI + crow;
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    st[u][i] = 0.f;
-#pragma unroll
-                for (int s = 0; s < KS; ++s) {
-                    const int key = 32 * u + col;
-                    const u32x4 kf = *(const u32x4 *)(kt + key * D + 8 * ((2 * s + hh) ^ (key & (CPR - 1))));
-                    st[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kf), as_bf16x8(qf[s]), st[u], 0, 0, 0);
+                    for (int e = 0; e < 2; ++e) {
+                        const int piece = 8 * ((2 * cpiece + e) ^ aw_swz<D>(r));
+                        if (t + 1 < t1)
+                            *(u32x4 *)(kl + nb * TILE + r * D + piece) = e4m3_to_bf16x8(kr[i][2 * e], kr[i][2 * e + 1]);
+                        if (t >= t0)
+                            *(u32x4 *)(vl + (nb ^ 1) * TILE + r * D + piece) = e4m3_to_bf16x8(vr[i][2 * e], vr[i][2 * e + 1]);
+                    }
                 }
-            }
-            if (FP8) {
+            if (threadIdx.x < 2 * BN)
+                sc[FP8 ? nb : 0][threadIdx.x / BN][FP8 ? threadIdx.x & (BN - 1) : 0] = scr;
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+    };
+    auto phase_end = [] {
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_barrier" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    // (opaque to the compiler, which would otherwise keep every address of both buffers in registers and spill)
+    auto tile_at = [](uint32_t at, int t) {
+        at ^= (t & 1) * TILE * 2;
+        asm volatile("" : "+v"(at));
+        return at;
+    };
+
+    f32x16 st[2], zero;
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+    for (int i = 0; i < 16; ++i)
+        zero[i] = 0.f;
+    u32x4 pf[4];
+    // S^T: rows = keys 32 u + 8 (i / 4) + 4 hh + i % 4, column = query
+    const uint32_t klane = col * D * 2 + 16 * (hh ^ aw_swz<D>(col));
+    auto kfrag = [&](uint32_t at, int s, int u) {
+        return *(const u32x4 *)((const uint8_t *)kl + (at ^ (32 * s)) + 64 * u * D);
+    };
+    auto scores = [&](int t) {
+        const uint32_t at = tile_at(klane, t);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const f32x4 k4 = *(const f32x4 *)(&sc[buf][0][32 * u + 8 * i + 4 * hh]);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            st[u][4 * i + e] *= k4[e];
-                    }
-            }
-            if (edge) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int key = kb + 32 * u + 8 * (i / 4) + 4 * hh + i % 4;
-                        const bool see = key < L && (!a.causal || key <= pos) &&
-                                         (a.window <= 0 || key > pos - a.window);
-                        st[u][i] = see ? st[u][i] : -INFINITY;
-                    }
-            }
-            float mx = st[0][0];
+        for (int s = 0; s < KS; ++s)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    mx = fmaxf(mx, st[u][i]);
-            mx *= cs;
-            if (__any(mx > m + ATTN_SLACK)) {
-                mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-                // (each column on its own: a row's bits do not depend on its neighbours)
-                const float mn = mx > m + ATTN_SLACK ? mx : m, f = __builtin_amdgcn_exp2f(m - mn);
-                m = mn;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DB; ++d)
-                    o[d] *= f;
-            }
-            // P^T: rounding to bf16 (2^-9 relative) for the matrix cores; the sum keeps fp32
-            u32x4 pf[4];
+                st[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kfrag(at, s, u)), as_bf16x8(qf[s]),
+                                                                s ? st[u] : zero, 0, 0, 0);
+    };
+    // scores to probabilities, P^T rounded to bf16 (half a step: 2^-8 relative) for the matrix cores; the sum keeps fp32
+    auto softmax = [&](int t, auto edge) {
+        const int buf = t & 1;
+        if (FP8)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    f32x4 p, v4;
-                    if (FP8)
-                        v4 = *(const f32x4 *)(&sc[FP8 ? buf : 0][1][FP8 ? 32 * u + 8 * i + 4 * hh : 0]);
+                    const f32x4 k4 = *(const f32x4 *)(&sc[FP8 ? buf : 0][0][FP8 ? 32 * u + 8 * i + 4 * hh : 0]);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float s = st[u][4 * i + e];
-                        const float x = __builtin_amdgcn_exp2f(fmaf(s, cs, -m));
-                        l += x;
-                        // (a masked key's scale may be anything)
-                        p[e] = !FP8 ? x : edge && s == -INFINITY ? 0.f : x * v4[e];
-                    }
-                    pf[2 * u + i / 2][2 * (i & 1)] = cvt_bf16x2(p[0], p[1]);
-                    pf[2 * u + i / 2][2 * (i & 1) + 1] = cvt_bf16x2(p[2], p[3]);
+                    for (int e = 0; e < 4; ++e)
+                        st[u][4 * i + e] *= k4[e];
                 }
-            // O^T += V^T P^T; k index (hh, e) of step s is key 16 s + 8 (e / 4) + 4 hh + e % 4
-            const int vi = lane & 15, vd = (lane >> 4) & 1;
-            auto vfrag = [&](int s, int d) {
-                u32x4 f;
+        if (edge)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int key = 16 * s + 8 * u + 4 * hh + (vi >> 2);
-                    const int piece = 4 * d + 2 * vd + ((vi & 3) >> 1);
-                    const u32x2 w = lds_read_tr(vt + key * D + 8 * (piece ^ (key & (CPR - 1))) + 4 * (vi & 1));
-                    f[2 * u] = w[0];
-                    f[2 * u + 1] = w[1];
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = t * BN + 32 * u + 8 * (i / 4) + 4 * hh + i % 4;
+                    const bool see = key < L && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
+                    st[u][i] = see ? st[u][i] : -INFINITY;
                 }
-                return f;
-            };
-            uint32_t bad = 0;
-            if (edge) {
+        float mx = st[0][0];
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                    for (int d = 0; d < DB; ++d) {
-                        const u32x4 f = vfrag(s, d);
+            for (int i = 0; i < 16; ++i)
+                mx = fmaxf(mx, st[u][i]);
+        mx *= cs;
+        if (__any(mx > m + ATTN_SLACK)) {
+            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+            // (each column on its own: a row's bits do not depend on its neighbours)
+            const float mn = mx > m + ATTN_SLACK ? mx : m, f = __builtin_amdgcn_exp2f(m - mn);
+            m = mn;
+            l *= f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            bad = not_finite(bad, f[i]);
-                    }
-            }
-            if (!__any((bad & 0x80008000u) != 0)) {
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll
-                    for (int d = 0; d < DB; ++d)
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(s, d)), as_bf16x8(pf[s]), o[d], 0, 0, 0);
-            } else {
-                // V holds an infinity or NaN where some row must not see it (0 x NaN is NaN): one key at
-                // a time, kept only by the rows that see it
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll 1
-                    for (int k = 0; k < 16; ++k) {
-                        const int key = kb + 16 * s + k, e = 4 * (k >> 3) + (k & 3);
-                        const bool mine = hh == ((k >> 2) & 1);
-                        const bool see = key < L && (!a.causal || key <= pos) &&
-                                         (a.window <= 0 || key > pos - a.window);
-                        const uint32_t half = (e & 1) ? 0xffff0000u : 0xffffu;
-#pragma unroll
-                        for (int d = 0; d < DB; ++d) {
-                            u32x4 f = vfrag(s, d);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                f[i] = mine && i == (e >> 1) ? f[i] & half : 0u;
-                            const f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(pf[s]), o[d], 0, 0, 0);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[d][i] = see ? x[i] : o[d][i];
-                        }
-                    }
-            }
+            for (int d = 0; d < DB; ++d)
+                o[d] *= f;
         }
-        if (t + 1 < t1)
-            deposit(buf ^ 1);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                f32x4 p, v4;
+                if (FP8)
+                    v4 = *(const f32x4 *)(&sc[FP8 ? buf : 0][1][FP8 ? 32 * u + 8 * i + 4 * hh : 0]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float s = st[u][4 * i + e];
+                    const float x = __builtin_amdgcn_exp2f(fmaf(s, cs, -m));
+                    l += x;
+                    // (a masked key's scale may be anything)
+                    p[e] = !FP8 ? x : edge && s == -INFINITY ? 0.f : x * v4[e];
+                }
+                pf[2 * u + i / 2][2 * (i & 1)] = cvt_bf16x2(p[0], p[1]);
+                pf[2 * u + i / 2][2 * (i & 1) + 1] = cvt_bf16x2(p[2], p[3]);
+            }
+    };
+    // O^T += V^T P^T; k index (hh, e) of step s is key 16 s + 8 (e / 4) + 4 hh + e % 4
+    const int vi = lane & 15, vd = (lane >> 4) & 1, vk = 4 * hh + (vi >> 2);
+    const uint32_t vlane = vk * D * 2 + 16 * ((2 * vd + ((vi & 3) >> 1)) ^ aw_swz<D>(vk)) + 8 * (vi & 1);
+    auto vfrag = [&](uint32_t at, int s, int d) {
+        u32x4 f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {       // keys 16 s + 8 u + vk, values 32 d ..
+            const u32x2 w = lds_read_tr((const uint16_t *)((const uint8_t *)vl + (at ^ (64 * d + 32 * u)) + (16 * u + 32 * s) * D));
+            f[2 * u] = w[0];
+            f[2 * u + 1] = w[1];
+        }
+        return f;
+    };
+    auto outputs = [&](int t) {
+        const uint32_t at = tile_at(vlane, t);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d)), as_bf16x8(pf[s]), o[d], 0, 0, 0);
+    };
+    // scores(t + 1) and outputs(t) in steps of two products, the fragments read AHEAD steps before their use; the
+    // fences keep the compiler to that order
+    auto products = [&](int t) {
+        constexpr int N = KS + 2 * DB, AHEAD = 4;
+        const uint32_t ka = tile_at(klane, t + 1), va = tile_at(vlane, t);
+        u32x4 f[AHEAD][2];
+        auto read = [&](int i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                f[i % AHEAD][e] = i < KS ? kfrag(ka, i, e) : vfrag(va, 2 * (i - KS) / DB, 2 * (i - KS) % DB + e);
+        };
+#pragma unroll
+        for (int i = 0; i < AHEAD; ++i)
+            read(i);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const bf16x8 x = as_bf16x8(f[i % AHEAD][e]);
+                const int d = (2 * (i - KS) % DB + e) & (DB - 1), s = 2 * (i - KS) / DB;
+                if (i < KS)
+                    st[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(qf[i < KS ? i : 0]), i ? st[e] : zero, 0, 0, 0);
+                else
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(pf[i < KS ? 0 : s]), o[d], 0, 0, 0);
+            }
+            if (i + AHEAD < N)
+                read(i + AHEAD);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // the same for a tile that some rows see in part: V may hold an infinity or NaN where a row must not see it
+    // (0 x NaN is NaN); then one key at a time, kept only by the rows that see it
+    auto outputs_edge = [&](int t) {
+        const uint32_t at = tile_at(vlane, t);
+        uint32_t bad = 0;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                const u32x4 f = vfrag(at, s, d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    bad = not_finite(bad, f[i]);
+            }
+        if (!__any((bad & 0x80008000u) != 0)) {
+            outputs(t);
+            return;
+        }
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+                const int key = t * BN + 16 * s + k, e = 4 * (k >> 3) + (k & 3);
+                const bool mine = hh == ((k >> 2) & 1);
+                const bool see = key < L && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
+                const uint32_t half = (e & 1) ? 0xffff0000u : 0xffffu;
+#pragma unroll
+                for (int d = 0; d < DB; ++d) {
+                    u32x4 f = vfrag(at, s, d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        f[i] = mine && i == (e >> 1) ? f[i] & half : 0u;
+                    const f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(pf[s]), o[d], 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        o[d][i] = see ? x[i] : o[d][i];
+                }
+            }
+    };
+    // a tile on its own (K of it in place before; afterwards K of the next)
+    auto single = [&](int t) {
+        const bool work = t * BN < wmax && t * BN + BN > wmin;
+        issue(t);
+        if (work) {
+            scores(t);
+            softmax(t, std::true_type());
+        }
+        land(t);
+        phase_end();
+        if (work)
+            outputs_edge(t);
+    };
+
+    if (t0 < t1) {
+        lookup(t0);
+        issue(t0 - 1);
+        land(t0 - 1);
+    }
+    phase_end();
+    // On the tiles that all rows see in full the waves 4.. run half a tile behind the first four, so that on each
+    // SIMD one wave's products meet the other's exponentials: M(t) = scores(t), outputs(t - 1) against softmax(t).
+    const bool late = NW > 4 && wave >= 4;
+    for (int t = t0; t < t1;) {
+        if (t != f0 || f0 >= f1) {
+            single(t);
+            ++t;
+            continue;
+        }
+        if (late) {
+            issue(t);
+            phase_end();
+        } else {
+            issue(t);
+        }
+        scores(t);
+        auto between = [&] {                // from scores(t) to what it brings
+            if (late)
+                land(t);
+            phase_end();
+            if (late && t + 1 < f1)
+                issue(t + 1);
+            softmax(t, std::false_type());
+            if (!late)
+                land(t);
+            phase_end();
+        };
+        for (; t + 1 < f1; ++t) {
+            between();
+            if (!late)
+                issue(t + 1);
+            __builtin_amdgcn_s_setprio(1);
+            products(t);
+            __builtin_amdgcn_s_setprio(0);
+        }
+        between();
+        outputs(t);
+        if (!late)
+            phase_end();
+        ++t;
     }
 
     l += __shfl_xor(l, 32, 64);
