@@ -56,8 +56,7 @@ struct AttnArgs {
 };
 // Whole prompts (cache unused) or, with pages, chunks of new tokens.
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream);
-// Rows (queries x heads of a group) of one workgroup for these sizes: 128 or 256.
-int wide_rows(int64_t T, int32_t hq, int32_t group);
+constexpr int WIDE_ROWS = 128;    // rows (queries x heads of a group) of one workgroup
 hipError_t launch_attn_wide_combine(const AttnArgs &a, int head_dim, hipStream_t stream);
 // Sequences of up to 16 * nq rows (nq 1 or 2) over pages.
 hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, hipStream_t stream);

@@ -112,7 +112,7 @@ PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t
         }
     }
     if (p.wide) {
-        const int64_t bm = wide_rows(T, hq, (int32_t)group), items = (T * group + bm - 1) / bm * hkv;
+        const int64_t items = (T * group + WIDE_ROWS - 1) / WIDE_ROWS * hkv;
         if (items >= 192)
             p.wide_chunk = (max_kv + 127) & ~INT64_C(127), p.wide_chunks = 1;
         else

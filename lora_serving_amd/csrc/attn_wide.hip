@@ -40,7 +40,6 @@ __device__ __forceinline__ int aw_swz(int key)
 // The sequence and row block of an item: the longest row blocks (the last ones of a causal prompt) first, of
 // all sequences up to 64 of them (they start first, so that the launch ends on short ones: 8 prompts of 2048
 // tokens), in each sequence where there are more (short prompts, or one chunk among many single tokens).
-template <int BM>
 __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, int *seq, int *block)
 {
     auto blocks = [&](int s) {
@@ -49,7 +48,7 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, i
         const int64_t lo = min((int64_t)max(a.cu_q[s], 0), a.T), hi = min((int64_t)max(a.cu_q[s + 1], 0), a.T);
         const int64_t rows = (hi - lo) * a.group;
         const bool mine = hi > lo && hi - lo <= a.max_q && rows >= a.min_rows && rows <= a.max_rows;
-        return mine ? (int)((rows + BM - 1) / BM) : 0;
+        return mine ? (int)((rows + WIDE_ROWS - 1) / WIDE_ROWS) : 0;
     };
     if (a.n_seqs <= 64) {
         const int nb = blocks(lane);
@@ -100,11 +99,11 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, i
     return false;
 }
 
-template <int D, int NW, int SRC>
-__global__ __launch_bounds__(NW * 64, 2) void attn_wide_kernel(AttnArgs a)
+template <int D, int SRC>
+__global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
 {
     constexpr bool FP8 = SRC == AW_PAGES_E4M3;
-    constexpr int BM = NW * 32, BN = AW_BN;
+    constexpr int NW = 4, BM = WIDE_ROWS, BN = AW_BN;
     constexpr int KS = D / 16;              // k-steps of the first product
     constexpr int DB = D / 32;              // row blocks of the second
     constexpr int CPR = D / 8;              // 16-byte pieces of a bf16 row
@@ -123,7 +122,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_wide_kernel(AttnArgs a)
 
     // the item's sequence and row block
     int b, rb;
-    if (!aw_item<BM>(a, item, lane, &b, &rb))
+    if (!aw_item(a, item, lane, &b, &rb))
         return;
     const int q0 = uniform((int)min((int64_t)max(a.cu_q[b], 0), a.T));
     const int n = uniform((int)min((int64_t)max(a.cu_q[b + 1], 0), a.T)) - q0;
@@ -398,45 +397,69 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_wide_kernel(AttnArgs a)
     // (0 x NaN is NaN); then one key at a time, kept only by the rows that see it
     auto outputs_edge = [&](int t) {
         const uint32_t at = tile_at(vlane, t);
+        // keys of this lane's fragments (k index (hh, e) of step s) that hold an infinity or NaN: bit 8 s + e
         uint32_t bad = 0;
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+            u32x4 w = {0, 0, 0, 0};
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
                 const u32x4 f = vfrag(at, s, d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    bad = not_finite(bad, f[i]);
+                    w[i] = not_finite(w[i], f[i]);
             }
-        if (!__any((bad & 0x80008000u) != 0)) {
-            outputs(t);
-            return;
+            uint32_t b8 = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b8 |= ((w[i] >> 15) & 1u) << (2 * i) | (w[i] >> 31) << (2 * i + 1);
+            bad |= b8 << (8 * s);
         }
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll 1
-            for (int k = 0; k < 16; ++k) {
-                const int key = t * BN + 16 * s + k, e = 4 * (k >> 3) + (k & 3);
-                const bool mine = hh == ((k >> 2) & 1);
-                const bool see = key < L && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
-                const uint32_t half = (e & 1) ? 0xffff0000u : 0xffffu;
+        for (int off = 1; off < 32; off <<= 1)
+            bad |= __shfl_xor(bad, off, 64);
+        const uint64_t some = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)bad, 32) << 32) | (uint32_t)uniform((int)bad);
+        for (uint64_t rest = some; rest; rest &= rest - 1) {
+            const int bit = __ffsll((unsigned long long)rest) - 1, s = (bit & 31) >> 3, e = bit & 7;
+            const int key = t * BN + 16 * s + 8 * (e >> 2) + 4 * (bit >> 5) + (e & 3);
+            const bool see = key < L && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
+            const uint32_t half = hh != (bit >> 5) ? 0u : (e & 1) ? 0xffff0000u : 0xffffu;
+            u32x4 p;
 #pragma unroll
-                for (int d = 0; d < DB; ++d) {
-                    u32x4 f = vfrag(at, s, d);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        f[i] = mine && i == (e >> 1) ? f[i] & half : 0u;
-                    const f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(pf[s]), o[d], 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        o[d][i] = see ? x[i] : o[d][i];
-                }
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t a0 = pf[0][i], a1 = pf[1][i], a2 = pf[2][i], a3 = pf[3][i];
+                p[i] = (s & 2) ? ((s & 1) ? a3 : a2) : ((s & 1) ? a1 : a0);
             }
+#pragma unroll
+            for (int d = 0; d < DB; ++d) {
+                u32x4 f = vfrag(at, s, d);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[i] &= i == (e >> 1) ? half : 0u;
+                const f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(p), o[d], 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[d][i] = see ? x[i] : o[d][i];
+            }
+        }
+        // and the rest
+        const uint32_t mine = (uint32_t)(some >> (32 * hh));
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            u32x4 keep;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                keep[i] = ((mine >> (8 * s + 2 * i)) & 1 ? 0u : 0xffffu) | ((mine >> (8 * s + 2 * i + 1)) & 1 ? 0u : 0xffff0000u);
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d) & keep), as_bf16x8(pf[s]), o[d], 0, 0, 0);
+        }
     };
     // a tile on its own (K of it in place before; afterwards K of the next)
     auto single = [&](int t) {
         const bool work = t * BN < wmax && t * BN + BN > wmin;
-        issue(t);
+        if (t > t0)
+            issue(t);
         if (work) {
             scores(t);
             softmax(t, std::true_type());
@@ -450,68 +473,67 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_wide_kernel(AttnArgs a)
     if (t0 < t1) {
         lookup(t0);
         issue(t0 - 1);
-        land(t0 - 1);
+        if (FP8)
+            land(t0 - 1);
+        issue(t0);
+        if (!FP8)       // K of t0 has arrived when no more than the copies of V are in flight
+            asm volatile("s_waitcnt vmcnt(%0)" :: "i"(IPW) : "memory");
     }
     phase_end();
-    // On the tiles that all rows see in full the waves 4.. run half a tile behind the first four, so that on each
-    // SIMD one wave's products meet the other's exponentials: M(t) = scores(t), outputs(t - 1) against softmax(t).
-    const bool late = NW > 4 && wave >= 4;
-    for (int t = t0; t < t1;) {
-        if (t != f0 || f0 >= f1) {
-            single(t);
-            ++t;
-            continue;
-        }
-        if (late) {
+    int t = t0;
+    const int lead = f0 < f1 ? f0 : t1;
+    for (; t < lead; ++t)
+        single(t);
+    if (t < t1) {
+        // tiles that all rows see in full
+        if (t > t0)
             issue(t);
-            phase_end();
-        } else {
-            issue(t);
-        }
         scores(t);
-        auto between = [&] {                // from scores(t) to what it brings
-            if (late)
-                land(t);
-            phase_end();
-            if (late && t + 1 < f1)
-                issue(t + 1);
-            softmax(t, std::false_type());
-            if (!late)
-                land(t);
-            phase_end();
-        };
         for (; t + 1 < f1; ++t) {
-            between();
-            if (!late)
-                issue(t + 1);
+            softmax(t, std::false_type());
+            land(t);
+            phase_end();
+            issue(t + 1);
             __builtin_amdgcn_s_setprio(1);
             products(t);
             __builtin_amdgcn_s_setprio(0);
         }
-        between();
+        softmax(t, std::false_type());
+        land(t);
+        phase_end();
         outputs(t);
-        if (!late)
-            phase_end();
-        ++t;
+        for (++t; t < t1; ++t)
+            single(t);
     }
 
     l += __shfl_xor(l, 32, 64);
-    if (row >= rows)
-        return;
     if (a.n_chunks == 1) {
+        // through the wave's own part of LDS (the tiles are done with), so that whole rows are stored
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-        uint16_t *dst = a.out + (int64_t)(q0 + ri) * a.out_stride + (int64_t)hd * D + 4 * hh;
+        phase_end();
+        uint16_t *part = kl + wave * 32 * D;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                *(u32x2 *)(dst + 32 * d + 8 * i) =
+                *(u32x2 *)(part + col * D + 8 * ((4 * d + i) ^ (col & (CPR - 1))) + 4 * hh) =
                     u32x2{cvt_bf16x2(o[d][4 * i] * inv, o[d][4 * i + 1] * inv),
                           cvt_bf16x2(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
+        const int64_t to = (int64_t)(q0 + ri) * a.out_stride + (int64_t)hd * D;
+#pragma unroll
+        for (int j = 0; j < 32 * CPR / 64; ++j) {
+            const int r = j * (64 / CPR) + lane / CPR, piece = lane & (CPR - 1);
+            const u32x4 w = *(const u32x4 *)(part + r * D + 8 * (piece ^ (r & (CPR - 1))));
+            const int64_t at = (int64_t)((uint64_t)(uint32_t)__shfl((int)(to >> 32), r, 64) << 32 | (uint32_t)__shfl((int)to, r, 64));
+            if (wrow + r < rows)
+                *(u32x4 *)(a.out + at + 8 * piece) = w;
+        }
+        if (row >= rows)
+            return;
         if (a.lse && hh == 0)
             a.lse[(int64_t)(q0 + ri) * a.hq + hd] =
                 l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * (1.f / ATTN_LOG2E);
-    } else {
+    } else if (row < rows) {
         const int64_t slot = ((int64_t)(q0 + ri) * a.hq + hd) * a.n_chunks + blockIdx.y;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -576,26 +598,17 @@ __global__ __launch_bounds__(256) void attn_wide_combine_kernel(AttnArgs a)
         a.lse[th] = sum == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
 }
 
-int wide_rows(int64_t T, int32_t hq, int32_t group)
-{
-    (void)group;
-    return T * hq >= 256 * 256 ? 256 : 128;
-}
-
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream)
 {
-    const int bm = wide_rows(a.T, a.hq, a.group);
     // each sequence's last row block may be part empty: at most one more block a sequence
-    const int64_t items = std::min(a.T * a.group / bm + a.n_seqs,
-                                   a.n_seqs * ((a.max_q * a.group + bm - 1) / bm));
+    const int64_t items = std::min(a.T * a.group / WIDE_ROWS + a.n_seqs,
+                                   a.n_seqs * ((a.max_q * a.group + WIDE_ROWS - 1) / WIDE_ROWS));
     if (items * a.hkv > 0x7fffffff)
         return hipErrorInvalidValue;
     const dim3 grid((unsigned)(items * a.hkv), (unsigned)a.n_chunks);
-#define AW(D, NW, SRC) attn_wide_kernel<D, NW, SRC><<<grid, dim3(NW * 64), 0, stream>>>(a)
-#define AW_S(D, NW) (!pages ? AW(D, NW, AW_ROWS) : a.cache.fp8 ? AW(D, NW, AW_PAGES_E4M3) : AW(D, NW, AW_PAGES))
-#define AW_N(D) (bm == 256 ? AW_S(D, 8) : AW_S(D, 4))
-    head_dim == 64 ? AW_N(64) : AW_N(128);
-#undef AW_N
+#define AW(D, SRC) attn_wide_kernel<D, SRC><<<grid, dim3(256), 0, stream>>>(a)
+#define AW_S(D) (!pages ? AW(D, AW_ROWS) : a.cache.fp8 ? AW(D, AW_PAGES_E4M3) : AW(D, AW_PAGES))
+    head_dim == 64 ? AW_S(64) : AW_S(128);
 #undef AW_S
 #undef AW
     return hipGetLastError();
