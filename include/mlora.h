@@ -390,7 +390,7 @@ mlora_status mlora_cache_read(const mlora_cache *cache, const int32_t *slot, int
  *   cu_q, cu_k  int32 [n_seqs + 1] device, ascending from 0; entries beyond the T given are read
  *       as T.  max_q: an upper bound of the sequences' query counts (host; sizes the launch).
  *   scale  of the scores, finite and not negative; 0 means head_dim^(-1/2)
- * T_q and T_k are below 2^30, T_q * n_q_heads below 2^31, k_stride and v_stride below 2^26.
+ * T_q and T_k are below 2^30, T_q * n_q_heads below 2^31, k_stride and v_stride below 2^24.
  */
 mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                              const void *v, int64_t v_stride, int64_t T_q, int64_t T_k,

@@ -109,12 +109,11 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
     constexpr int CPR = D / 8;              // 16-byte pieces of a bf16 row
     constexpr int LPR = FP8 ? D / 16 : CPR; // lanes a row of the copy
     constexpr int RPI = 64 / LPR;           // rows a copy instruction
-    constexpr int IPW = BN / RPI / NW > 0 ? BN / RPI / NW : 1;  // copies a wave, for K and for V each
-    constexpr int COPIERS = BN / RPI / IPW; // waves that copy
+    constexpr int IPW = BN / RPI / NW;      // copies a wave, for K and for V each
     constexpr int TILE = BN * D;
     __shared__ __attribute__((aligned(4 * TILE))) uint16_t kl[2 * TILE];
     __shared__ __attribute__((aligned(4 * TILE))) uint16_t vl[2 * TILE];
-    __shared__ __attribute__((aligned(16))) float sc[FP8 ? 2 : 1][2][FP8 ? BN : 4];
+    __shared__ __attribute__((aligned(16))) float sc[FP8 ? 4 : 1][2][FP8 ? BN : 4];
 
     const int wave = uniform(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, col = lane & 31, hh = lane >> 5;
@@ -170,59 +169,68 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
             o[d][i] = 0.f;
     float m = ATTN_LOWEST, l = 0.f;
 
-    // copies of a tile: K and V rows [key][D], the 16-byte pieces of a row swizzled by the key
-    const int crow = lane / LPR, cpiece = lane % LPR;
+    // Copies of a tile: K and V rows [key][D], the 16-byte pieces of a row swizzled by the key.  A wave copies 16
+    // rows, which lie in one page, from a scalar base with constant 32-bit offsets.  Rows past the end of a sequence
+    // are the last key again, or in a page whatever it holds: they are masked.
+    const int w16 = 16 * wave, crow = lane / LPR, cpiece = lane % LPR;
     const int32_t *__restrict__ table = SRC == AW_ROWS ? nullptr : a.table + (int64_t)b * a.table_stride;
     const int ps = a.cache.ps, pm = (1 << ps) - 1;
-    int pgk[IPW], pgv[IPW];
+    uint32_t off_k[IPW], off_v[IPW], piece[IPW];
+#pragma unroll
+    for (int i = 0; i < IPW; ++i) {
+        const int r = RPI * i + crow;
+        piece[i] = 16 * (FP8 ? cpiece : cpiece ^ aw_swz<D>(r));
+        off_k[i] = piece[i] + (SRC == AW_ROWS ? (uint32_t)(w16 + r) * (uint32_t)(2 * a.k_stride) : (uint32_t)r * D * (FP8 ? 1 : 2));
+        off_v[i] = SRC == AW_ROWS ? piece[i] + (uint32_t)(w16 + r) * (uint32_t)(2 * a.v_stride) : off_k[i];
+    }
+    const uint16_t *kp = a.k + ((int64_t)key0 + (int64_t)t0 * BN) * a.k_stride + (int64_t)h * D;   // rows: the next tile
+    const uint16_t *vp = a.v + ((int64_t)key0 + (int64_t)t0 * BN) * a.v_stride + (int64_t)h * D;
+    int pgk = 0, pgv = 0;
     u32x4 kr[IPW], vr[IPW];
     float scr = 0.f;
-    // pages of the rows of tile t that this wave copies (a copy's rows lie in one page)
-    auto lookup = [&](int t) {
-        if (SRC == AW_ROWS)
-            return;
-#pragma unroll
-        for (int i = 0; i < IPW; ++i)
-            pgk[i] = clamp_page(table[min(t * BN + (wave * IPW + i) * RPI, L - 1) >> ps], a.cache.n_pages);
+    auto lookup = [&](int t) {      // the page of this wave's rows of tile t
+        if (SRC != AW_ROWS)
+            pgk = clamp_page(table[min(t * BN + w16, L - 1) >> ps], a.cache.n_pages);
     };
-    // (one scalar base and a 32-bit offset a lane: row strides are below 2^26 elements)
-    auto copy = [&](int t, const uint16_t *rowbase, int64_t stride, const uint8_t *pages, const int *pg, uint16_t *lds, u32x4 *regs) {
-        if (COPIERS < NW && wave >= COPIERS)
-            return;
+    auto copy = [&](int t, const uint16_t *&rows, int64_t stride, const uint8_t *pages, int pg, const uint32_t (&off)[IPW],
+                    uint16_t *lds, u32x4 (&regs)[IPW]) {
+        if (SRC == AW_ROWS) {
+            if (t * BN + BN <= L) {
 #pragma unroll
-        for (int i = 0; i < IPW; ++i) {
-            const int r0 = (wave * IPW + i) * RPI;
-            const int key = min(t * BN + r0, L - 1);
-            const uint32_t cr = (uint32_t)min(crow, L - 1 - key);    // rows past the end: the last key again
-            const uint32_t piece = 16 * (cpiece ^ aw_swz<D>(r0 + crow));
-            if (SRC == AW_ROWS) {
-                const uint16_t *base = rowbase + ((int64_t)key0 + key) * stride + (int64_t)h * D;
-                aw_dma(base, cr * (uint32_t)(2 * stride) + piece, lds + r0 * D);
+                for (int i = 0; i < IPW; ++i)
+                    aw_dma(rows, off[i], lds + (w16 + RPI * i) * D);
             } else {
-                const int64_t at = (((int64_t)uniform(pg[i]) * a.cache.hkv + h) << ps) + (key & pm);
-                if (!FP8)
-                    aw_dma(pages + at * D * 2, cr * (uint32_t)(2 * D) + piece, lds + r0 * D);
-                else
-                    regs[i] = *(const u32x4 *)(pages + at * D + (cr * (uint32_t)D + 16 * cpiece));
+#pragma unroll
+                for (int i = 0; i < IPW; ++i)
+                    aw_dma(rows, (uint32_t)min(w16 + RPI * i + crow, L - 1 - t * BN) * (uint32_t)(2 * stride) + piece[i],
+                           lds + (w16 + RPI * i) * D);
             }
+            rows += BN * stride;
+        } else {
+            const int64_t at = (((int64_t)uniform(pg) * a.cache.hkv + h) << ps) + ((t * BN + w16) & pm);
+            const uint8_t *base = pages + at * D * (FP8 ? 1 : 2);
+#pragma unroll
+            for (int i = 0; i < IPW; ++i)
+                if (!FP8)
+                    aw_dma(base, off[i], lds + (w16 + RPI * i) * D);
+                else
+                    regs[i] = *(const u32x4 *)(base + off[i]);
         }
     };
-    // K of tile t + 1 and V of tile t on their way (pgk: the pages of tile t + 1, pgv: of tile t)
+    // K of tile t + 1 and V of tile t on their way (pgk: the page of tile t + 1, pgv: of tile t)
     auto issue = [&](int t) {
         const int nb = (t + 1) & 1;
         if (t + 1 < t1)
-            copy(t + 1, a.k, a.k_stride, a.cache.k, pgk, kl + nb * TILE, kr);
+            copy(t + 1, kp, a.k_stride, a.cache.k, pgk, off_k, kl + nb * TILE, kr);
         if (t >= t0)
-            copy(t, a.v, a.v_stride, a.cache.v, pgv, vl + (nb ^ 1) * TILE, vr);
+            copy(t, vp, a.v_stride, a.cache.v, pgv, off_v, vl + (nb ^ 1) * TILE, vr);
         if (FP8 && threadIdx.x < 2 * BN) {      // scales of K and of V, both of tile t + 1
             const int key = min((t + 1) * BN + (int)(threadIdx.x & (BN - 1)), L - 1);
             const int page = clamp_page(table[key >> ps], a.cache.n_pages);
             scr = (threadIdx.x < BN ? a.cache.k_scale : a.cache.v_scale)[(((int64_t)page * a.cache.hkv + h) << ps) + (key & pm)];
         }
         if (SRC != AW_ROWS) {
-#pragma unroll
-            for (int i = 0; i < IPW; ++i)
-                pgv[i] = pgk[i];
+            pgv = pgk;
             if (t + 2 < t1)
                 lookup(t + 2);
         }
@@ -231,21 +239,20 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
     auto land = [&](int t) {
         if (FP8) {
             const int nb = (t + 1) & 1;
-            if (wave < COPIERS)
 #pragma unroll
-                for (int i = 0; i < IPW; ++i) {
-                    const int r = (wave * IPW + i) * RPI + crow;
+            for (int i = 0; i < IPW; ++i) {
+                const int r = w16 + RPI * i + crow;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int piece = 8 * ((2 * cpiece + e) ^ aw_swz<D>(r));
-                        if (t + 1 < t1)
-                            *(u32x4 *)(kl + nb * TILE + r * D + piece) = e4m3_to_bf16x8(kr[i][2 * e], kr[i][2 * e + 1]);
-                        if (t >= t0)
-                            *(u32x4 *)(vl + (nb ^ 1) * TILE + r * D + piece) = e4m3_to_bf16x8(vr[i][2 * e], vr[i][2 * e + 1]);
-                    }
+                for (int e = 0; e < 2; ++e) {
+                    const int p = 8 * ((2 * cpiece + e) ^ aw_swz<D>(r));
+                    if (t + 1 < t1)
+                        *(u32x4 *)(kl + nb * TILE + r * D + p) = e4m3_to_bf16x8(kr[i][2 * e], kr[i][2 * e + 1]);
+                    if (t >= t0)
+                        *(u32x4 *)(vl + (nb ^ 1) * TILE + r * D + p) = e4m3_to_bf16x8(vr[i][2 * e], vr[i][2 * e + 1]);
                 }
+            }
             if (threadIdx.x < 2 * BN)
-                sc[FP8 ? nb : 0][threadIdx.x / BN][FP8 ? threadIdx.x & (BN - 1) : 0] = scr;
+                sc[FP8 ? (t + 1) & 3 : 0][threadIdx.x / BN][FP8 ? threadIdx.x & (BN - 1) : 0] = scr;
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         } else {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -264,7 +271,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
         return at;
     };
 
-    f32x16 st[2], zero;
+    f32x16 sa[2], sb[2], zero;
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         zero[i] = 0.f;
@@ -274,7 +281,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
     auto kfrag = [&](uint32_t at, int s, int u) {
         return *(const u32x4 *)((const uint8_t *)kl + (at ^ (32 * s)) + 64 * u * D);
     };
-    auto scores = [&](int t) {
+    auto scores = [&](int t, f32x16 (&st)[2]) {
         const uint32_t at = tile_at(klane, t);
 #pragma unroll
         for (int s = 0; s < KS; ++s)
@@ -283,34 +290,35 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
                 st[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kfrag(at, s, u)), as_bf16x8(qf[s]),
                                                                 s ? st[u] : zero, 0, 0, 0);
     };
-    // scores to probabilities, P^T rounded to bf16 (half a step: 2^-8 relative) for the matrix cores; the sum keeps fp32
-    auto softmax = [&](int t, auto edge) {
-        const int buf = t & 1;
+    // e4m3: the keys' scales
+    auto scaled = [&](int t, int u, f32x16 (&st)[2]) {
         if (FP8)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 k4 = *(const f32x4 *)(&sc[FP8 ? t & 3 : 0][0][FP8 ? 32 * u + 8 * i + 4 * hh : 0]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f32x4 k4 = *(const f32x4 *)(&sc[FP8 ? buf : 0][0][FP8 ? 32 * u + 8 * i + 4 * hh : 0]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        st[u][4 * i + e] *= k4[e];
-                }
-        if (edge)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int key = t * BN + 32 * u + 8 * (i / 4) + 4 * hh + i % 4;
-                    const bool see = key < L && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
-                    st[u][i] = see ? st[u][i] : -INFINITY;
-                }
-        float mx = st[0][0];
+                for (int e = 0; e < 4; ++e)
+                    st[u][4 * i + e] *= k4[e];
+            }
+    };
+    auto hide = [&](int t, f32x16 (&st)[2]) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                mx = fmaxf(mx, st[u][i]);
+            for (int i = 0; i < 16; ++i) {
+                const int key = t * BN + 32 * u + 8 * (i / 4) + 4 * hh + i % 4;
+                const bool see = key < L && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
+                st[u][i] = see ? st[u][i] : -INFINITY;
+            }
+    };
+    auto largest = [&](const f32x16 &s, float mx) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            mx = fmaxf(mx, s[i]);
+        return mx;
+    };
+    // the running maximum follows the largest score of a tile, and what was summed before with it
+    auto raise = [&](float mx) {
         mx *= cs;
         if (__any(mx > m + ATTN_SLACK)) {
             mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
@@ -322,24 +330,24 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
             for (int d = 0; d < DB; ++d)
                 o[d] *= f;
         }
+    };
+    // 4 scores to probabilities (i: 0 .. 7), P^T rounded to bf16 (half a step: 2^-8 relative) for the matrix cores;
+    // the sum keeps fp32
+    auto powers = [&](int t, int i, const f32x16 (&st)[2], auto edge) {
+        const int u = i >> 2, j = i & 3;
+        f32x4 p, v4;
+        if (FP8)
+            v4 = *(const f32x4 *)(&sc[FP8 ? t & 3 : 0][1][FP8 ? 32 * u + 8 * j + 4 * hh : 0]);
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                f32x4 p, v4;
-                if (FP8)
-                    v4 = *(const f32x4 *)(&sc[FP8 ? buf : 0][1][FP8 ? 32 * u + 8 * i + 4 * hh : 0]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float s = st[u][4 * i + e];
-                    const float x = __builtin_amdgcn_exp2f(fmaf(s, cs, -m));
-                    l += x;
-                    // (a masked key's scale may be anything)
-                    p[e] = !FP8 ? x : edge && s == -INFINITY ? 0.f : x * v4[e];
-                }
-                pf[2 * u + i / 2][2 * (i & 1)] = cvt_bf16x2(p[0], p[1]);
-                pf[2 * u + i / 2][2 * (i & 1) + 1] = cvt_bf16x2(p[2], p[3]);
-            }
+        for (int e = 0; e < 4; ++e) {
+            const float s = st[u][4 * j + e];
+            const float x = __builtin_amdgcn_exp2f(fmaf(s, cs, -m));
+            l += x;
+            // (a masked key's scale may be anything)
+            p[e] = !FP8 ? x : edge && s == -INFINITY ? 0.f : x * v4[e];
+        }
+        pf[i >> 1][2 * (i & 1)] = cvt_bf16x2(p[0], p[1]);
+        pf[i >> 1][2 * (i & 1) + 1] = cvt_bf16x2(p[2], p[3]);
     };
     // O^T += V^T P^T; k index (hh, e) of step s is key 16 s + 8 (e / 4) + 4 hh + e % 4
     const int vi = lane & 15, vd = (lane >> 4) & 1, vk = 4 * hh + (vi >> 2);
@@ -362,10 +370,12 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
             for (int d = 0; d < DB; ++d)
                 o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d)), as_bf16x8(pf[s]), o[d], 0, 0, 0);
     };
-    // scores(t + 1) and outputs(t) in steps of two products, the fragments read AHEAD steps before their use; the
-    // fences keep the compiler to that order
-    auto products = [&](int t) {
+    // Scores of tile t + 1 (into nx), powers of tile t (from st) and its outputs, in steps of two products: the
+    // fragments are read AHEAD steps before their use, the powers of a step's keys come before it, and the next
+    // tile's largest score after its last; the fences keep the compiler to that order.
+    auto body = [&](int t, const f32x16 (&st)[2], f32x16 (&nx)[2]) {
         constexpr int N = KS + 2 * DB, AHEAD = 4;
+        issue(t + 1);
         const uint32_t ka = tile_at(klane, t + 1), va = tile_at(vlane, t);
         u32x4 f[AHEAD][2];
         auto read = [&](int i) {
@@ -377,6 +387,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
         for (int i = 0; i < AHEAD; ++i)
             read(i);
         __builtin_amdgcn_sched_barrier(0);
+        float mx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
 #pragma unroll
@@ -384,14 +395,32 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
                 const bf16x8 x = as_bf16x8(f[i % AHEAD][e]);
                 const int d = (2 * (i - KS) % DB + e) & (DB - 1), s = 2 * (i - KS) / DB;
                 if (i < KS)
-                    st[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(qf[i < KS ? i : 0]), i ? st[e] : zero, 0, 0, 0);
+                    nx[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(qf[i < KS ? i : 0]), i ? nx[e] : zero, 0, 0, 0);
                 else
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(pf[i < KS ? 0 : s]), o[d], 0, 0, 0);
             }
             if (i + AHEAD < N)
                 read(i + AHEAD);
+            // D = 128: powers 0 .. 3 in steps 1, 3, 5, 7, 4 .. 7 in 8 .. 11; D = 64: 0 .. 3, 4 .. 7 in 4, 4, 5, 5
+            if (D == 128 ? (i < 8 ? (i & 1) : i < 12) : i < 6) {
+                if (D == 128) {
+                    powers(t, i < 8 ? i >> 1 : i - 4, st, std::false_type());
+                } else if (i < 4) {
+                    powers(t, i, st, std::false_type());
+                } else {
+                    powers(t, 2 * i - 4, st, std::false_type());
+                    powers(t, 2 * i - 3, st, std::false_type());
+                }
+            }
+            if (i >= N - 2) {
+                scaled(t + 1, i - (N - 2), nx);
+                mx = largest(nx[i - (N - 2)], mx);
+            }
             __builtin_amdgcn_sched_barrier(0);
         }
+        raise(mx);
+        land(t + 1);
+        phase_end();
     };
     // the same for a tile that some rows see in part: V may hold an infinity or NaN where a row must not see it
     // (0 x NaN is NaN); then one key at a time, kept only by the rows that see it
@@ -461,8 +490,14 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
         if (t > t0)
             issue(t);
         if (work) {
-            scores(t);
-            softmax(t, std::true_type());
+            scores(t, sa);
+            scaled(t, 0, sa);
+            scaled(t, 1, sa);
+            hide(t, sa);
+            raise(largest(sa[1], largest(sa[0], -INFINITY)));
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                powers(t, i, sa, std::true_type());
         }
         land(t);
         phase_end();
@@ -488,19 +523,25 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
         // tiles that all rows see in full
         if (t > t0)
             issue(t);
-        scores(t);
-        for (; t + 1 < f1; ++t) {
-            softmax(t, std::false_type());
-            land(t);
-            phase_end();
-            issue(t + 1);
-            __builtin_amdgcn_s_setprio(1);
-            products(t);
-            __builtin_amdgcn_s_setprio(0);
-        }
-        softmax(t, std::false_type());
+        scores(t, sa);
+        scaled(t, 0, sa);
+        scaled(t, 1, sa);
+        raise(largest(sa[1], largest(sa[0], -INFINITY)));
         land(t);
         phase_end();
+        for (; t + 2 < f1; t += 2) {
+            body(t, sa, sb);
+            body(t + 1, sb, sa);
+        }
+        if (t + 1 < f1) {
+            body(t, sa, sb);
+            sa[0] = sb[0];
+            sa[1] = sb[1];
+            ++t;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            powers(t, i, sa, std::false_type());
         outputs(t);
         for (++t; t < t1; ++t)
             single(t);
