@@ -62,6 +62,18 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t acc, uint32_t w)
 // a value that is the same in all lanes, as a scalar
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// Sum over the 64 lanes of a wave, as a scalar (DPP: no trip through LDS).
+__device__ __forceinline__ int wave_total(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 15, 15, false);    // row_shr 1, 2, 4, 8
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 15, 15, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 15, 15, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 15, 15, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 10, 15, false);    // lane 15 of rows 0, 2 to rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 12, 15, false);    // lane 31 to rows 2, 3
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
 __device__ __forceinline__ int clamp_page(int page, int n_pages)
 {
     return min(max(page, 0), n_pages - 1);

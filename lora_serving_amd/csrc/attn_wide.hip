@@ -37,36 +37,48 @@ __device__ __forceinline__ int aw_swz(int key)
     return D == 128 ? ((key & 3) << 2) | ((key >> 2) & 3) : (((key >> 1) & 1) << 2) | ((key >> 2) & 3);
 }
 
+// A workgroup's work: row block `block` of a sequence's query rows [q0, q0 + n), its L keys (rows: from key0 on).
+struct WideItem {
+    int seq, block, q0, n, key0, L;
+};
+
 // The sequence and row block of an item: the longest row blocks (the last ones of a causal prompt) first, of
 // all sequences up to 64 of them (they start first, so that the launch ends on short ones: 8 prompts of 2048
 // tokens), in each sequence where there are more (short prompts, or one chunk among many single tokens).
-__device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, int *seq, int *block)
+template <bool ROWS>
+__device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, WideItem *w)
 {
-    auto blocks = [&](int s) {
-        if (s >= a.n_seqs)
-            return 0;
-        const int64_t lo = min((int64_t)max(a.cu_q[s], 0), a.T), hi = min((int64_t)max(a.cu_q[s + 1], 0), a.T);
-        const int64_t rows = (hi - lo) * a.group;
-        const bool mine = hi > lo && hi - lo <= a.max_q && rows >= a.min_rows && rows <= a.max_rows;
+    int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+    auto load = [&](int s) {
+        q0 = q1 = k0 = k1 = 0;
+        if (s < a.n_seqs) {
+            const int32_t *cu = ROWS && a.cu_k ? a.cu_k : a.cu_q;
+            const int32_t qa = a.cu_q[s], qb = a.cu_q[s + 1], ka = ROWS ? cu[s] : 0, kb = ROWS ? cu[s + 1] : a.kv_len[s];
+            q0 = (int)min((int64_t)max(qa, 0), a.T);
+            q1 = (int)min((int64_t)max(qb, 0), a.T);
+            k0 = (int)min((int64_t)max(ka, 0), a.Tk);
+            k1 = (int)min((int64_t)max(kb, 0), ROWS ? a.Tk : min(a.max_kv, a.table_stride << a.cache.ps));
+        }
+        const int64_t rows = (int64_t)(q1 - q0) * a.group;
+        const bool mine = q1 > q0 && q1 - q0 <= a.max_q && rows >= a.min_rows && rows <= a.max_rows;
         return mine ? (int)((rows + WIDE_ROWS - 1) / WIDE_ROWS) : 0;
     };
+    auto take = [&](int s0, int src, int block) {
+        w->seq = s0 + src;
+        w->block = block;
+        w->q0 = __builtin_amdgcn_readlane(q0, src);
+        w->n = __builtin_amdgcn_readlane(q1, src) - w->q0;
+        w->key0 = __builtin_amdgcn_readlane(k0, src);
+        w->L = max(__builtin_amdgcn_readlane(k1, src) - w->key0, 0);
+    };
     if (a.n_seqs <= 64) {
-        const int nb = blocks(lane);
-        int most = nb;
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1)
-            most = max(most, __shfl_xor(most, off, 64));
+        const int nb = load(lane);
         // items of block numbers >= r
-        auto count = [&](int r) {
-            int c = max(nb - r, 0);
-#pragma unroll
-            for (int off = 32; off >= 1; off >>= 1)
-                c += __shfl_xor(c, off, 64);
-            return uniform(c);
-        };
+        auto count = [&](int r) { return wave_total(max(nb - r, 0)); };
         if (item >= count(0))
             return false;
-        int lo = 0, hi = uniform(most);                  // count(lo) > item >= count(hi)
+        // count(lo) > item >= count(hi)
+        int lo = 0, hi = (int)((a.max_q * a.group + WIDE_ROWS - 1) / WIDE_ROWS);
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (count(mid) > item)
@@ -77,21 +89,18 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, i
         const int nth = item - count(hi);       // among the sequences of more than lo blocks
         const uint64_t have = ballot64(nb > lo);
         const int rank = __popcll(have & ((UINT64_C(1) << lane) - 1));
-        const uint64_t hit = ballot64(nb > lo && rank == nth);
-        *seq = uniform(__ffsll((unsigned long long)hit) - 1);
-        *block = uniform(lo);
+        take(0, uniform(__ffsll((unsigned long long)ballot64(nb > lo && rank == nth)) - 1), lo);
         return true;
     }
     for (int s0 = 0, base = 0; s0 < a.n_seqs; s0 += 64) {
-        const int nb = blocks(s0 + lane);
+        const int nb = load(s0 + lane);
         int total;
         const int ex = wave_exclusive_scan(nb, &total);
         total = uniform(total);
         if (item < base + total) {
             const uint64_t hit = ballot64(item >= base + ex && item < base + ex + nb);
-            const int src = __ffsll((unsigned long long)hit) - 1;
-            *seq = uniform(s0 + src);
-            *block = uniform(__shfl(nb, src, 64) - 1 - (item - base - __shfl(ex, src, 64)));
+            const int src = uniform(__ffsll((unsigned long long)hit) - 1);
+            take(s0, src, __builtin_amdgcn_readlane(nb, src) - 1 - (item - base - __builtin_amdgcn_readlane(ex, src)));
             return true;
         }
         base += total;
@@ -119,20 +128,10 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
     const int lane = threadIdx.x & 63, col = lane & 31, hh = lane >> 5;
     const int item = (int)(blockIdx.x / a.hkv), h = (int)(blockIdx.x - (unsigned)item * a.hkv);
 
-    // the item's sequence and row block
-    int b, rb;
-    if (!aw_item(a, item, lane, &b, &rb))
+    WideItem it;
+    if (!aw_item<SRC == AW_ROWS>(a, item, lane, &it))
         return;
-    const int q0 = uniform((int)min((int64_t)max(a.cu_q[b], 0), a.T));
-    const int n = uniform((int)min((int64_t)max(a.cu_q[b + 1], 0), a.T)) - q0;
-    int L, key0 = 0;
-    if (SRC == AW_ROWS) {
-        const int32_t *cu = a.cu_k ? a.cu_k : a.cu_q;
-        key0 = uniform((int)min((int64_t)max(cu[b], 0), a.Tk));
-        L = max(uniform((int)min((int64_t)max(cu[b + 1], 0), a.Tk)) - key0, 0);
-    } else {
-        L = uniform((int)min((int64_t)max(a.kv_len[b], 0), min(a.max_kv, a.table_stride << a.cache.ps)));
-    }
+    const int b = it.seq, rb = it.block, q0 = it.q0, n = it.n, L = it.L, key0 = it.key0;
     const int rows = n * a.group;
 
     // this lane's row, and the keys that the workgroup's and the wave's rows see
@@ -444,9 +443,10 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
                 b8 |= ((w[i] >> 15) & 1u) << (2 * i) | (w[i] >> 31) << (2 * i + 1);
             bad |= b8 << (8 * s);
         }
+        if (__any(bad != 0))
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1)
-            bad |= __shfl_xor(bad, off, 64);
+            for (int off = 1; off < 32; off <<= 1)
+                bad |= __shfl_xor(bad, off, 64);
         const uint64_t some = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)bad, 32) << 32) | (uint32_t)uniform((int)bad);
         for (uint64_t rest = some; rest; rest &= rest - 1) {
             const int bit = __ffsll((unsigned long long)rest) - 1, s = (bit & 31) >> 3, e = bit & 7;
