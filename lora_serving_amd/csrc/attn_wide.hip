@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
     // fragments are read AHEAD steps before their use, the powers of a step's keys come before it, and the next
     // tile's largest score after its last; the fences keep the compiler to that order.
     auto body = [&](int t, const f32x16 (&st)[2], f32x16 (&nx)[2]) {
-        constexpr int N = KS + 2 * DB, AHEAD = 4;
+        constexpr int N = KS + 2 * DB, AHEAD = FP8 ? 2 : 4;   // (e4m3: as the registers allow)
         issue(t + 1);
         const uint32_t ka = tile_at(klane, t + 1), va = tile_at(vlane, t);
         u32x4 f[AHEAD][2];
