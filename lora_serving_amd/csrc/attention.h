@@ -59,7 +59,7 @@ hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStre
 constexpr int WIDE_ROWS = 128;    // rows (queries x heads of a group) of one workgroup
 hipError_t launch_attn_wide_combine(const AttnArgs &a, int head_dim, hipStream_t stream);
 // Sequences of up to 16 * nq rows (nq 1 or 2) over pages.
-hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, hipStream_t stream);
+hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int waves, hipStream_t stream);
 hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, hipStream_t stream);
 
 }  // namespace mlora

@@ -14,6 +14,13 @@ namespace {
 
 constexpr int64_t MAX_ROWS = INT64_C(1) << 31;   // query rows x heads: 32-bit row numbers
 constexpr int64_t MAX_KEYS = INT64_C(1) << 30;   // tokens: positions and windows add up within 32 bits
+#ifndef AD_WANT
+#define AD_WANT 2048
+#endif
+#ifndef AD_KV
+#define AD_KV 2048
+#define AD_ITEMS 256
+#endif
 constexpr int64_t MAX_STRIDE = INT64_C(1) << 24; // K and V rows: 64 of them within a 32-bit byte offset
 
 bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
@@ -75,7 +82,7 @@ size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 // How a paged call is cut: which kernels run, and the chunks of keys that give each enough
 // workgroups.  Made from the sizes alone, so that the workspace can be sized before the call.
 struct PagedPlan {
-    int nq = 1;                          // column tiles of the decode kernel
+    int nq = 1, waves = 4;               // column tiles and waves of the decode kernel
     int64_t dec_rows = 0;                // sequences of up to this many rows go to it (0: none can)
     bool wide = false;                   // some sequence may have more
     int64_t dec_chunk = 0, dec_chunks = 0, wide_chunk = 0, wide_chunks = 0;
@@ -104,7 +111,14 @@ PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t
             p.dec_rows = 0;
     }
     if (p.dec_rows > 0) {
-        cut((int64_t)n_seqs * hkv, 2048, 128, &p.dec_chunk, &p.dec_chunks);
+        const int64_t items = (int64_t)n_seqs * hkv;
+        if (p.nq == 1 && items <= AD_ITEMS && max_kv <= AD_KV) {
+            p.waves = 8;
+            p.dec_chunk = (max_kv + 127) & ~INT64_C(127);
+            p.dec_chunks = 1;
+        } else {
+            cut(items, AD_WANT, 128, &p.dec_chunk, &p.dec_chunks);
+        }
         if (p.dec_chunks > 1) {
             const size_t slots = (size_t)n_seqs * hkv * p.dec_rows * p.dec_chunks;
             p.dec_o = align_up(slots * d * 4);
@@ -379,7 +393,7 @@ mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, i
         a.n_chunks = (int32_t)p.dec_chunks;
         a.part_o = (float *)base;
         a.part_ml = (float *)(base + p.dec_o);
-        e = launch_attn_decode(a, d, p.nq, stream);
+        e = launch_attn_decode(a, d, p.nq, p.waves, stream);
         if (e == hipSuccess && p.dec_chunks > 1)
             e = launch_attn_combine(a, d, stream);
     }

@@ -9,6 +9,7 @@
 // reads (ds_read_b64_tr_b16: 16 lanes read 4 keys x 16 values and get 4 keys of one value each).
 #pragma once
 
+#include "attention.h"
 #include "common.h"
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -72,6 +73,72 @@ __device__ __forceinline__ int wave_total(int v)
     v += __builtin_amdgcn_update_dpp(0, v, 0x142, 10, 15, false);    // lane 15 of rows 0, 2 to rows 1, 3
     v += __builtin_amdgcn_update_dpp(0, v, 0x143, 12, 15, false);    // lane 31 to rows 2, 3
     return __builtin_amdgcn_readlane(v, 63);
+}
+
+// Largest over the 64 lanes of a wave, as a scalar.
+__device__ __forceinline__ float wave_largest(float v)
+{
+    const int lowest = __float_as_int(-INFINITY);
+#define STEP(ctrl, rows) \
+    v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(lowest, __float_as_int(v), ctrl, rows, 15, false)))
+    STEP(0x111, 15);
+    STEP(0x112, 15);
+    STEP(0x114, 15);
+    STEP(0x118, 15);
+    STEP(0x142, 10);
+    STEP(0x143, 12);
+#undef STEP
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// One wave: chunks [ca, cb) of a row (partial outputs, maxima and sums from `slot` on) joined into row t of head hd.
+template <int D>
+__device__ __forceinline__ void join_chunks(const AttnArgs &a, int64_t slot, int ca, int cb, int64_t t, int hd)
+{
+    constexpr int VPT = D / 64, AHEAD = 8;
+    const int lane = threadIdx.x & 63;
+    float mx = ATTN_LOWEST, sum = 0.f, acc[VPT];
+    for (int c = ca + lane; c < cb; c += 64)
+        mx = fmaxf(mx, a.part_ml[2 * (slot + c)]);
+    mx = wave_largest(mx);
+#pragma unroll
+    for (int e = 0; e < VPT; ++e)
+        acc[e] = 0.f;
+    for (int c0 = ca; c0 < cb; c0 += 64) {
+        float f = 0.f;                          // this lane's chunk
+        if (c0 + lane < cb) {
+            const f32x2 ml = *(const f32x2 *)(a.part_ml + 2 * (slot + c0 + lane));
+            f = __builtin_amdgcn_exp2f(ml[0] - mx);
+            sum += f * ml[1];
+        }
+        const int n = min(64, cb - c0);
+        for (int i = 0; i < n; i += AHEAD) {
+            float x[AHEAD][VPT];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+#pragma unroll
+                for (int e = 0; e < VPT; ++e)
+                    x[j][e] = a.part_o[(slot + c0 + min(i + j, n - 1)) * D + lane * VPT + e];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), i + j));
+#pragma unroll
+                for (int e = 0; e < VPT; ++e)
+                    acc[e] += i + j < n ? w * x[j][e] : 0.f;
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        sum += __shfl_xor(sum, off, 64);
+    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+    uint16_t *dst = a.out + t * a.out_stride + (int64_t)hd * D + lane * VPT;
+    if (VPT == 2)
+        *(uint32_t *)dst = cvt_bf16x2(acc[0] * inv, acc[VPT - 1] * inv);
+    else
+        dst[0] = (uint16_t)cvt_bf16x2(acc[0] * inv, 0.f);
+    if (a.lse && lane == 0)
+        a.lse[t * a.hq + hd] = sum == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
 }
 
 __device__ __forceinline__ int clamp_page(int page, int n_pages)

@@ -8,6 +8,7 @@
 // transposed, so the loop has no barrier.  The next step's loads are issued while this one's
 // softmax and second product run.  Bound by HBM (or, for a short batch, by latency).
 #include <algorithm>
+#include <type_traits>
 
 #include "attention.h"
 #include "attention_device.h"
@@ -38,29 +39,82 @@ __device__ __forceinline__ bool answers(const AttnArgs &a, const SeqChunks &s)
            (int64_t)s.n * a.group <= a.max_rows;
 }
 
-template <int D, int NQ, bool FP8>
-__global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a)
+// Swizzle of the 16-byte pieces of a V row in LDS by its key: writes of one piece over 16 keys and transposing
+// reads of 8 keys x 2 pieces both touch every bank once.
+template <int D>
+__device__ __forceinline__ int ad_swz(int key)
 {
+    return D == 128 ? (key & 7) << 1 | ((key >> 3) & 1) : ((key >> 1) & 3) << 1 | ((key >> 3) & 1);
+}
+
+template <int D, int NQ, bool FP8, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void attn_decode_kernel(AttnArgs a)
+{
+    constexpr int ESZ = FP8 ? 1 : 2;
     constexpr int KS = D / 32;          // k-steps of the first product
     constexpr int DB = D / 16;          // row blocks of the second
     constexpr int LD = FP8 ? D / 64 : D / 32;   // 16-byte loads per lane and 16-key block
     constexpr int OS = D + 4;           // row stride of the joined accumulators in LDS
     constexpr int VW = 32 * D;          // a wave's V rows in LDS
-    __shared__ __attribute__((aligned(16))) uint16_t lds[4 * (VW > 32 * OS ? VW : 32 * OS)];
-    __shared__ float ml[4][16][2];
+    constexpr int STEP = 32 * NW;       // keys the workgroup takes at a time
+    __shared__ __attribute__((aligned(16))) uint16_t lds[NW * (VW > 32 * OS ? VW : 32 * OS)];
+    __shared__ float ml[NW][16][2];
 
     const int b = (int)(blockIdx.x / a.hkv), h = (int)(blockIdx.x - (unsigned)b * a.hkv);
+    const int c = blockIdx.y, wave = uniform(threadIdx.x >> 6);
     const SeqChunks sq = seq_chunks(a, b);
-    const int c = blockIdx.y;
-    if (!answers(a, sq) || c >= sq.count)
-        return;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int rows = sq.n * a.group, L = sq.L;
     const int k0 = max((sq.c0 + c) * a.chunk, sq.lo & ~31), k1 = min(L, (sq.c0 + c + 1) * a.chunk);
     const int32_t *__restrict__ table = a.table + (int64_t)b * a.table_stride;
     const int ps = a.cache.ps, pm = (1 << ps) - 1;
     uint16_t *vl = lds + wave * VW;
+
+    u32x4 kr[2][LD], vr[2][LD];
+    f32x4 ks[2], vs[2];
+    int pg[2];
+    // pages of the two 16-key blocks of the step at kb (what a table holds past the end is read as some page,
+    // whose keys are masked: so the first lookup need not wait for the length)
+    const int last = (int)a.table_stride - 1;
+    auto lookup = [&](int kb) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            pg[u] = table[min((kb + 16 * u) >> ps, last)];
+    };
+    // (a scalar base and a constant offset a lane)
+    const uint32_t off = col * D * ESZ + 16 * g;
+    auto load = [&](int kb) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int64_t at = (((int64_t)clamp_page(uniform(pg[u]), a.cache.n_pages) * a.cache.hkv + h) << ps) + ((kb + 16 * u) & pm);
+            const uint8_t *kp = a.cache.k + at * D * ESZ, *vp = a.cache.v + at * D * ESZ;
+#pragma unroll
+            for (int s = 0; s < LD; ++s)
+                kr[u][s] = *(const u32x4 *)(kp + (off + 64 * s));
+#pragma unroll
+            for (int s = 0; s < LD; ++s)
+                vr[u][s] = *(const u32x4 *)(vp + (off + 64 * s));
+            if (FP8) {
+                ks[u] = *(const f32x4 *)(a.cache.k_scale + at + 4 * g);
+                vs[u] = *(const f32x4 *)(a.cache.v_scale + at + 4 * g);
+            }
+        }
+    };
+    int kb = c * a.chunk + 32 * wave;
+    if (a.table_stride > 0)
+        lookup(kb);
+    if (!answers(a, sq) || c >= sq.count)
+        return;
+    if (k0 != c * a.chunk) {            // a window hides the first chunks
+        kb = k0 + 32 * wave;
+        if (kb < k1)
+            lookup(kb);
+    }
+    if (kb < k1) {
+        load(kb);
+        if (kb + STEP < k1)
+            lookup(kb + STEP);
+    }
 
     // Q as B operand: column = row of the sequence, 8 values a k-step; its position
     u32x4 qf[NQ][KS];
@@ -87,45 +141,10 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a)
             o[j][d] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 
-    u32x4 kr[2][LD], vr[2][LD];
-    f32x4 ks[2], vs[2];
-    int pg[2];
-    // pages of the two 16-key blocks of the step at kb (blocks past the end: the last key's page)
-    auto lookup = [&](int kb) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-            pg[u] = clamp_page(table[min(kb + 16 * u, L - 1) >> ps], a.cache.n_pages);
-    };
-    auto load = [&](int kb) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int64_t at = (((int64_t)pg[u] * a.cache.hkv + h) << ps) + (min(kb + 16 * u, (L - 1) & ~15) & pm);
-            const int esz = FP8 ? 1 : 2;
-            const uint8_t *kp = a.cache.k + (at + col) * D * esz + 16 * g;
-            const uint8_t *vp = a.cache.v + (at + col) * D * esz + 16 * g;
-#pragma unroll
-            for (int s = 0; s < LD; ++s)
-                kr[u][s] = *(const u32x4 *)(kp + 64 * s);
-#pragma unroll
-            for (int s = 0; s < LD; ++s)
-                vr[u][s] = *(const u32x4 *)(vp + 64 * s);
-            if (FP8) {
-                ks[u] = *(const f32x4 *)(a.cache.k_scale + at + 4 * g);
-                vs[u] = *(const f32x4 *)(a.cache.v_scale + at + 4 * g);
-            }
-        }
-    };
-
-    int kb = k0 + 32 * wave;
-    if (kb < k1) {
-        lookup(kb);
-        load(kb);
-        if (kb + 128 < k1)
-            lookup(kb + 128);
-    }
-    for (; kb < k1; kb += 128) {
-        // a step whose keys some query of the sequence does not see
-        const bool edge = kb + 32 > L - sq.n + 1 || (a.window > 0 && kb <= L - 1 - a.window);
+    const uint32_t wlane = col * D * 2 + 16 * ((FP8 ? 2 * g : g) ^ ad_swz<D>(col));
+    const int vk = 4 * g + (col >> 2);
+    const uint32_t rlane = vk * D * 2 + 16 * (((col & 3) >> 1) ^ ad_swz<D>(vk)) + 8 * (col & 1);
+    auto step = [&](auto edge) {
         // S^T: rows = keys 16 u + 4 g + i, column = query
         f32x4 st[NQ][2];
 #pragma unroll
@@ -144,9 +163,15 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a)
                 for (int j = 0; j < NQ; ++j)
                     st[j][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, as_bf16x8(qf[j][s]), st[j][u], 0, 0, 0);
             }
+#pragma unroll
+            for (int j = 0; j < NQ; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    st[j][u][i] *= FP8 ? cs * ks[u][i] : cs;
         }
-        // V rows into LDS ([key][D], 16-byte pieces swizzled by key); rows outside [lo, L) as zeros
-        uint32_t bad = 0;
+        // V rows into LDS ([key][D], pieces swizzled); rows outside [lo, L) as zeros
+        uint32_t bad[2] = {0, 0}, wl = wlane;
+        asm volatile("" : "+v"(wl));        // (keeps the compiler from holding every address in a register)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int key = 16 * u + col;
@@ -163,50 +188,48 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a)
 #pragma unroll
                 for (int e = 0; e < (FP8 ? 2 : 1); ++e) {
                     if (edge) {
-                        w[e] = in ? w[e] : u32x4{0, 0, 0, 0};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            bad = not_finite(bad, w[e][i]);
+                        for (int i = 0; i < 4; ++i) {
+                            w[e][i] = in ? w[e][i] : 0u;
+                            bad[u] = not_finite(bad[u], w[e][i]);
+                        }
                     }
-                    const int piece = FP8 ? 8 * s + 2 * g + e : 4 * s + g;   // D = 64: 8 pieces a row
-                    *(u32x4 *)(vl + key * D + 8 * (piece ^ (key & (D / 8 - 1)))) = w[e];
+                    // piece 8 s + 2 g + e (e4m3) or 4 s + g
+                    *(u32x4 *)((uint8_t *)vl + (wl ^ (FP8 ? 128 * s + 16 * e : 64 * s)) + 32 * u * D) = w[e];
                 }
             }
         }
-        f32x4 kss[2], vss[2];
+        f32x4 vss[2];
         if (FP8) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                kss[u] = ks[u];
+            for (int u = 0; u < 2; ++u)
                 vss[u] = vs[u];
-            }
         }
         // the next step's loads
-        if (kb + 128 < k1) {
-            load(kb + 128);
-            if (kb + 256 < k1)
-                lookup(kb + 256);
+        if (kb + STEP < k1) {
+            load(kb + STEP);
+            if (kb + 2 * STEP < k1)
+                lookup(kb + 2 * STEP);
         }
         u32x4 pf[NQ];
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
+            if (edge)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = kb + 16 * u + 4 * g + i;
+                        const bool see = key < L && (!a.causal || key <= pos[j]) &&
+                                         (a.window <= 0 || key > pos[j] - a.window);
+                        st[j][u][i] = see ? st[j][u][i] : -INFINITY;
+                    }
             float mx = -INFINITY;
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float s = st[j][u][i] * cs;
-                    if (FP8)
-                        s *= kss[u][i];
-                    if (edge) {
-                        const int key = kb + 16 * u + 4 * g + i;
-                        const bool see = key < L && (!a.causal || key <= pos[j]) &&
-                                         (a.window <= 0 || key > pos[j] - a.window);
-                        s = see ? s : -INFINITY;
-                    }
-                    st[j][u][i] = s;
-                    mx = fmaxf(mx, s);
-                }
+                for (int i = 0; i < 4; ++i)
+                    mx = fmaxf(mx, st[j][u][i]);
             if (__any(mx > m[j] + ATTN_SLACK)) {
                 mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
                 mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
@@ -228,45 +251,44 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a)
                     // (a masked key's scale may be anything)
                     p[4 * u + i] = !FP8 ? e : edge && st[j][u][i] == -INFINITY ? 0.f : e * vss[u][i];
                 }
+            // P^T rounded to bf16 (half a step: 2^-8 relative) for the matrix cores; the sum keeps fp32
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 pf[j][i] = cvt_bf16x2(p[2 * i], p[2 * i + 1]);
         }
         // O^T += V^T P^T; k index (g, e) is key 16 (e / 4) + 4 g + e % 4
+        uint32_t rl = rlane;
+        asm volatile("" : "+v"(rl));
         auto vfrag = [&](int d) {
             u32x4 f;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int key = 16 * u + 4 * g + (col >> 2), piece = 2 * d + ((col & 3) >> 1);
-                const u32x2 w = lds_read_tr(vl + key * D + 8 * (piece ^ (key & (D / 8 - 1))) + 4 * (col & 1));
+            for (int u = 0; u < 2; ++u) {       // keys 16 u + vk, values 16 d ..
+                const u32x2 w = lds_read_tr((const uint16_t *)((const uint8_t *)vl + (rl ^ (32 * d)) + 32 * u * D));
                 f[2 * u] = w[0];
                 f[2 * u + 1] = w[1];
             }
             return f;
         };
-        if (!(edge && __any((bad & 0x80008000u) != 0))) {
+        if (edge && sq.n > 1) {
+            // V may hold an infinity or NaN where some query must not see it (0 x NaN is NaN): such keys one at
+            // a time, kept only by the queries that see them, and zeroed for the rest
+            uint32_t some = 0;
 #pragma unroll
-            for (int d = 0; d < DB; ++d) {
-                const bf16x8 vf = as_bf16x8(vfrag(d));
-#pragma unroll
-                for (int j = 0; j < NQ; ++j)
-                    o[j][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, as_bf16x8(pf[j]), o[j][d], 0, 0, 0);
+            for (int u = 0; u < 2; ++u) {
+                uint64_t x = ballot64((bad[u] & 0x80008000u) != 0);
+                x |= x >> 32;
+                x |= x >> 16;
+                some |= (uint32_t)(x & 0xffff) << (16 * u);
             }
-        } else {
-            // V holds an infinity or NaN where some query must not see it (0 x NaN is NaN): one key at a
-            // time, kept only by the queries that see it
-#pragma unroll 1
-            for (int key = 0; key < 32; ++key) {
-                const bool mine = g == ((key & 15) >> 2);
-                const int e = 4 * (key >> 4) + (key & 3);
-                const uint32_t half = (e & 1) ? 0xffff0000u : 0xffffu;
-                const int ka = kb + key;
+            for (; some; some &= some - 1) {
+                const int key = __ffs((int)some) - 1, e = 4 * (key >> 4) + (key & 3), ka = kb + key;
+                const uint32_t half = g != ((key & 15) >> 2) ? 0u : (e & 1) ? 0xffff0000u : 0xffffu;
 #pragma unroll
                 for (int d = 0; d < DB; ++d) {
                     u32x4 f = vfrag(d);
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        f[i] = mine && i == (e >> 1) ? f[i] & half : 0u;
+                        f[i] &= i == (e >> 1) ? half : 0u;
 #pragma unroll
                     for (int j = 0; j < NQ; ++j) {
                         const f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f), as_bf16x8(pf[j]), o[j][d], 0, 0, 0);
@@ -277,11 +299,30 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a)
                             o[j][d][i] = see ? t[i] : o[j][d][i];
                     }
                 }
+                if (lane < D / 8)
+                    *(u32x4 *)(vl + key * D + 8 * lane) = u32x4{0, 0, 0, 0};
             }
         }
-    }
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+            const bf16x8 vf = as_bf16x8(vfrag(d));
+#pragma unroll
+            for (int j = 0; j < NQ; ++j)
+                o[j][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, as_bf16x8(pf[j]), o[j][d], 0, 0, 0);
+            if (d & 1)
+                __builtin_amdgcn_sched_barrier(0);      // (not all fragments at once: registers)
+        }
+    };
+    // steps that hold a key which some query of the sequence does not see: below `free` and from `full` on
+    const int full = L - sq.n + 1 - 32, free = a.window > 0 ? L - a.window : 0;
+    for (; kb < k1 && kb < free; kb += STEP)
+        step(std::true_type());
+    for (; kb < k1 && kb <= full; kb += STEP)
+        step(std::false_type());
+    for (; kb < k1; kb += STEP)
+        step(std::true_type());
 
-    // join the four waves, 16 rows at a time
+    // join the waves, 16 rows at a time
     float *of = (float *)lds;
 #pragma unroll
     for (int j = 0; j < NQ; ++j) {
@@ -290,35 +331,39 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a)
         float lj = l[j] + __shfl_xor(l[j], 16, 64);
         lj += __shfl_xor(lj, 32, 64);
         __syncthreads();
+        if (16 * j + col < rows) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
-            *(f32x4 *)(of + (wave * 16 + col) * OS + 16 * d + 4 * g) = o[j][d];
-        if (g == 0) {
-            ml[wave][col][0] = m[j];
-            ml[wave][col][1] = lj;
+            for (int d = 0; d < DB; ++d)
+                *(f32x4 *)(of + (wave * 16 + col) * OS + 16 * d + 4 * g) = o[j][d];
+            if (g == 0) {
+                ml[wave][col][0] = m[j];
+                ml[wave][col][1] = lj;
+            }
         }
         __syncthreads();
         const int r = threadIdx.x >> 4, part = threadIdx.x & 15;
         const int row = 16 * j + r;
-        if (row < rows) {
+        if (r < 16 && row < rows) {
             float mx = ml[0][r][0];
 #pragma unroll
-            for (int w = 1; w < 4; ++w)
+            for (int w = 1; w < NW; ++w)
                 mx = fmaxf(mx, ml[w][r][0]);
-            float f[4], sum = 0.f;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                f[w] = __builtin_amdgcn_exp2f(ml[w][r][0] - mx);
-                sum += f[w] * ml[w][r][1];
-            }
             constexpr int VPT = D / 16;   // values a thread
-            float acc[VPT];
+            float sum = 0.f, acc[VPT];
 #pragma unroll
-            for (int e = 0; e < VPT; ++e) {
+            for (int e = 0; e < VPT; ++e)
                 acc[e] = 0.f;
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    acc[e] += f[w] * of[(w * 16 + r) * OS + part * VPT + e];
+            for (int w = 0; w < NW; ++w) {
+                const float f = __builtin_amdgcn_exp2f(ml[w][r][0] - mx);
+                sum += f * ml[w][r][1];
+#pragma unroll
+                for (int e = 0; e < VPT; e += 4) {
+                    const f32x4 x = *(const f32x4 *)(of + (w * 16 + r) * OS + part * VPT + e);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        acc[e + i] += f * x[i];
+                }
             }
             const int i = row / a.group, hd = h * a.group + row - i * a.group;
             if (sq.count == 1) {
@@ -346,46 +391,24 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a)
     }
 }
 
-// One wave a row: the row's chunks joined by their maxima and sums.  Rows of one chunk were
-// written whole.  Slots are numbered by (sequence, kv head, row).
+// One wave a row: the row's chunks joined.  Rows of one chunk were written whole.  Slots are numbered by
+// (sequence, kv head, row).
 template <int D>
 __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs a)
 {
-    constexpr int VPT = D / 64;
     const int b = (int)(blockIdx.x / a.hkv), h = (int)(blockIdx.x - (unsigned)b * a.hkv);
     const SeqChunks sq = seq_chunks(a, b);
-    const int row = (int)blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int row = (int)blockIdx.y * 4 + (threadIdx.x >> 6);
     if (!answers(a, sq) || sq.count <= 1 || row >= sq.n * a.group)
         return;
-    const int64_t slot = (((int64_t)b * a.hkv + h) * a.max_rows + row) * a.n_chunks;
-    float mx = ATTN_LOWEST, sum = 0.f, acc[VPT];
-    for (int c = 0; c < sq.count; ++c)
-        mx = fmaxf(mx, a.part_ml[2 * (slot + c)]);
-#pragma unroll
-    for (int e = 0; e < VPT; ++e)
-        acc[e] = 0.f;
-    for (int c = 0; c < sq.count; ++c) {
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (slot + c)] - mx);
-        sum += f * a.part_ml[2 * (slot + c) + 1];
-#pragma unroll
-        for (int e = 0; e < VPT; ++e)
-            acc[e] += f * a.part_o[(slot + c) * D + lane * VPT + e];
-    }
-    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
     const int i = row / a.group, hd = h * a.group + row - i * a.group;
-    uint16_t *dst = a.out + (sq.q0 + i) * a.out_stride + (int64_t)hd * D + lane * VPT;
-#pragma unroll
-    for (int e = 0; e < VPT; ++e)
-        dst[e] = f32_to_bf16(acc[e] * inv);
-    if (a.lse && lane == 0)
-        a.lse[(int64_t)(sq.q0 + i) * a.hq + hd] =
-            sum == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
+    join_chunks<D>(a, (((int64_t)b * a.hkv + h) * a.max_rows + row) * a.n_chunks, 0, sq.count, sq.q0 + i, hd);
 }
 
-hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, hipStream_t stream)
+hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int waves, hipStream_t stream)
 {
     const dim3 grid((unsigned)(a.n_seqs * (int64_t)a.hkv), (unsigned)a.n_chunks);
-#define DEC(D, NQ, F) attn_decode_kernel<D, NQ, F><<<grid, dim3(256), 0, stream>>>(a)
+#define DEC(D, NQ, F) (waves == 8 ? attn_decode_kernel<D, 1, F, 8><<<grid, dim3(512), 0, stream>>>(a) : attn_decode_kernel<D, NQ, F, 4><<<grid, dim3(256), 0, stream>>>(a))
 #define DEC_F(D, NQ) (a.cache.fp8 ? DEC(D, NQ, true) : DEC(D, NQ, false))
 #define DEC_Q(D) (nq == 1 ? DEC_F(D, 1) : DEC_F(D, 2))
     head_dim == 64 ? DEC_Q(64) : DEC_Q(128);

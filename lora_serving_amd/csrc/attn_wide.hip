@@ -591,7 +591,6 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
 template <int D>
 __global__ __launch_bounds__(256) void attn_wide_combine_kernel(AttnArgs a)
 {
-    constexpr int VPT = D / 64;
     const int64_t th = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     if (th >= a.T * a.hq)
@@ -615,28 +614,8 @@ __global__ __launch_bounds__(256) void attn_wide_combine_kernel(AttnArgs a)
     const int L = (int)min((int64_t)max(a.kv_len[b], 0), min(a.max_kv, a.table_stride << a.cache.ps));
     const int pos = L - n + t - q0;
     const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0, hi = a.causal ? min(L, pos + 1) : L;
-    const int64_t slot = th * a.n_chunks;
     const int ca = lo / a.chunk, cb = hi > lo ? (hi - 1) / a.chunk + 1 : ca;
-    float mx = ATTN_LOWEST, sum = 0.f, acc[VPT];
-    for (int c = ca; c < cb; ++c)
-        mx = fmaxf(mx, a.part_ml[2 * (slot + c)]);
-#pragma unroll
-    for (int e = 0; e < VPT; ++e)
-        acc[e] = 0.f;
-    for (int c = ca; c < cb; ++c) {
-        const float f = __builtin_amdgcn_exp2f(a.part_ml[2 * (slot + c)] - mx);
-        sum += f * a.part_ml[2 * (slot + c) + 1];
-#pragma unroll
-        for (int e = 0; e < VPT; ++e)
-            acc[e] += f * a.part_o[(slot + c) * D + lane * VPT + e];
-    }
-    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
-    uint16_t *dst = a.out + (int64_t)t * a.out_stride + (int64_t)hd * D + lane * VPT;
-#pragma unroll
-    for (int e = 0; e < VPT; ++e)
-        dst[e] = f32_to_bf16(acc[e] * inv);
-    if (a.lse && lane == 0)
-        a.lse[th] = sum == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
+    join_chunks<D>(a, th * a.n_chunks, ca, cb, t, hd);
 }
 
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream)

@@ -171,11 +171,28 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream):
+_raw_stream = None      # handle of the current stream (torch is loaded at the first call)
+
+
+def _load_raw_stream():
+    """torch.cuda.current_stream() builds a Stream object at every call (2.8 us, as much as a
+    launch); torch's own handle lookup takes 0.1 us."""
+    global _raw_stream
     import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    c = torch._C
+    if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+        torch.cuda.current_stream()             # initialises the device once
+        _raw_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())  # noqa: E731
+    else:
+        _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+
+
+def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is None:
+        _load_raw_stream()
+    return _raw_stream()
 
 
 def _need(t, dtypes, name):
@@ -431,35 +448,58 @@ def mlora_cache_bytes(n_pages: int, n_kv_heads: int, page_size: int, head_dim: i
     return int(_lib.mlora_cache_bytes(n_pages, n_kv_heads, page_size, head_dim, dtype))
 
 
+_bf16_type = _i32_type = _f32_type = None
+
+
+def _load_types():
+    global _bf16_type, _i32_type, _f32_type
+    import torch
+    _bf16_type, _i32_type, _f32_type = torch.bfloat16, torch.int32, torch.float32
+
+
 def _rows(t, name, shape=None):
     """Row stride of a bf16 [T][heads][head_dim] device tensor whose rows may lie apart."""
-    import torch
+    if _bf16_type is None:
+        _load_types()
     if t is None or not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
-    if t.dtype != torch.bfloat16 or t.dim() != 3:
+    if t.dtype is not _bf16_type or t.dim() != 3:
         raise ValueError(f"{name} must be bf16 [T][heads][head_dim]")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     n, h, d = t.shape
-    st = t.stride()
-    if n > 0 and (st[2] != 1 or (h > 1 and st[1] != d)):
+    if shape is not None and (n, h, d) != tuple(shape):
+        raise ValueError(f"{name} has shape {(n, h, d)}, expected {tuple(shape)}")
+    sn, sh, sd = t.stride()
+    if n > 0 and (sd != 1 or (h > 1 and sh != d)):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return st[0] if n > 1 else h * d
+    return sn if n > 1 else h * d
 
 
 def _ints(t, n, name):
-    import torch
-    _need(t, (torch.int32,), name)
+    if _i32_type is None:
+        _load_types()
+    if t is None or t.dtype is not _i32_type or not t.is_cuda or not t.is_contiguous():
+        _need(t, (_i32_type,), name)
     if t.numel() != n:
         raise ValueError(f"{name} has {t.numel()} values, expected {n}")
     return t.data_ptr()
 
 
+def _dense(t, shape, name):
+    if _bf16_type is None:
+        _load_types()
+    if t.dtype is not _bf16_type or not t.is_cuda or not t.is_contiguous():
+        _need(t, (_bf16_type,), name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}")
+    return t.data_ptr()
+
+
 def _lse(lse, T, heads):
-    import torch
     if lse is None:
         return None
-    _need(lse, (torch.float32,), "lse")
+    if _f32_type is None:
+        _load_types()
+    _need(lse, (_f32_type,), "lse")
     if lse.shape != (T, heads):
         raise ValueError(f"lse must have shape {(T, heads)}")
     return lse.data_ptr()
@@ -470,38 +510,41 @@ def mlora_qk_rope(qkv, n_q_heads: int, n_kv_heads: int, head_dim: int, pos, rope
                   cache: Cache | None = None, slot=None, stream=None):
     """qkv bf16 [T][(n_q_heads + 2 n_kv_heads) * head_dim]; q_out, k_out bf16
     [T][heads][head_dim], also views of qkv's own query and key parts."""
-    import torch
-    if qkv.dtype != torch.bfloat16 or not qkv.is_cuda or qkv.dim() != 2:
+    if _bf16_type is None:
+        _load_types()
+    if qkv.dtype is not _bf16_type or not qkv.is_cuda or qkv.dim() != 2:
         raise ValueError("qkv must be a bf16 [T][width] device tensor")
-    T = qkv.shape[0]
+    T, w = qkv.shape
     width = (n_q_heads + 2 * n_kv_heads) * head_dim
-    if qkv.shape[1] != width or (T > 0 and qkv.stride(1) != 1):
+    row, one = qkv.stride()
+    if w != width or (T > 0 and one != 1):
         raise ValueError(f"rows of qkv must hold {width} contiguous values")
     q_stride = _rows(q_out, "q_out", (T, n_q_heads, head_dim))
     k_stride = 0 if k_out is None else _rows(k_out, "k_out", (T, n_kv_heads, head_dim))
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None and _bf16(w, name).numel() != head_dim:
             raise ValueError(f"{name} must hold head_dim values")
-    _check(_lib.mlora_qk_rope(qkv.data_ptr(), T, qkv.stride(0) if T > 1 else width, n_q_heads,
-                              n_kv_heads, head_dim, _ints(pos, T, "pos"), rope.ref,
-                              _ptr(q_weight), _ptr(k_weight), eps, q_out.data_ptr(), q_stride,
-                              _ptr(k_out), k_stride, None if cache is None else cache.ref,
-                              None if slot is None else _ints(slot, T, "slot"),
-                              _stream(stream)), "mlora_qk_rope")
+    code = _lib.mlora_qk_rope(qkv.data_ptr(), T, row if T > 1 else width, n_q_heads, n_kv_heads,
+                              head_dim, _ints(pos, T, "pos"), rope.ref,
+                              None if q_weight is None else q_weight.data_ptr(),
+                              None if k_weight is None else k_weight.data_ptr(), eps,
+                              q_out.data_ptr(), q_stride,
+                              None if k_out is None else k_out.data_ptr(), k_stride,
+                              None if cache is None else cache.ref,
+                              None if slot is None else _ints(slot, T, "slot"), _stream(stream))
+    if code:
+        _check(code, "mlora_qk_rope")
 
 
 def mlora_cache_read(cache: Cache, slot, k, v, stream=None):
     """Tokens slot[0..T) of the cache into k, v bf16 [T][n_kv_heads][head_dim] (either None)."""
-    import torch
     T = slot.numel()
-    for t, name in ((k, "k"), (v, "v")):
-        if t is not None:
-            _need(t, (torch.bfloat16,), name)
-            if t.shape != (T, cache.n_kv_heads, cache.head_dim):
-                raise ValueError(f"{name} must have shape "
-                                 f"{(T, cache.n_kv_heads, cache.head_dim)}")
-    _check(_lib.mlora_cache_read(cache.ref, _ints(slot, T, "slot"), T, _ptr(k), _ptr(v),
-                                 _stream(stream)), "mlora_cache_read")
+    shape = (T, cache.n_kv_heads, cache.head_dim)
+    code = _lib.mlora_cache_read(cache.ref, _ints(slot, T, "slot"), T,
+                                 None if k is None else _dense(k, shape, "k"),
+                                 None if v is None else _dense(v, shape, "v"), _stream(stream))
+    if code:
+        _check(code, "mlora_cache_read")
 
 
 def mlora_attention(q, k, v, cu_q, out, cu_k=None, max_q: int | None = None, causal: bool = True,
@@ -509,17 +552,20 @@ def mlora_attention(q, k, v, cu_q, out, cu_k=None, max_q: int | None = None, cau
     """q, out bf16 [T_q][n_q_heads][head_dim], k, v bf16 [T_k][n_kv_heads][head_dim], rows of any
     stride (views of a merged row); cu_q, cu_k int32 [n_seqs + 1] device.  max_q: the longest
     sequence's queries (None: T_q)."""
-    T, hq, d = q.shape
-    hkv = k.shape[1]
+    q_shape, k_shape = q.shape, k.shape
+    q_stride = _rows(q, "q")
+    T, hq, d = q_shape
+    k_stride = _rows(k, "k", (k_shape[0], k_shape[1], d))
     n = cu_q.numel() - 1
-    _check(_lib.mlora_attention(q.data_ptr(), _rows(q, "q"), k.data_ptr(),
-                                _rows(k, "k", (k.shape[0], hkv, d)), v.data_ptr(),
-                                _rows(v, "v", k.shape), T, k.shape[0], n,
+    code = _lib.mlora_attention(q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(),
+                                _rows(v, "v", k_shape), T, k_shape[0], n,
                                 _ints(cu_q, n + 1, "cu_q"),
-                                None if cu_k is None else _ints(cu_k, n + 1, "cu_k"), hq, hkv, d,
-                                T if max_q is None else max_q, int(causal), window, scale,
-                                out.data_ptr(), _rows(out, "out", q.shape), _lse(lse, T, hq),
-                                _stream(stream)), "mlora_attention")
+                                None if cu_k is None else _ints(cu_k, n + 1, "cu_k"), hq,
+                                k_shape[1], d, T if max_q is None else max_q, int(causal), window,
+                                scale, out.data_ptr(), _rows(out, "out", q_shape),
+                                _lse(lse, T, hq), _stream(stream))
+    if code:
+        _check(code, "mlora_attention")
 
 
 def mlora_paged_workspace_size(T: int, n_seqs: int, n_q_heads: int, n_kv_heads: int,
@@ -543,20 +589,26 @@ def mlora_paged_attention(q, cache: Cache, page_table, cu_q, kv_len, out, max_q:
                           lse=None, ws=None, stream=None):
     """q, out bf16 [T][n_q_heads][head_dim] (rows of any stride); page_table int32
     [n_seqs][pages], cu_q int32 [n_seqs + 1], kv_len int32 [n_seqs], device."""
-    T, hq, d = q.shape
+    q_shape = q.shape
+    q_stride = _rows(q, "q")
+    T, hq, d = q_shape
     n = kv_len.numel()
     if page_table.dim() != 2 or page_table.shape[0] != n:
         raise ValueError("page_table must be [n_seqs][pages]")
     if d != cache.head_dim:
         raise ValueError("q and the cache must have one head_dim")
-    _check(_lib.mlora_paged_attention(q.data_ptr(), _rows(q, "q"), T, hq, cache.ref,
+    if ws is not None and not ws.is_cuda:
+        raise ValueError("ws must be a device tensor")
+    code = _lib.mlora_paged_attention(q.data_ptr(), q_stride, T, hq, cache.ref,
                                       _ints(page_table, page_table.numel(), "page_table"),
                                       page_table.shape[1], n, _ints(cu_q, n + 1, "cu_q"),
                                       _ints(kv_len, n, "kv_len"), max_q, max_kv, int(causal),
-                                      window, scale, out.data_ptr(), _rows(out, "out", q.shape),
+                                      window, scale, out.data_ptr(), _rows(out, "out", q_shape),
                                       _lse(lse, T, hq), None if ws is None else ws.data_ptr(),
                                       0 if ws is None else ws.numel() * ws.element_size(),
-                                      _stream(stream)), "mlora_paged_attention")
+                                      _stream(stream))
+    if code:
+        _check(code, "mlora_paged_attention")
 
 
 def mlora_validate_pages(cache: Cache, page_table, cu_q, kv_len, T: int, max_q: int,
