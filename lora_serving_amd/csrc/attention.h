@@ -48,18 +48,23 @@ struct AttnArgs {
     float scale;
     uint16_t *out;
     float *lse;
-    // split over keys: sequences of more than one chunk leave fp32 partial rows that
-    // launch_attn_combine joins
-    int32_t chunk, n_chunks;       // keys per chunk (a multiple of 64), chunks a launch covers
-    float *part_o, *part_ml;       // [rows][n_chunks][head_dim], [rows][n_chunks][2]
+    // split over keys: parts as fp32 rows and their maxima and sums, which a second kernel joins.  Wide: chunks of
+    // `chunk` keys (a multiple of 64), [token][head][n_chunks]; decode: two slots of max_rows rows a share
+    // (part_o == nullptr: no split).
+    int32_t chunk, n_chunks;
+    float *part_o, *part_ml;       // [..][head_dim], [..][2]
     int32_t min_rows, max_rows;    // sequences this launch answers: rows = queries * group
 };
 // Whole prompts (cache unused) or, with pages, chunks of new tokens.
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream);
 constexpr int WIDE_ROWS = 128;    // rows (queries x heads of a group) of one workgroup
 hipError_t launch_attn_wide_combine(const AttnArgs &a, int head_dim, hipStream_t stream);
-// Sequences of up to 16 * nq rows (nq 1 or 2) over pages.
-hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int waves, hipStream_t stream);
-hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, hipStream_t stream);
+// Sequences of up to 16 * nq rows (nq 1 or 2) over pages, their keys cut into `shares` equal shares, or (part_o ==
+// nullptr) one workgroup a sequence and kv head, then shares = n_seqs * hkv.
+constexpr int DECODE_UNIT = 128;  // keys: the unit that shares are made of
+// Workgroups that a CU holds at a time.
+constexpr int decode_slots(int head_dim, int nq) { return head_dim == 64 && nq == 1 ? 3 : 2; }
+hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream);
+hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream);
 
 }  // namespace mlora

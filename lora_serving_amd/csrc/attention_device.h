@@ -63,8 +63,8 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t acc, uint32_t w)
 // a value that is the same in all lanes, as a scalar
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-// Sum over the 64 lanes of a wave, as a scalar (DPP: no trip through LDS).
-__device__ __forceinline__ int wave_total(int v)
+// Sum of the lanes up to and with this one (DPP: no trip through LDS).
+__device__ __forceinline__ int wave_prefix(int v)
 {
     v += __builtin_amdgcn_update_dpp(0, v, 0x111, 15, 15, false);    // row_shr 1, 2, 4, 8
     v += __builtin_amdgcn_update_dpp(0, v, 0x112, 15, 15, false);
@@ -72,8 +72,10 @@ __device__ __forceinline__ int wave_total(int v)
     v += __builtin_amdgcn_update_dpp(0, v, 0x118, 15, 15, false);
     v += __builtin_amdgcn_update_dpp(0, v, 0x142, 10, 15, false);    // lane 15 of rows 0, 2 to rows 1, 3
     v += __builtin_amdgcn_update_dpp(0, v, 0x143, 12, 15, false);    // lane 31 to rows 2, 3
-    return __builtin_amdgcn_readlane(v, 63);
+    return v;
 }
+// Sum over the 64 lanes of a wave, as a scalar.
+__device__ __forceinline__ int wave_total(int v) { return __builtin_amdgcn_readlane(wave_prefix(v), 63); }
 
 // Largest over the 64 lanes of a wave, as a scalar.
 __device__ __forceinline__ float wave_largest(float v)
@@ -91,15 +93,15 @@ __device__ __forceinline__ float wave_largest(float v)
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// One wave: chunks [ca, cb) of a row (partial outputs, maxima and sums from `slot` on) joined into row t of head hd.
-template <int D>
-__device__ __forceinline__ void join_chunks(const AttnArgs &a, int64_t slot, int ca, int cb, int64_t t, int hd)
+// One wave: parts [ca, cb) of a row (fp32 outputs, maxima and sums at slot(c)) joined into row t of head hd.
+template <int D, class Slot>
+__device__ __forceinline__ void join_parts(const AttnArgs &a, int ca, int cb, Slot slot, int64_t t, int hd)
 {
     constexpr int VPT = D / 64, AHEAD = 8;
     const int lane = threadIdx.x & 63;
     float mx = ATTN_LOWEST, sum = 0.f, acc[VPT];
     for (int c = ca + lane; c < cb; c += 64)
-        mx = fmaxf(mx, a.part_ml[2 * (slot + c)]);
+        mx = fmaxf(mx, a.part_ml[2 * slot(c)]);
     mx = wave_largest(mx);
 #pragma unroll
     for (int e = 0; e < VPT; ++e)
@@ -107,7 +109,7 @@ __device__ __forceinline__ void join_chunks(const AttnArgs &a, int64_t slot, int
     for (int c0 = ca; c0 < cb; c0 += 64) {
         float f = 0.f;                          // this lane's chunk
         if (c0 + lane < cb) {
-            const f32x2 ml = *(const f32x2 *)(a.part_ml + 2 * (slot + c0 + lane));
+            const f32x2 ml = *(const f32x2 *)(a.part_ml + 2 * slot(c0 + lane));
             f = __builtin_amdgcn_exp2f(ml[0] - mx);
             sum += f * ml[1];
         }
@@ -118,7 +120,7 @@ __device__ __forceinline__ void join_chunks(const AttnArgs &a, int64_t slot, int
             for (int j = 0; j < AHEAD; ++j)
 #pragma unroll
                 for (int e = 0; e < VPT; ++e)
-                    x[j][e] = a.part_o[(slot + c0 + min(i + j, n - 1)) * D + lane * VPT + e];
+                    x[j][e] = a.part_o[slot(c0 + min(i + j, n - 1)) * D + lane * VPT + e];
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), i + j));

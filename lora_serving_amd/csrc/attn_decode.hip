@@ -1,12 +1,15 @@
 // Attention of few query rows over a paged cache (decode), and the join of split rows.
 //
 // The rows of one sequence and kv head (queries x heads of the group, up to 16 NQ) are the
-// columns of 16x16x32 MFMA tiles, so K and V are read once for all of them.  A workgroup takes
-// one (sequence, kv head, chunk of keys); its four waves take steps of 32 keys in turn, each with
-// its own running maximum, sums and accumulators, joined in LDS at the end.  K goes from memory
-// straight into the fragments; V through a wave's own piece of LDS, written by rows and read
-// transposed, so the loop has no barrier.  The next step's loads are issued while this one's
-// softmax and second product run.  Bound by HBM (or, for a short batch, by latency).
+// columns of 16x16x32 MFMA tiles, so K and V are read once for all of them.  The keys of all
+// sequences and kv heads, in units of 128, are laid end to end and cut into equal shares, one a
+// workgroup and as many as the card holds at a time: ragged batches end together, and few
+// sequences still use every CU.  A sequence and head that crosses a cut leaves fp32 parts, which
+// a second kernel joins.  A workgroup's four waves take steps of 32 keys in turn, each with its
+// own running maximum, sums and accumulators, joined in LDS at the end of a piece.  K goes from
+// memory straight into the fragments; V through a wave's own piece of LDS, written by rows and
+// read transposed, so the loop has no barrier.  The next step's loads are issued while this
+// one's softmax and second product run.  Bound by HBM (or, for a short batch, by latency).
 #include <algorithm>
 #include <type_traits>
 
@@ -15,28 +18,91 @@
 
 namespace mlora {
 
-// Chunks of a sequence: keys [lo, L) that its queries can see, cut at multiples of `chunk`.
-struct SeqChunks {
-    int q0, n, L, lo, c0, count;
+// A sequence: its queries and the units [first, first + units) of the keys [lo, L) that they see (at least one
+// unit; none if this launch does not answer the sequence).
+struct SeqUnits {
+    int q0, n, L, lo, first, units;
 };
 
-__device__ __forceinline__ SeqChunks seq_chunks(const AttnArgs &a, int b)
+__device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b)
 {
-    SeqChunks s;
+    SeqUnits s;
     s.q0 = (int)min((int64_t)max(a.cu_q[b], 0), a.T);
     s.n = (int)min((int64_t)max(a.cu_q[b + 1], 0), a.T) - s.q0;
-    s.L = (int)min((int64_t)max(a.kv_len[b], 0),
-                   min(a.max_kv, a.table_stride << a.cache.ps));
+    s.L = (int)min((int64_t)max(a.kv_len[b], 0), min(a.max_kv, a.table_stride << a.cache.ps));
     s.lo = a.window > 0 ? max(0, s.L - s.n - a.window + 1) : 0;
-    s.c0 = s.lo / a.chunk;
-    s.count = s.L > s.lo ? (s.L - 1) / a.chunk - s.c0 + 1 : 1;
+    s.first = s.lo / DECODE_UNIT;
+    const int64_t rows = (int64_t)s.n * a.group;
+    const bool mine = s.n > 0 && s.n <= a.max_q && rows >= a.min_rows && rows <= a.max_rows;
+    s.units = mine ? max(1, (s.L + DECODE_UNIT - 1) / DECODE_UNIT - s.first) : 0;
     return s;
 }
 
-__device__ __forceinline__ bool answers(const AttnArgs &a, const SeqChunks &s)
+// Units of the sequences per lane (`per` consecutive ones each): this lane's, those before it, and all (one head's).
+struct LaneUnits {
+    int per, mine, before, total;
+};
+
+__device__ __forceinline__ LaneUnits lane_units(const AttnArgs &a, int lane)
 {
-    return s.n > 0 && s.n <= a.max_q && (int64_t)s.n * a.group >= a.min_rows &&
-           (int64_t)s.n * a.group <= a.max_rows;
+    LaneUnits u;
+    u.per = (a.n_seqs + 63) / 64;
+    u.mine = 0;
+    for (int i = 0; i < u.per; ++i) {
+        const int s = lane * u.per + i;
+        if (s < a.n_seqs)
+            u.mine += seq_units(a, s).units;
+    }
+    const int upto = wave_prefix(u.mine);
+    u.before = upto - u.mine;
+    u.total = __builtin_amdgcn_readlane(upto, 63);
+    return u;
+}
+
+// `all` units (below 2^31) cut into n <= all shares, the first `more` of them one unit longer.
+struct Shares {
+    uint32_t n, each, more;
+    __device__ __forceinline__ Shares(uint32_t all, uint32_t most) : n(min(all, most)), each(0), more(0)
+    {
+        if (n) {
+            each = all / n;
+            more = all - each * n;
+        }
+    }
+    __device__ __forceinline__ uint32_t start(uint32_t w) const { return w * each + min(w, more); }
+    __device__ __forceinline__ uint32_t of(uint32_t unit) const
+    {
+        const uint32_t longer = more * (each + 1);
+        return unit < longer ? unit / (each + 1) : more + (unit - longer) / each;
+    }
+};
+
+// The (sequence, head) that holds unit `at`, and the unit's number in it.
+struct UnitPlace {
+    int b, h, f;
+    SeqUnits sq;
+};
+
+__device__ __forceinline__ UnitPlace find_unit(const AttnArgs &a, const LaneUnits &u, uint32_t at)
+{
+    UnitPlace p;
+    const uint32_t first = (uint32_t)u.before * a.hkv;
+    const uint64_t hit = ballot64(first <= at && at - first < (uint32_t)u.mine * a.hkv);
+    const int src = __ffsll((unsigned long long)hit) - 1;
+    uint32_t rest = at - (uint32_t)__builtin_amdgcn_readlane(u.before, src) * a.hkv;
+    p.b = src * u.per;
+    for (p.sq = seq_units(a, p.b); rest >= (uint32_t)p.sq.units * a.hkv; p.sq = seq_units(a, ++p.b))
+        rest -= (uint32_t)p.sq.units * a.hkv;
+    p.h = (int)(rest / (uint32_t)p.sq.units);
+    p.f = (int)rest - p.h * p.sq.units;
+    return p;
+}
+
+// Slot of a part: a share leaves at most two, one of what began before it (which = true) and one of what goes on
+// after it.
+__device__ __forceinline__ int64_t part_slot(const AttnArgs &a, int share, bool which, int row)
+{
+    return (2 * (int64_t)share + (which ? 0 : 1)) * a.max_rows + row;
 }
 
 // Swizzle of the 16-byte pieces of a V row in LDS by its key: writes of one piece over 16 keys and transposing
@@ -47,8 +113,8 @@ __device__ __forceinline__ int ad_swz(int key)
     return D == 128 ? (key & 7) << 1 | ((key >> 3) & 1) : ((key >> 1) & 3) << 1 | ((key >> 3) & 1);
 }
 
-template <int D, int NQ, bool FP8, int NW>
-__global__ __launch_bounds__(NW * 64, 2) void attn_decode_kernel(AttnArgs a)
+template <int D, int NQ, bool FP8>
+__global__ __launch_bounds__(256, decode_slots(D, NQ)) void attn_decode_kernel(AttnArgs a)
 {
     constexpr int ESZ = FP8 ? 1 : 2;
     constexpr int KS = D / 32;          // k-steps of the first product
@@ -56,26 +122,49 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_decode_kernel(AttnArgs a)
     constexpr int LD = FP8 ? D / 64 : D / 32;   // 16-byte loads per lane and 16-key block
     constexpr int OS = D + 4;           // row stride of the joined accumulators in LDS
     constexpr int VW = 32 * D;          // a wave's V rows in LDS
-    constexpr int STEP = 32 * NW;       // keys the workgroup takes at a time
+    constexpr int NW = 4, STEP = 32 * NW;       // waves; keys they take at a time
+    static_assert(STEP == DECODE_UNIT, "units are whole steps");
     __shared__ __attribute__((aligned(16))) uint16_t lds[NW * (VW > 32 * OS ? VW : 32 * OS)];
     __shared__ float ml[NW][16][2];
 
-    const int b = (int)(blockIdx.x / a.hkv), h = (int)(blockIdx.x - (unsigned)b * a.hkv);
-    const int c = blockIdx.y, wave = uniform(threadIdx.x >> 6);
-    const SeqChunks sq = seq_chunks(a, b);
+    const int wave = uniform(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-    const int rows = sq.n * a.group, L = sq.L;
-    const int k0 = max((sq.c0 + c) * a.chunk, sq.lo & ~31), k1 = min(L, (sq.c0 + c + 1) * a.chunk);
-    const int32_t *__restrict__ table = a.table + (int64_t)b * a.table_stride;
     const int ps = a.cache.ps, pm = (1 << ps) - 1;
     uint16_t *vl = lds + wave * VW;
+
+    // this workgroup's share: `left` units from unit f of (sequence b, head h) on
+    UnitPlace at;
+    int left;
+    if (a.part_o == nullptr) {          // one workgroup a sequence and head
+        at.b = (int)(blockIdx.x / a.hkv);
+        at.h = (int)(blockIdx.x - (unsigned)at.b * a.hkv);
+        at.f = 0;
+        at.sq = seq_units(a, at.b);
+        left = at.sq.units;
+    } else {
+        const LaneUnits u = lane_units(a, lane);
+        const Shares cut((uint32_t)u.total * a.hkv, gridDim.x);
+        if (blockIdx.x >= cut.n)
+            return;
+        const uint32_t u0 = cut.start(blockIdx.x);
+        left = (int)(cut.start(blockIdx.x + 1) - u0);
+        at = find_unit(a, u, u0);
+    }
+    int b = at.b, h = at.h, f = at.f;
+    SeqUnits sq = at.sq;
+    const float cs = a.scale * ATTN_LOG2E;
+    const int last = (int)a.table_stride - 1;
+
+  for (; left > 0;) {
+    const int end = min(sq.units, f + left);
+    const int rows = sq.n * a.group, L = sq.L;
+    const int k0 = max((sq.first + f) * DECODE_UNIT, sq.lo & ~31), k1 = min(L, (sq.first + end) * DECODE_UNIT);
+    const int32_t *__restrict__ table = a.table + (int64_t)b * a.table_stride;
 
     u32x4 kr[2][LD], vr[2][LD];
     f32x4 ks[2], vs[2];
     int pg[2];
-    // pages of the two 16-key blocks of the step at kb (what a table holds past the end is read as some page,
-    // whose keys are masked: so the first lookup need not wait for the length)
-    const int last = (int)a.table_stride - 1;
+    // pages of the two 16-key blocks of the step at kb (past the end: some page, whose keys are masked)
     auto lookup = [&](int kb) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -100,17 +189,9 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_decode_kernel(AttnArgs a)
             }
         }
     };
-    int kb = c * a.chunk + 32 * wave;
-    if (a.table_stride > 0)
-        lookup(kb);
-    if (!answers(a, sq) || c >= sq.count)
-        return;
-    if (k0 != c * a.chunk) {            // a window hides the first chunks
-        kb = k0 + 32 * wave;
-        if (kb < k1)
-            lookup(kb);
-    }
+    int kb = k0 + 32 * wave;
     if (kb < k1) {
+        lookup(kb);
         load(kb);
         if (kb + STEP < k1)
             lookup(kb + STEP);
@@ -128,8 +209,6 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_decode_kernel(AttnArgs a)
         for (int s = 0; s < KS; ++s)   // e4m3 K comes 16 values a lane: two k-steps side by side
             qf[j][s] = *(const u32x4 *)(qr + (FP8 ? 64 * (s >> 1) + 16 * g + 8 * (s & 1) : 32 * s + 8 * g));
     }
-    const float cs = a.scale * ATTN_LOG2E;
-
     f32x4 o[NQ][DB];
     float m[NQ], l[NQ];
 #pragma unroll
@@ -366,7 +445,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_decode_kernel(AttnArgs a)
                 }
             }
             const int i = row / a.group, hd = h * a.group + row - i * a.group;
-            if (sq.count == 1) {
+            if (f == 0 && end == sq.units) {
                 const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
                 uint16_t *dst = a.out + (sq.q0 + i) * a.out_stride + (int64_t)hd * D + part * VPT;
 #pragma unroll
@@ -379,7 +458,7 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_decode_kernel(AttnArgs a)
                     a.lse[(int64_t)(sq.q0 + i) * a.hq + hd] =
                         sum == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
             } else {
-                const int64_t slot = (((int64_t)b * a.hkv + h) * a.max_rows + row) * a.n_chunks + c;
+                const int64_t slot = part_slot(a, blockIdx.x, f > 0, row);
                 float *dst = a.part_o + slot * D + part * VPT;
 #pragma unroll
                 for (int e = 0; e < VPT; e += 4)
@@ -389,26 +468,46 @@ __global__ __launch_bounds__(NW * 64, 2) void attn_decode_kernel(AttnArgs a)
             }
         }
     }
+    // the next head or sequence
+    left -= end - f;
+    if (left <= 0)
+        break;
+    f = 0;
+    if (++h == a.hkv) {
+        h = 0;
+        do
+            sq = seq_units(a, ++b);
+        while (sq.units == 0);
+    }
+    __syncthreads();
+  }
 }
 
-// One wave a row: the row's chunks joined.  Rows of one chunk were written whole.  Slots are numbered by
-// (sequence, kv head, row).
+// The join, a workgroup a cut between shares: the first cut within a sequence and head joins its parts, one wave a row.
 template <int D>
-__global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs a)
+__global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs a, int shares)
 {
-    const int b = (int)(blockIdx.x / a.hkv), h = (int)(blockIdx.x - (unsigned)b * a.hkv);
-    const SeqChunks sq = seq_chunks(a, b);
-    const int row = (int)blockIdx.y * 4 + (threadIdx.x >> 6);
-    if (!answers(a, sq) || sq.count <= 1 || row >= sq.n * a.group)
+    const int lane = threadIdx.x & 63, w1 = blockIdx.x + 1;
+    const LaneUnits u = lane_units(a, lane);
+    const Shares cut((uint32_t)u.total * a.hkv, (uint32_t)shares);
+    if ((uint32_t)w1 >= cut.n)
         return;
-    const int i = row / a.group, hd = h * a.group + row - i * a.group;
-    join_chunks<D>(a, (((int64_t)b * a.hkv + h) * a.max_rows + row) * a.n_chunks, 0, sq.count, sq.q0 + i, hd);
+    const uint32_t u1 = cut.start(w1);
+    const UnitPlace at = find_unit(a, u, u1);
+    const int w0 = w1 - 1;
+    if (at.f == 0 || cut.start(w0) > u1 - at.f)     // nothing is cut here, or an earlier cut joins it
+        return;
+    const int end = (int)cut.of(u1 - at.f + at.sq.units - 1) + 1, rows = at.sq.n * a.group;
+    for (int row = threadIdx.x >> 6; row < rows; row += 4) {
+        const int i = row / a.group, hd = at.h * a.group + row - i * a.group;
+        join_parts<D>(a, w0, end, [&](int w) { return part_slot(a, w, w > w0, row); }, at.sq.q0 + i, hd);
+    }
 }
 
-hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int waves, hipStream_t stream)
+hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream)
 {
-    const dim3 grid((unsigned)(a.n_seqs * (int64_t)a.hkv), (unsigned)a.n_chunks);
-#define DEC(D, NQ, F) (waves == 8 ? attn_decode_kernel<D, 1, F, 8><<<grid, dim3(512), 0, stream>>>(a) : attn_decode_kernel<D, NQ, F, 4><<<grid, dim3(256), 0, stream>>>(a))
+    const dim3 grid((unsigned)shares);
+#define DEC(D, NQ, F) attn_decode_kernel<D, NQ, F><<<grid, dim3(256), 0, stream>>>(a)
 #define DEC_F(D, NQ) (a.cache.fp8 ? DEC(D, NQ, true) : DEC(D, NQ, false))
 #define DEC_Q(D) (nq == 1 ? DEC_F(D, 1) : DEC_F(D, 2))
     head_dim == 64 ? DEC_Q(64) : DEC_Q(128);
@@ -418,13 +517,15 @@ hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int waves
     return hipGetLastError();
 }
 
-hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, hipStream_t stream)
+hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream)
 {
-    const dim3 grid((unsigned)(a.n_seqs * (int64_t)a.hkv), (unsigned)((a.max_rows + 3) / 4));
+    if (shares < 2)
+        return hipSuccess;
+    const dim3 grid((unsigned)(shares - 1));
     if (head_dim == 64)
-        attn_combine_kernel<64><<<grid, dim3(256), 0, stream>>>(a);
+        attn_combine_kernel<64><<<grid, dim3(256), 0, stream>>>(a, shares);
     else
-        attn_combine_kernel<128><<<grid, dim3(256), 0, stream>>>(a);
+        attn_combine_kernel<128><<<grid, dim3(256), 0, stream>>>(a, shares);
     return hipGetLastError();
 }
 

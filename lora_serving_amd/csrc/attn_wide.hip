@@ -615,7 +615,7 @@ __global__ __launch_bounds__(256) void attn_wide_combine_kernel(AttnArgs a)
     const int pos = L - n + t - q0;
     const int lo = a.window > 0 ? max(0, pos - a.window + 1) : 0, hi = a.causal ? min(L, pos + 1) : L;
     const int ca = lo / a.chunk, cb = hi > lo ? (hi - 1) / a.chunk + 1 : ca;
-    join_chunks<D>(a, th * a.n_chunks, ca, cb, t, hd);
+    join_parts<D>(a, ca, cb, [&](int c) { return th * a.n_chunks + c; }, t, hd);
 }
 
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream)

@@ -210,7 +210,7 @@ def check(got, ref, mag, big):
     scaling to a power of two), exponentials to 2^-21."""
     rel = 2 * 2.0 ** -23 * (big[..., None] + 16) * 4
     tol = (BF + rel) * mag + BF * ref.abs() + BF * BF * mag + 1e-30
-    bad = (got.cpu().double() - ref).abs() > tol
+    bad = ~((got.cpu().double() - ref).abs() <= tol)        # (a NaN is bad)
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()}, worst " \
                           f"{float(((got.cpu().double() - ref).abs() / tol).max()):.2f} of the tolerance"
 
