@@ -38,20 +38,23 @@ __device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b)
     return s;
 }
 
-// Units of the sequences per lane (`per` consecutive ones each): this lane's, those before it, and all (one head's).
+// Units of the sequences per lane (`per` consecutive ones each): this lane's, those before it, and all (one head's);
+// and the lane's last sequence.
 struct LaneUnits {
     int per, mine, before, total;
+    SeqUnits own;
 };
 
 __device__ __forceinline__ LaneUnits lane_units(const AttnArgs &a, int lane)
 {
-    LaneUnits u;
+    LaneUnits u{};
     u.per = (a.n_seqs + 63) / 64;
-    u.mine = 0;
     for (int i = 0; i < u.per; ++i) {
         const int s = lane * u.per + i;
-        if (s < a.n_seqs)
-            u.mine += seq_units(a, s).units;
+        if (s < a.n_seqs) {
+            u.own = seq_units(a, s);
+            u.mine += u.own.units;
+        }
     }
     const int upto = wave_prefix(u.mine);
     u.before = upto - u.mine;
@@ -91,7 +94,17 @@ __device__ __forceinline__ UnitPlace find_unit(const AttnArgs &a, const LaneUnit
     const int src = __ffsll((unsigned long long)hit) - 1;
     uint32_t rest = at - (uint32_t)__builtin_amdgcn_readlane(u.before, src) * a.hkv;
     p.b = src * u.per;
-    for (p.sq = seq_units(a, p.b); rest >= (uint32_t)p.sq.units * a.hkv; p.sq = seq_units(a, ++p.b))
+    if (u.per == 1) {           // (no second trip to memory)
+        p.sq.q0 = __builtin_amdgcn_readlane(u.own.q0, src);
+        p.sq.n = __builtin_amdgcn_readlane(u.own.n, src);
+        p.sq.L = __builtin_amdgcn_readlane(u.own.L, src);
+        p.sq.lo = __builtin_amdgcn_readlane(u.own.lo, src);
+        p.sq.first = __builtin_amdgcn_readlane(u.own.first, src);
+        p.sq.units = __builtin_amdgcn_readlane(u.own.units, src);
+    } else {
+        p.sq = seq_units(a, p.b);
+    }
+    for (; rest >= (uint32_t)p.sq.units * a.hkv; p.sq = seq_units(a, ++p.b))
         rest -= (uint32_t)p.sq.units * a.hkv;
     p.h = (int)(rest / (uint32_t)p.sq.units);
     p.f = (int)rest - p.h * p.sq.units;
