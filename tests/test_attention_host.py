@@ -99,6 +99,11 @@ def test_attention_refusals(m):
     assert call_attention(m, hq=5) == m.MLORA_ERR_SHAPE
     assert call_attention(m, d=80) == m.MLORA_ERR_UNSUPPORTED
     assert call_attention(m, Tq=1 << 30, Tk=1 << 30) == m.MLORA_ERR_UNSUPPORTED
+    assert call_attention(m, Tk=1 << 30, cu_k=PTR) == m.MLORA_ERR_UNSUPPORTED        # positions within 32 bits
+    assert call_attention(m, ks=1 << 24) == m.MLORA_ERR_UNSUPPORTED                  # offsets within a tile too
+    assert call_attention(m, vs=1 << 24) == m.MLORA_ERR_UNSUPPORTED
+    for scale in (-0.5, math.inf, -math.inf):                                        # the largest score leads
+        assert call_attention(m, scale=scale) == m.MLORA_ERR_ARG
 
 
 def call_paged(m, c=None, q=PTR, T=4, hq=4, table=PTR, stride=4, n=4, cu=PTR, lens=PTR, max_q=1, max_kv=64, window=0,
@@ -122,6 +127,9 @@ def test_paged_refusals(m):
     assert call_paged(m, qs=8) == m.MLORA_ERR_SHAPE
     assert call_paged(m, max_kv=1 << 40) == m.MLORA_ERR_UNSUPPORTED
     assert call_paged(m, c=cache(m, dtype=1, ks=PTR)) == m.MLORA_ERR_ARG
+    for scale in (-0.5, math.inf, math.nan):
+        assert call_paged(m, scale=scale) == m.MLORA_ERR_ARG
+    assert call_paged(m, n=1 << 20, max_kv=(1 << 30) - 1) == m.MLORA_ERR_UNSUPPORTED   # units of all heads: 32 bits
     # a long batch is split over keys and needs room for the parts
     need = m._lib.mlora_paged_workspace_size(4, 4, 4, 2, 64, 1, 8192)
     assert need > 4 * 4 * 64 * 4

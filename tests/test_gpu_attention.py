@@ -405,6 +405,107 @@ def test_unseen_values_have_no_effect(m, d, bad):
     assert torch.equal(ap[~seen_p], bp[~seen_p]) and bp[seen_p].isnan().any(-1).all()
 
 
+LONG_PROMPTS = [
+    # lens of queries, lens of keys (None: the same), hq, hkv, d, causal, window
+    ([700], None, 4, 2, 128, True, 0),                # several tiles seen in full, one and two rows blocks at the edge
+    ([390], None, 3, 3, 64, True, 0),
+    ([33], [1000], 8, 2, 128, False, 0),
+    ([300], None, 2, 1, 128, True, 150),              # full tiles between two edges
+    ([130], [600], 2, 2, 64, False, 400),
+    ([4] * 70 + [150], None, 2, 1, 64, True, 0),      # more than 64 sequences
+    ([1, 260, 3], [5, 900, 2], 2, 1, 128, True, 2 ** 31 - 1),   # a window wider than any sequence
+]
+
+
+@pytest.mark.parametrize("case", LONG_PROMPTS, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[:60])
+def test_long_prompts(m, case):
+    test_prompts(m, case)
+
+
+LONG_PAGED = [
+    # (queries, keys) of the sequences, hq, hkv, d, page, fp8, causal, window
+    ([(1, 1 + 61 * i % 1500) for i in range(70)], 2, 1, 64, 16, False, True, 0),       # more than 64 sequences
+    ([(1, 40 * i) for i in range(130)], 2, 2, 64, 32, True, True, 0),
+    ([(1, 1200), (0, 0), (3, 0), (1, 5000), (2, 1), (4, 4)], 8, 2, 128, 16, False, True, 0),
+    ([(1, 3000), (1, 1)], 8, 2, 128, 64, True, True, 2 ** 31 - 1),
+    ([(3, 2), (1, 700)], 4, 2, 128, 16, False, True, 2 ** 31 - 1),                     # fewer keys than queries
+    ([(7, 1500), (8, 900)], 8, 2, 128, 16, False, True, 0),                           # 32 rows, split
+    ([(6, 1000)], 4, 1, 128, 32, True, False, 300),
+    ([(150, 1300), (1, 900), (1, 30)], 4, 2, 128, 16, False, True, 0),                # chunks split too
+    ([(140, 900)], 6, 2, 128, 32, True, True, 260),
+    ([(129, 700)], 2, 2, 64, 64, True, False, 0),
+    ([(1, 2000)] * 3, 48, 1, 64, 16, False, True, 0),                                  # a group of 48
+]
+
+
+@pytest.mark.parametrize("poison", [False, True], ids=["", "poison"])
+@pytest.mark.parametrize("case", LONG_PAGED, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[:60])
+def test_long_paged(m, case, poison):
+    test_paged(m, case, poison)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n,window", [(1, 0), (1, 100), (3, 0), (5, 90), (60, 0), (60, 130)])
+def test_unseen_values_in_pages(m, n, window, d, fp8):
+    """NaN in K, V and the scales of single keys reaches only the queries that see them, split or not."""
+    g = gen(n + d + window)
+    hq, hkv, page, dev, L = 4, 2, 16, "cuda", 900
+    c, table, _ = paged_batch(m, g, [(n, L)], hkv, d, page, fp8)
+    q = randn(g, n, hq, d).to(dev)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    ws = m.paged_workspace(n, 1, hq, hkv, d, n, L)
+    pos = torch.arange(L - n, L)
+    for key in (0, 100, L - window - 2, L - window, L - 33, L - 3, L - 2, L - 1):
+        if not 0 <= key < L:
+            continue
+        outs = []
+        old = [t.clone() for t in (c.k, c.v) + ((c.k_scale, c.v_scale) if fp8 else ())]
+        for poison in (False, True):
+            if poison:
+                pg, at = int(table[0, key // page]), key % page
+                for t in (c.k, c.v):
+                    if fp8:
+                        t.view(torch.uint8)[pg, :, at, 7] = 0x7f
+                    else:
+                        t[pg, :, at, 7] = math.nan
+                if fp8:
+                    c.k_scale[pg, :, at] = math.nan
+                    c.v_scale[pg, :, at] = math.inf
+            o = torch.empty(n, hq, d, device=dev, dtype=torch.bfloat16)
+            m.mlora_paged_attention(q, c, table.to(dev), ints(0, n), ints(L), o, n, L, window=window, ws=ws)
+            torch.cuda.synchronize()
+            outs.append(o.cpu())
+        for t, v in zip((c.k, c.v) + ((c.k_scale, c.v_scale) if fp8 else ()), old):
+            t.copy_(v)
+        seen = (pos >= key) & ((pos - window < key) if window else torch.ones(n, dtype=torch.bool))
+        assert torch.equal(outs[0][~seen], outs[1][~seen])
+        assert outs[1][seen].isnan().any(-1).all()
+
+
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("d", [64, 128])
+def test_unseen_values_in_long_prompts(m, d, window):
+    """The same where a row block has tiles that it sees in full."""
+    g = gen(d + window)
+    n, hq, hkv, dev = 600, 2, 1, "cuda"
+    q, k, v = randn(g, n, hq, d).to(dev), randn(g, n, hkv, d).to(dev), randn(g, n, hkv, d).to(dev)
+    cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+    good = torch.empty(n, hq, d, device=dev, dtype=torch.bfloat16)
+    m.mlora_attention(q, k, v, cu, good, window=window)
+    pos = torch.arange(n)
+    for key in (0, 63, 64, 255, 300, 511, 599):
+        kk, vv = k.clone(), v.clone()
+        vv[key, 0, 11] = math.inf
+        kk[key, 0, 2] = math.nan
+        out = torch.empty_like(good)
+        m.mlora_attention(q, kk, vv, cu, out, window=window)
+        torch.cuda.synchronize()
+        seen = (pos >= key) & ((pos - window < key) if window else torch.ones(n, dtype=torch.bool))
+        assert torch.equal(out.cpu()[~seen], good.cpu()[~seen])
+        assert out.cpu()[seen].isnan().any(-1).all()
+
+
 def test_large_scores(m):
     """Scores of hundreds: the maximum is taken off before the exponential."""
     g = gen(3)
