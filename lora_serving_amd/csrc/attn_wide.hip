@@ -20,13 +20,13 @@ constexpr int AW_BN = 64;      // keys a tile
 enum { AW_ROWS = 0, AW_PAGES = 1, AW_PAGES_E4M3 = 2 };
 
 // One 16-byte copy a lane from global memory (a scalar base and a byte offset of the lane) straight into
-// LDS: 64 lanes fill 1 KB at lds.  In asm, so that the compiler does not drain the copies in flight
-// before each LDS read (it cannot tell the buffers apart); every copy is waited for by hand.
-__device__ __forceinline__ void aw_dma(const void *base, uint32_t off, uint16_t *lds)
+// LDS: 64 lanes fill 1 KB at byte `to` + `more` of it.  In asm, so that the compiler does not drain the
+// copies in flight before each LDS read (it cannot tell the buffers apart); every copy is waited for by
+// hand.  (Nothing else here uses m0.)
+__device__ __forceinline__ void aw_dma(const void *base, uint32_t off, uint32_t to, int more)
 {
-    const uint32_t to = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void *)lds;
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                 :: "v"(off), "s"(base), "s"(uniform((int)to)) : "memory");    // (nothing else here uses m0)
+    asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :: "v"(off), "s"(base), "s"(to), "i"(more) : "memory", "scc");
 }
 
 // Swizzle of the 16-byte pieces of a row by its key, a bijection for reads of one piece over 16 keys
@@ -108,8 +108,8 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, W
     return false;
 }
 
-template <int D, int SRC>
-__global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
+template <int D, int SRC, int KG>
+__global__ __launch_bounds__(KG * 256, 2) void attn_wide_kernel(AttnArgs a)
 {
     constexpr bool FP8 = SRC == AW_PAGES_E4M3;
     constexpr int NW = 4, BM = WIDE_ROWS, BN = AW_BN;
@@ -120,11 +120,14 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
     constexpr int RPI = 64 / LPR;           // rows a copy instruction
     constexpr int IPW = BN / RPI / NW;      // copies a wave, for K and for V each
     constexpr int TILE = BN * D;
-    __shared__ __attribute__((aligned(4 * TILE))) uint16_t kl[2 * TILE];
-    __shared__ __attribute__((aligned(4 * TILE))) uint16_t vl[2 * TILE];
+    constexpr int GROUP = 4 * TILE;         // two tiles of K, two of V
+    __shared__ __attribute__((aligned(16))) uint16_t lds[KG * GROUP];
+    __shared__ float joint[KG > 1 ? 4 : 1][KG > 1 ? 64 : 1][2];
     __shared__ __attribute__((aligned(16))) float sc[FP8 ? 4 : 1][2][FP8 ? BN : 4];
 
-    const int wave = uniform(threadIdx.x >> 6);
+    static_assert(KG == 1 || !FP8, "one set of scales");
+    const int kg = KG > 1 ? uniform(threadIdx.x >> 8) : 0, wave = uniform((threadIdx.x >> 6) & 3);
+    uint16_t *const kl = lds + kg * GROUP, *const vl = kl + 2 * TILE;
     const int lane = threadIdx.x & 63, col = lane & 31, hh = lane >> 5;
     const int item = (int)(blockIdx.x / a.hkv), h = (int)(blockIdx.x - (unsigned)item * a.hkv);
 
@@ -147,7 +150,9 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
         return;
     const int wrow = rb * BM + wave * 32;
     const int wmin = first_key(wrow), wmax = wrow < rows ? end_key(wrow + 31) : 0;
-    const int t0 = kmin / BN, t1 = kmax > kmin ? (kmax + BN - 1) / BN : t0;
+    // the tiles, or this half's of them
+    const int ta = kmin / BN, tb = kmax > kmin ? (kmax + BN - 1) / BN : ta, tm = KG > 1 ? ta + (tb - ta + 1) / 2 : tb;
+    const int t0 = kg ? tm : ta, t1 = kg ? tb : tm;
     // tiles [f0, f1): every row of the workgroup sees every key
     const int f0 = max(t0, (first_key(rb * BM + BM - 1) + BN - 1) / BN);
     const int f1 = max(min(t1, min(kmax, end_key(rb * BM)) / BN), f0);
@@ -191,18 +196,19 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
         if (SRC != AW_ROWS)
             pgk = clamp_page(table[min(t * BN + w16, L - 1) >> ps], a.cache.n_pages);
     };
+    // (to: where the tile goes, bytes of LDS, this wave's rows)
     auto copy = [&](int t, const uint16_t *&rows, int64_t stride, const uint8_t *pages, int pg, const uint32_t (&off)[IPW],
-                    uint16_t *lds, u32x4 (&regs)[IPW]) {
+                    uint32_t to, u32x4 (&regs)[IPW]) __attribute__((always_inline)) {
         if (SRC == AW_ROWS) {
             if (t * BN + BN <= L) {
 #pragma unroll
                 for (int i = 0; i < IPW; ++i)
-                    aw_dma(rows, off[i], lds + (w16 + RPI * i) * D);
+                    aw_dma(rows, off[i], to, RPI * i * D * 2);
             } else {
 #pragma unroll
                 for (int i = 0; i < IPW; ++i)
                     aw_dma(rows, (uint32_t)min(w16 + RPI * i + crow, L - 1 - t * BN) * (uint32_t)(2 * stride) + piece[i],
-                           lds + (w16 + RPI * i) * D);
+                           to, RPI * i * D * 2);
             }
             rows += BN * stride;
         } else {
@@ -211,28 +217,35 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
 #pragma unroll
             for (int i = 0; i < IPW; ++i)
                 if (!FP8)
-                    aw_dma(base, off[i], lds + (w16 + RPI * i) * D);
+                    aw_dma(base, off[i], to, RPI * i * D * 2);
                 else
                     regs[i] = *(const u32x4 *)(base + off[i]);
         }
     };
-    // K of tile t + 1 and V of tile t on their way (pgk: the page of tile t + 1, pgv: of tile t)
-    auto issue = [&](int t) {
-        const int nb = (t + 1) & 1;
+    const uint32_t to_k = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint16_t *)lds +
+                          (uint32_t)(kg * GROUP + w16 * D) * 2, to_v = to_k + 4 * TILE;
+    // K of tile t + 1 on its way (pgk: its page), and V of tile t (pgv: its page); K first
+    auto issue_k = [&](int t) __attribute__((always_inline)) {
         if (t + 1 < t1)
-            copy(t + 1, kp, a.k_stride, a.cache.k, pgk, off_k, kl + nb * TILE, kr);
-        if (t >= t0)
-            copy(t, vp, a.v_stride, a.cache.v, pgv, off_v, vl + (nb ^ 1) * TILE, vr);
+            copy(t + 1, kp, a.k_stride, a.cache.k, pgk, off_k, to_k + ((t + 1) & 1) * (2 * TILE), kr);
         if (FP8 && threadIdx.x < 2 * BN) {      // scales of K and of V, both of tile t + 1
             const int key = min((t + 1) * BN + (int)(threadIdx.x & (BN - 1)), L - 1);
             const int page = clamp_page(table[key >> ps], a.cache.n_pages);
             scr = (threadIdx.x < BN ? a.cache.k_scale : a.cache.v_scale)[(((int64_t)page * a.cache.hkv + h) << ps) + (key & pm)];
         }
+    };
+    auto issue_v = [&](int t) __attribute__((always_inline)) {
+        if (t >= t0)
+            copy(t, vp, a.v_stride, a.cache.v, pgv, off_v, to_v + (t & 1) * (2 * TILE), vr);
         if (SRC != AW_ROWS) {
             pgv = pgk;
             if (t + 2 < t1)
                 lookup(t + 2);
         }
+    };
+    auto issue = [&](int t) __attribute__((always_inline)) {
+        issue_k(t);
+        issue_v(t);
     };
     // what issue(t) started has arrived in LDS (this wave's part; a barrier makes it the workgroup's)
     auto land = [&](int t) {
@@ -276,9 +289,9 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
         zero[i] = 0.f;
     u32x4 pf[4];
     // S^T: rows = keys 32 u + 8 (i / 4) + 4 hh + i % 4, column = query
-    const uint32_t klane = col * D * 2 + 16 * (hh ^ aw_swz<D>(col));
+    const uint32_t klane = kg * GROUP * 2 + col * D * 2 + 16 * (hh ^ aw_swz<D>(col));
     auto kfrag = [&](uint32_t at, int s, int u) {
-        return *(const u32x4 *)((const uint8_t *)kl + (at ^ (32 * s)) + 64 * u * D);
+        return *(const u32x4 *)((const uint8_t *)lds + (at ^ (32 * s)) + 64 * u * D);
     };
     auto scores = [&](int t, f32x16 (&st)[2]) {
         const uint32_t at = tile_at(klane, t);
@@ -289,16 +302,19 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
                 st[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(kfrag(at, s, u)), as_bf16x8(qf[s]),
                                                                 s ? st[u] : zero, 0, 0, 0);
     };
-    // e4m3: the keys' scales
-    auto scaled = [&](int t, int u, f32x16 (&st)[2]) {
-        if (FP8)
+    // e4m3: the keys' scales (of 4 scores)
+    auto scaled = [&](int t, int u, int i, f32x16 (&st)[2]) {
+        if (FP8) {
+            const f32x4 k4 = *(const f32x4 *)(&sc[FP8 ? t & 3 : 0][0][FP8 ? 32 * u + 8 * i + 4 * hh : 0]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const f32x4 k4 = *(const f32x4 *)(&sc[FP8 ? t & 3 : 0][0][FP8 ? 32 * u + 8 * i + 4 * hh : 0]);
+            for (int e = 0; e < 4; ++e)
+                st[u][4 * i + e] *= k4[e];
+        }
+    };
+    auto all_scaled = [&](int t, f32x16 (&st)[2]) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    st[u][4 * i + e] *= k4[e];
-            }
+        for (int i = 0; i < 8; ++i)
+            scaled(t, i >> 2, i & 3, st);
     };
     auto hide = [&](int t, f32x16 (&st)[2]) {
 #pragma unroll
@@ -310,9 +326,9 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
                 st[u][i] = see ? st[u][i] : -INFINITY;
             }
     };
-    auto largest = [&](const f32x16 &s, float mx) {
+    auto largest = [&](const f32x16 &s, int i0, int i1, float mx) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = i0; i < i1; ++i)
             mx = fmaxf(mx, s[i]);
         return mx;
     };
@@ -330,32 +346,37 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
                 o[d] *= f;
         }
     };
-    // 4 scores to probabilities (i: 0 .. 7), P^T rounded to bf16 (half a step: 2^-8 relative) for the matrix cores;
+    // 2 scores to probabilities (k: 0 .. 15), P^T rounded to bf16 (half a step: 2^-8 relative) for the matrix cores;
     // the sum keeps fp32
-    auto powers = [&](int t, int i, const f32x16 (&st)[2], auto edge) {
-        const int u = i >> 2, j = i & 3;
-        f32x4 p, v4;
+    auto powers = [&](int t, int k, const f32x16 (&st)[2], auto edge) {
+        const int u = k >> 3, i = 2 * (k & 7);
+        float p[2];
+        f32x2 v2;
         if (FP8)
-            v4 = *(const f32x4 *)(&sc[FP8 ? t & 3 : 0][1][FP8 ? 32 * u + 8 * j + 4 * hh : 0]);
+            v2 = *(const f32x2 *)(&sc[FP8 ? t & 3 : 0][1][FP8 ? 32 * u + 8 * (i >> 2) + 4 * hh + (i & 3) : 0]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float s = st[u][4 * j + e];
+        for (int e = 0; e < 2; ++e) {
+            const float s = st[u][i + e];
             const float x = __builtin_amdgcn_exp2f(fmaf(s, cs, -m));
             l += x;
             // (a masked key's scale may be anything)
-            p[e] = !FP8 ? x : edge && s == -INFINITY ? 0.f : x * v4[e];
+            p[e] = !FP8 ? x : edge && s == -INFINITY ? 0.f : x * v2[e];
         }
-        pf[i >> 1][2 * (i & 1)] = cvt_bf16x2(p[0], p[1]);
-        pf[i >> 1][2 * (i & 1) + 1] = cvt_bf16x2(p[2], p[3]);
+        pf[k >> 2][k & 3] = cvt_bf16x2(p[0], p[1]);
+    };
+    auto all_powers = [&](int t, const f32x16 (&st)[2], auto edge) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            powers(t, k, st, edge);
     };
     // O^T += V^T P^T; k index (hh, e) of step s is key 16 s + 8 (e / 4) + 4 hh + e % 4
     const int vi = lane & 15, vd = (lane >> 4) & 1, vk = 4 * hh + (vi >> 2);
-    const uint32_t vlane = vk * D * 2 + 16 * ((2 * vd + ((vi & 3) >> 1)) ^ aw_swz<D>(vk)) + 8 * (vi & 1);
+    const uint32_t vlane = kg * GROUP * 2 + vk * D * 2 + 16 * ((2 * vd + ((vi & 3) >> 1)) ^ aw_swz<D>(vk)) + 8 * (vi & 1);
     auto vfrag = [&](uint32_t at, int s, int d) {
         u32x4 f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {       // keys 16 s + 8 u + vk, values 32 d ..
-            const u32x2 w = lds_read_tr((const uint16_t *)((const uint8_t *)vl + (at ^ (64 * d + 32 * u)) + (16 * u + 32 * s) * D));
+            const u32x2 w = lds_read_tr((const uint16_t *)((const uint8_t *)(lds + 2 * TILE) + (at ^ (64 * d + 32 * u)) + (16 * u + 32 * s) * D));
             f[2 * u] = w[0];
             f[2 * u + 1] = w[1];
         }
@@ -371,10 +392,13 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
     };
     // Scores of tile t + 1 (into nx), powers of tile t (from st) and its outputs, in steps of two products: the
     // fragments are read AHEAD steps before their use, the powers of a step's keys come before it, and the next
-    // tile's largest score after its last; the fences keep the compiler to that order.
-    auto body = [&](int t, const f32x16 (&st)[2], f32x16 (&nx)[2]) {
-        constexpr int N = KS + 2 * DB, AHEAD = FP8 ? 2 : 4;   // (e4m3: as the registers allow)
-        issue(t + 1);
+    // tile's largest score after its last; the fences keep the compiler to that order.  Copies of rows are issued
+    // between the first products (10000 tokens of one head: 115 us against 123), those of pages, whose
+    // addresses take longer, before them (2048 tokens over 8192: 232 us against 239).
+    auto body = [&](int t, const f32x16 (&st)[2], f32x16 (&nx)[2]) __attribute__((always_inline)) {
+        constexpr int N = KS + 2 * DB, AHEAD = FP8 ? 2 : 4;     // (e4m3: as the registers allow)
+        if (SRC != AW_ROWS)
+            issue(t + 1);
         const uint32_t ka = tile_at(klane, t + 1), va = tile_at(vlane, t);
         u32x4 f[AHEAD][2];
         auto read = [&](int i) {
@@ -382,6 +406,8 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
             for (int e = 0; e < 2; ++e)
                 f[i % AHEAD][e] = i < KS ? kfrag(ka, i, e) : vfrag(va, 2 * (i - KS) / DB, 2 * (i - KS) % DB + e);
         };
+        // powers that are done after step i
+        auto done = [](int i) { return D == 128 ? (i < 8 ? (i + 1) / 2 * 2 : i < 12 ? 2 * i - 6 : 16) : i < 4 ? 2 * i + 2 : i < 6 ? 4 * i - 4 : 16; };
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
             read(i);
@@ -400,22 +426,22 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
             }
             if (i + AHEAD < N)
                 read(i + AHEAD);
-            // D = 128: powers 0 .. 3 in steps 1, 3, 5, 7, 4 .. 7 in 8 .. 11; D = 64: 0 .. 3, 4 .. 7 in 4, 4, 5, 5
-            if (D == 128 ? (i < 8 ? (i & 1) : i < 12) : i < 6) {
-                if (D == 128) {
-                    powers(t, i < 8 ? i >> 1 : i - 4, st, std::false_type());
-                } else if (i < 4) {
-                    powers(t, i, st, std::false_type());
-                } else {
-                    powers(t, 2 * i - 4, st, std::false_type());
-                    powers(t, 2 * i - 3, st, std::false_type());
-                }
-            }
+#pragma unroll
+            for (int k = i ? done(i - 1) : 0; k < done(i); ++k)
+                powers(t, k, st, std::false_type());
             if (i >= N - 2) {
-                scaled(t + 1, i - (N - 2), nx);
-                mx = largest(nx[i - (N - 2)], mx);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    scaled(t + 1, i - (N - 2), j, nx);
+                mx = largest(nx[i - (N - 2)], 0, 16, mx);
             }
             __builtin_amdgcn_sched_barrier(0);
+            if (SRC == AW_ROWS && i == 0)
+                issue_k(t + 1);
+            if (SRC == AW_ROWS && i == KS / 2)
+                issue_v(t + 1);
+            if (SRC == AW_ROWS && (i == 0 || i == KS / 2))
+                __builtin_amdgcn_sched_barrier(0);
         }
         raise(mx);
         land(t + 1);
@@ -491,13 +517,10 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
             issue(t);
         if (work) {
             scores(t, sa);
-            scaled(t, 0, sa);
-            scaled(t, 1, sa);
+            all_scaled(t, sa);
             hide(t, sa);
-            raise(largest(sa[1], largest(sa[0], -INFINITY)));
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                powers(t, i, sa, std::true_type());
+            raise(largest(sa[1], 0, 16, largest(sa[0], 0, 16, -INFINITY)));
+            all_powers(t, sa, std::true_type());
         }
         land(t);
         phase_end();
@@ -524,9 +547,8 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
         if (t > t0)
             issue(t);
         scores(t, sa);
-        scaled(t, 0, sa);
-        scaled(t, 1, sa);
-        raise(largest(sa[1], largest(sa[0], -INFINITY)));
+        all_scaled(t, sa);
+        raise(largest(sa[1], 0, 16, largest(sa[0], 0, 16, -INFINITY)));
         land(t);
         phase_end();
         for (; t + 2 < f1; t += 2) {
@@ -539,19 +561,51 @@ __global__ __launch_bounds__(256, 2) void attn_wide_kernel(AttnArgs a)
             sa[1] = sb[1];
             ++t;
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            powers(t, i, sa, std::false_type());
+        all_powers(t, sa, std::false_type());
         outputs(t);
         for (++t; t < t1; ++t)
             single(t);
     }
 
     l += __shfl_xor(l, 32, 64);
+    if (KG > 1) {
+        // a tile took one barrier; the first half has a tile more if their number is odd
+        if ((tb - ta) & 1 && kg)
+            phase_end();
+        phase_end();
+        // the second half's sums join the first's
+        f32x4 *part = (f32x4 *)(lds + GROUP) + wave * DB * 4 * 64 + lane;
+        if (kg) {
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    part[(4 * d + i) * 64] = f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+            joint[wave][KG > 1 ? lane : 0][0] = m;
+            joint[wave][KG > 1 ? lane : 0][1] = l;
+        }
+        __syncthreads();
+        if (kg)
+            return;
+        const float m1 = joint[wave][KG > 1 ? lane : 0][0], l1 = joint[wave][KG > 1 ? lane : 0][1], mx = fmaxf(m, m1);
+        const float s0 = __builtin_amdgcn_exp2f(m - mx), s1 = __builtin_amdgcn_exp2f(m1 - mx);
+        m = mx;
+        l = l * s0 + l1 * s1;
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const f32x4 x = part[(4 * d + i) * 64];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[d][4 * i + e] = o[d][4 * i + e] * s0 + x[e] * s1;
+            }
+    }
     if (a.n_chunks == 1) {
         // through the wave's own part of LDS (the tiles are done with), so that whole rows are stored
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-        phase_end();
+        if (KG == 1)
+            phase_end();
         uint16_t *part = kl + wave * 32 * D;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
@@ -626,8 +680,11 @@ hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStre
     if (items * a.hkv > 0x7fffffff)
         return hipErrorInvalidValue;
     const dim3 grid((unsigned)(items * a.hkv), (unsigned)a.n_chunks);
-#define AW(D, SRC) attn_wide_kernel<D, SRC><<<grid, dim3(256), 0, stream>>>(a)
-#define AW_S(D) (!pages ? AW(D, AW_ROWS) : a.cache.fp8 ? AW(D, AW_PAGES_E4M3) : AW(D, AW_PAGES))
+    // Whole prompts that fill at most one workgroup a CU: the tiles go to two halves of a workgroup of twice the
+    // waves, which a CU holds as well as two workgroups (pages are cut into chunks instead).
+    const bool halves = items * a.hkv <= 256;
+#define AW(D, SRC, KG) attn_wide_kernel<D, SRC, KG><<<grid, dim3(KG * 256), 0, stream>>>(a)
+#define AW_S(D) (!pages ? halves ? AW(D, AW_ROWS, 2) : AW(D, AW_ROWS, 1) : a.cache.fp8 ? AW(D, AW_PAGES_E4M3, 1) : AW(D, AW_PAGES, 1))
     head_dim == 64 ? AW_S(64) : AW_S(128);
 #undef AW_S
 #undef AW
