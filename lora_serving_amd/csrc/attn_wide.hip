@@ -539,6 +539,14 @@ __global__ __launch_bounds__(KG * 256, 2) void attn_wide_kernel(AttnArgs a)
     }
     phase_end();
     int t = t0;
+    if (wrow >= rows) {             // no rows: this wave only copies
+        for (; t < t1; ++t) {
+            if (t > t0)
+                issue(t);
+            land(t);
+            phase_end();
+        }
+    }
     const int lead = f0 < f1 ? f0 : t1;
     for (; t < lead; ++t)
         single(t);
