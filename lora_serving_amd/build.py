@@ -1,4 +1,4 @@
-"""Build libmlora.so in-tree with hipcc for gfx950 (CDNA4).
+"""Build libmlora.so in-tree with hipcc for gfx950 (CDNA4), and the Python module _marshal beside it.
 
 Every .hip and .cpp file of csrc/ is compiled to an object in parallel, then linked into
 lora_serving_amd/libmlora.so.  All device code is built with the packed-FP32 feature switched
@@ -8,9 +8,11 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmlora.so")
+MARSHAL = os.path.join(PKG, "_marshal.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -52,7 +55,25 @@ def build(jobs: int = 8) -> str:
     subprocess.run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp],
                    check=True)
     os.replace(tmp, LIB)
+    build_marshal()
     return LIB
+
+
+def build_marshal() -> str:
+    """The binding's marshalling (csrc/python/marshal.cpp): host code over torch's tensor API."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE,
+           "-isystem", "/opt/rocm/include", "-isystem", os.path.join(torch, "include"), "-isystem",
+           os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem",
+           sysconfig.get_paths()["include"], os.path.join(CSRC, "python", "marshal.cpp"), "-o", tmp,
+           "-L", PKG, "-lmlora", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"), "-lc10",
+           "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout + r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":

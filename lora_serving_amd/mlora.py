@@ -1,4 +1,5 @@
-"""ctypes binding of libmlora (include/mlora.h): argument marshalling only.
+"""Binding of libmlora (include/mlora.h) through ctypes, and for the attention step's calls through
+_marshal (csrc/python/marshal.cpp): argument marshalling only.
 
 Every function here has the name of the C entry point it calls, turns torch tensors into raw
 device pointers and passes torch's current HIP stream.  No step of the layer is computed in
@@ -171,7 +172,7 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-_raw_stream = None      # handle of the current stream (torch is loaded at the first call)
+_raw_stream = None      # handle of the current stream (set at the first call with a device)
 
 
 def _load_raw_stream():
@@ -179,20 +180,20 @@ def _load_raw_stream():
     launch); torch's own handle lookup takes 0.1 us."""
     global _raw_stream
     import torch
+    if not torch.cuda.is_initialized():         # no device tensors: the call will be refused
+        return 0
     c = torch._C
     if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
-        torch.cuda.current_stream()             # initialises the device once
         _raw_stream = lambda: c._cuda_getCurrentRawStream(c._cuda_getDevice())  # noqa: E731
     else:
         _raw_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+    return _raw_stream()
 
 
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
-    if _raw_stream is None:
-        _load_raw_stream()
-    return _raw_stream()
+    return _load_raw_stream() if _raw_stream is None else _raw_stream()
 
 
 def _need(t, dtypes, name):
@@ -415,6 +416,7 @@ class Cache:
                                   self.n_kv_heads, self.page_size, self.head_dim,
                                   MLORA_CACHE_E4M3 if e4m3 else MLORA_CACHE_BF16)
         self.ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
 
 class Rope:
@@ -429,6 +431,7 @@ class Rope:
         self.struct = mlora_rope(_ptr(self.turns), self.rot_dim, int(bool(interleaved)),
                                  float(magnitude))
         self.ref = ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
 
 def mlora_rope_turns(rot_dim: int, base: float = 10000.0, scaling: int = MLORA_ROPE_PLAIN,
@@ -448,61 +451,18 @@ def mlora_cache_bytes(n_pages: int, n_kv_heads: int, page_size: int, head_dim: i
     return int(_lib.mlora_cache_bytes(n_pages, n_kv_heads, page_size, head_dim, dtype))
 
 
-_bf16_type = _i32_type = _f32_type = None
+class _Calls:
+    """csrc/python/marshal.cpp, loaded at the first call (it is linked against torch)."""
+
+    def __getattr__(self, name):
+        global _calls
+        import torch  # noqa: F401
+        from lora_serving_amd import _marshal
+        _calls = _marshal
+        return getattr(_marshal, name)
 
 
-def _load_types():
-    global _bf16_type, _i32_type, _f32_type
-    import torch
-    _bf16_type, _i32_type, _f32_type = torch.bfloat16, torch.int32, torch.float32
-
-
-def _rows(t, name, shape=None):
-    """Row stride of a bf16 [T][heads][head_dim] device tensor whose rows may lie apart."""
-    if _bf16_type is None:
-        _load_types()
-    if t is None or not t.is_cuda:
-        raise ValueError(f"{name} must be a device tensor")
-    if t.dtype is not _bf16_type or t.dim() != 3:
-        raise ValueError(f"{name} must be bf16 [T][heads][head_dim]")
-    n, h, d = t.shape
-    if shape is not None and (n, h, d) != tuple(shape):
-        raise ValueError(f"{name} has shape {(n, h, d)}, expected {tuple(shape)}")
-    sn, sh, sd = t.stride()
-    if n > 0 and (sd != 1 or (h > 1 and sh != d)):
-        raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return sn if n > 1 else h * d
-
-
-def _ints(t, n, name):
-    if _i32_type is None:
-        _load_types()
-    if t is None or t.dtype is not _i32_type or not t.is_cuda or not t.is_contiguous():
-        _need(t, (_i32_type,), name)
-    if t.numel() != n:
-        raise ValueError(f"{name} has {t.numel()} values, expected {n}")
-    return t.data_ptr()
-
-
-def _dense(t, shape, name):
-    if _bf16_type is None:
-        _load_types()
-    if t.dtype is not _bf16_type or not t.is_cuda or not t.is_contiguous():
-        _need(t, (_bf16_type,), name)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {shape}")
-    return t.data_ptr()
-
-
-def _lse(lse, T, heads):
-    if lse is None:
-        return None
-    if _f32_type is None:
-        _load_types()
-    _need(lse, (_f32_type,), "lse")
-    if lse.shape != (T, heads):
-        raise ValueError(f"lse must have shape {(T, heads)}")
-    return lse.data_ptr()
+_calls = _Calls()
 
 
 def mlora_qk_rope(qkv, n_q_heads: int, n_kv_heads: int, head_dim: int, pos, rope: Rope, q_out,
@@ -510,39 +470,16 @@ def mlora_qk_rope(qkv, n_q_heads: int, n_kv_heads: int, head_dim: int, pos, rope
                   cache: Cache | None = None, slot=None, stream=None):
     """qkv bf16 [T][(n_q_heads + 2 n_kv_heads) * head_dim]; q_out, k_out bf16
     [T][heads][head_dim], also views of qkv's own query and key parts."""
-    if _bf16_type is None:
-        _load_types()
-    if qkv.dtype is not _bf16_type or not qkv.is_cuda or qkv.dim() != 2:
-        raise ValueError("qkv must be a bf16 [T][width] device tensor")
-    T, w = qkv.shape
-    width = (n_q_heads + 2 * n_kv_heads) * head_dim
-    row, one = qkv.stride()
-    if w != width or (T > 0 and one != 1):
-        raise ValueError(f"rows of qkv must hold {width} contiguous values")
-    q_stride = _rows(q_out, "q_out", (T, n_q_heads, head_dim))
-    k_stride = 0 if k_out is None else _rows(k_out, "k_out", (T, n_kv_heads, head_dim))
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and _bf16(w, name).numel() != head_dim:
-            raise ValueError(f"{name} must hold head_dim values")
-    code = _lib.mlora_qk_rope(qkv.data_ptr(), T, row if T > 1 else width, n_q_heads, n_kv_heads,
-                              head_dim, _ints(pos, T, "pos"), rope.ref,
-                              None if q_weight is None else q_weight.data_ptr(),
-                              None if k_weight is None else k_weight.data_ptr(), eps,
-                              q_out.data_ptr(), q_stride,
-                              None if k_out is None else k_out.data_ptr(), k_stride,
-                              None if cache is None else cache.ref,
-                              None if slot is None else _ints(slot, T, "slot"), _stream(stream))
+    code = _calls.qk_rope(qkv, n_q_heads, n_kv_heads, head_dim, pos, rope.address, q_out, k_out,
+                          q_weight, k_weight, eps, None if cache is None else cache.address, slot,
+                          _stream(stream))
     if code:
         _check(code, "mlora_qk_rope")
 
 
 def mlora_cache_read(cache: Cache, slot, k, v, stream=None):
     """Tokens slot[0..T) of the cache into k, v bf16 [T][n_kv_heads][head_dim] (either None)."""
-    T = slot.numel()
-    shape = (T, cache.n_kv_heads, cache.head_dim)
-    code = _lib.mlora_cache_read(cache.ref, _ints(slot, T, "slot"), T,
-                                 None if k is None else _dense(k, shape, "k"),
-                                 None if v is None else _dense(v, shape, "v"), _stream(stream))
+    code = _calls.cache_read(cache.address, slot, k, v, _stream(stream))
     if code:
         _check(code, "mlora_cache_read")
 
@@ -552,18 +489,8 @@ def mlora_attention(q, k, v, cu_q, out, cu_k=None, max_q: int | None = None, cau
     """q, out bf16 [T_q][n_q_heads][head_dim], k, v bf16 [T_k][n_kv_heads][head_dim], rows of any
     stride (views of a merged row); cu_q, cu_k int32 [n_seqs + 1] device.  max_q: the longest
     sequence's queries (None: T_q)."""
-    q_shape, k_shape = q.shape, k.shape
-    q_stride = _rows(q, "q")
-    T, hq, d = q_shape
-    k_stride = _rows(k, "k", (k_shape[0], k_shape[1], d))
-    n = cu_q.numel() - 1
-    code = _lib.mlora_attention(q.data_ptr(), q_stride, k.data_ptr(), k_stride, v.data_ptr(),
-                                _rows(v, "v", k_shape), T, k_shape[0], n,
-                                _ints(cu_q, n + 1, "cu_q"),
-                                None if cu_k is None else _ints(cu_k, n + 1, "cu_k"), hq,
-                                k_shape[1], d, T if max_q is None else max_q, int(causal), window,
-                                scale, out.data_ptr(), _rows(out, "out", q_shape),
-                                _lse(lse, T, hq), _stream(stream))
+    code = _calls.attention(q, k, v, cu_q, out, cu_k, max_q, causal, window, scale, lse,
+                            _stream(stream))
     if code:
         _check(code, "mlora_attention")
 
@@ -589,24 +516,8 @@ def mlora_paged_attention(q, cache: Cache, page_table, cu_q, kv_len, out, max_q:
                           lse=None, ws=None, stream=None):
     """q, out bf16 [T][n_q_heads][head_dim] (rows of any stride); page_table int32
     [n_seqs][pages], cu_q int32 [n_seqs + 1], kv_len int32 [n_seqs], device."""
-    q_shape = q.shape
-    q_stride = _rows(q, "q")
-    T, hq, d = q_shape
-    n = kv_len.numel()
-    if page_table.dim() != 2 or page_table.shape[0] != n:
-        raise ValueError("page_table must be [n_seqs][pages]")
-    if d != cache.head_dim:
-        raise ValueError("q and the cache must have one head_dim")
-    if ws is not None and not ws.is_cuda:
-        raise ValueError("ws must be a device tensor")
-    code = _lib.mlora_paged_attention(q.data_ptr(), q_stride, T, hq, cache.ref,
-                                      _ints(page_table, page_table.numel(), "page_table"),
-                                      page_table.shape[1], n, _ints(cu_q, n + 1, "cu_q"),
-                                      _ints(kv_len, n, "kv_len"), max_q, max_kv, int(causal),
-                                      window, scale, out.data_ptr(), _rows(out, "out", q_shape),
-                                      _lse(lse, T, hq), None if ws is None else ws.data_ptr(),
-                                      0 if ws is None else ws.numel() * ws.element_size(),
-                                      _stream(stream))
+    code = _calls.paged_attention(q, cache.address, page_table, cu_q, kv_len, out, max_q, max_kv,
+                                  causal, window, scale, lse, ws, _stream(stream))
     if code:
         _check(code, "mlora_paged_attention")
 

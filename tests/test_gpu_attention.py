@@ -539,6 +539,45 @@ def test_pages_outside_the_cache_do_not_fault(m):
         check(out[lo:hi], ref, mag, big)
 
 
+def test_binding_refusals(m):
+    """Tensors of another shape, dtype, layout or device raise before anything is launched."""
+    dev, bf = "cuda", torch.bfloat16
+    new = lambda *s, t=bf: torch.zeros(s, device=dev, dtype=t)  # noqa: E731
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+    x, k, cu, out = new(5, 4, 64), new(5, 2, 64), ints(0, 5), new(5, 4, 64)
+    c = m.Cache(new(2, 2, 16, 64), new(2, 2, 16, 64))
+    rope = m.Rope(m.mlora_rope_turns(64).to(dev), 64)
+    ws = m.paged_workspace(5, 1, 4, 2, 64, 5, 16)
+    pos = ints(0, 1, 2, 3, 4)
+    attend = lambda **a: m.mlora_attention(**{**dict(q=x, k=k, v=k, cu_q=cu, out=out), **a})  # noqa: E731
+    paged = lambda **a: m.mlora_paged_attention(**{**dict(q=x, cache=c, page_table=ints(0)[None], cu_q=cu,  # noqa: E731
+                                                          kv_len=ints(5), out=out, max_q=5, max_kv=16, ws=ws), **a})
+    rotate = lambda **a: m.mlora_qk_rope(**{**dict(qkv=new(5, 512), n_q_heads=4, n_kv_heads=2, head_dim=64,  # noqa: E731
+                                                   pos=pos, rope=rope, q_out=out), **a})
+    read = lambda **a: m.mlora_cache_read(**{**dict(cache=c, slot=pos, k=k, v=k.clone()), **a})  # noqa: E731
+    for call in (attend, paged, rotate, read):
+        call()
+    bad = [(attend, dict(q=x.float())), (attend, dict(q=x.cpu())), (attend, dict(q=x[0])), (attend, dict(q=None)),
+           (attend, dict(q=new(5, 64, 4).transpose(1, 2))), (attend, dict(v=new(4, 2, 64))), (attend, dict(out=new(5, 4, 128))),
+           (attend, dict(k=new(5, 2, 128), v=new(5, 2, 128))), (attend, dict(cu_q=cu.long())), (attend, dict(cu_k=ints(0, 2, 5))),
+           (attend, dict(lse=new(5, 4))), (attend, dict(lse=new(5, 2, t=torch.float32))), (attend, dict(window=2 ** 31)),
+           (paged, dict(kv_len=ints(5, 5))), (paged, dict(page_table=ints(0))), (paged, dict(q=new(5, 4, 128), out=new(5, 4, 128))),
+           (paged, dict(ws=ws.cpu())), (paged, dict(cu_q=ints(0, 2, 5))),
+           (rotate, dict(qkv=new(5, 500))), (rotate, dict(qkv=new(512, 5).t())), (rotate, dict(pos=ints(0, 1))),
+           (rotate, dict(q_weight=new(128))), (rotate, dict(k_weight=new(64, t=torch.float32))), (rotate, dict(q_out=new(4, 4, 64))),
+           (rotate, dict(k_out=new(5, 4, 64))), (rotate, dict(cache=c, slot=pos.long())),
+           (read, dict(slot=pos.long())), (read, dict(k=new(5, 2, 32))), (read, dict(v=k.transpose(0, 1)))]
+    for call, change in bad:
+        with pytest.raises(ValueError):
+            call(**change)
+    for call, change in ((attend, dict(scale=-1.0)), (attend, dict(k=new(5, 3, 64), v=new(5, 3, 64))), (rotate, dict(cache=c))):
+        with pytest.raises(m.MloraError):
+            call(**change)
+    with pytest.raises(TypeError):
+        attend(max_q="5")
+    torch.cuda.synchronize()
+
+
 def test_streams_and_graph(m):
     """On a stream of its own and captured in a graph, replayed with eager work between: the eager bits."""
     g = gen(21)
