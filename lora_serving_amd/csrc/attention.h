@@ -57,6 +57,7 @@ struct AttnArgs {
 };
 // Whole prompts (cache unused) or, with pages, chunks of new tokens.
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream);
+constexpr int64_t CUS = 256;      // of an MI355X
 constexpr int WIDE_ROWS = 128;    // rows (queries x heads of a group) of one workgroup
 hipError_t launch_attn_wide_combine(const AttnArgs &a, int head_dim, hipStream_t stream);
 // Sequences of up to 16 * nq rows (nq 1 or 2) over pages, their keys cut into `shares` equal shares, or (part_o ==

@@ -14,7 +14,6 @@ namespace {
 
 constexpr int64_t MAX_ROWS = INT64_C(1) << 31;   // query rows x heads: 32-bit row numbers
 constexpr int64_t MAX_KEYS = INT64_C(1) << 30;   // tokens: positions and windows add up within 32 bits
-constexpr int64_t CUS = 256;                     // of an MI355X
 constexpr int64_t MAX_STRIDE = INT64_C(1) << 24; // K and V rows: 64 of them within a 32-bit byte offset
 
 bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
