@@ -59,6 +59,12 @@ struct AttnArgs {
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream);
 constexpr int64_t CUS = 256;      // of an MI355X
 constexpr int WIDE_ROWS = 128;    // rows (queries x heads of a group) of one workgroup
+// Row blocks that a launch covers: each sequence's last one may be part empty, at most one more a sequence.
+inline int64_t wide_items(const AttnArgs &a)
+{
+    const int64_t most = (a.max_q * a.group + WIDE_ROWS - 1) / WIDE_ROWS, fill = a.T * a.group / WIDE_ROWS + a.n_seqs;
+    return most * a.n_seqs < fill ? most * a.n_seqs : fill;
+}
 hipError_t launch_attn_wide_combine(const AttnArgs &a, int head_dim, hipStream_t stream);
 // Sequences of up to 16 * nq rows (nq 1 or 2) over pages, their keys cut into `shares` equal shares, or (part_o ==
 // nullptr) one workgroup a sequence and kv head, then shares = n_seqs * hkv.
@@ -67,5 +73,7 @@ constexpr int DECODE_UNIT = 128;  // keys: the unit that shares are made of
 constexpr int decode_slots(int head_dim, int nq) { return head_dim == 64 && nq == 1 ? 3 : 2; }
 hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream);
 hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream);
+// Both kinds of sequences over pages in one launch: w as for launch_attn_wide, d as for launch_attn_decode (nq 1).
+hipError_t launch_attn_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int shares, hipStream_t stream);
 
 }  // namespace mlora

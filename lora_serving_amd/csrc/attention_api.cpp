@@ -369,28 +369,28 @@ mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, i
     a.scale = scale == 0.f ? (float)(1.0 / std::sqrt((double)d)) : scale;
     a.out = (uint16_t *)out;
     a.lse = lse;
+    AttnArgs w = a;                     // the wide part
+    w.min_rows = (int32_t)p.dec_rows + 1;
+    w.max_rows = 0x7fffffff;
+    w.chunk = (int32_t)p.wide_chunk;
+    w.n_chunks = (int32_t)p.wide_chunks;
+    w.part_o = (float *)(base + p.dec_o + p.dec_ml);
+    w.part_ml = (float *)(base + p.dec_o + p.dec_ml + p.wide_o);
+    a.max_rows = (int32_t)p.dec_rows;   // and the decode rows
+    a.part_o = p.split ? (float *)base : nullptr;
+    a.part_ml = p.split ? (float *)(base + p.dec_o) : nullptr;
     trace_mark(stream, true);
-    hipError_t e = hipSuccess;
-    if (p.wide) {
-        AttnArgs w = a;
-        w.min_rows = (int32_t)p.dec_rows + 1;
-        w.max_rows = 0x7fffffff;
-        w.chunk = (int32_t)p.wide_chunk;
-        w.n_chunks = (int32_t)p.wide_chunks;
-        w.part_o = (float *)(base + p.dec_o + p.dec_ml);
-        w.part_ml = (float *)(base + p.dec_o + p.dec_ml + p.wide_o);
+    hipError_t e;
+    if (p.wide && p.dec_rows > 0)
+        e = launch_attn_mixed(w, a, d, p.shares, stream);
+    else if (p.wide)
         e = launch_attn_wide(w, d, true, stream);
-        if (e == hipSuccess && p.wide_chunks > 1)
-            e = launch_attn_wide_combine(w, d, stream);
-    }
-    if (e == hipSuccess && p.dec_rows > 0) {
-        a.max_rows = (int32_t)p.dec_rows;
-        a.part_o = p.split ? (float *)base : nullptr;
-        a.part_ml = p.split ? (float *)(base + p.dec_o) : nullptr;
+    else
         e = launch_attn_decode(a, d, p.nq, p.shares, stream);
-        if (e == hipSuccess && p.split)
-            e = launch_attn_combine(a, d, p.shares, stream);
-    }
+    if (e == hipSuccess && p.wide_chunks > 1)
+        e = launch_attn_wide_combine(w, d, stream);
+    if (e == hipSuccess && p.split)
+        e = launch_attn_combine(a, d, p.shares, stream);
     trace_mark(stream, false);
     return hip_status(e);
 }

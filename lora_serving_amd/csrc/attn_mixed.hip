@@ -1,0 +1,59 @@
+// The mixed batch over pages: chunks of new tokens (attn_wide_body.h) and decode rows (attn_decode_body.h) in one
+// launch.  The former are bound by the matrix cores, the latter by memory, and a CU holds two workgroups of either
+// kind; so the launch begins with one of each on every CU and goes on with both in turn (256 tokens with contexts of
+// 64 to 2048 and a chunk of 2048 tokens after 6000: 391 us, one kernel after the other 449; with contexts of 1000
+// and a chunk over 8192 379 us against 438).
+#include "attn_decode_body.h"
+#include "attn_wide_body.h"
+
+namespace mlora {
+
+template <int D, bool FP8>
+__global__ __launch_bounds__(256, 2) void attn_mixed_kernel(AttnArgs w, AttnArgs d, uint32_t wide_x, uint32_t shares)
+{
+    constexpr int SRC = FP8 ? AW_PAGES_E4M3 : AW_PAGES;
+    constexpr int LDS = wide_lds<D, SRC, 1> > decode_lds<D, 1> ? wide_lds<D, SRC, 1> : decode_lds<D, 1>;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[LDS];
+    // the first 256 of the wide ones, the first 256 of the others, then groups of each in turn.  Workgroups go to the 8
+    // XCDs, and within one to its shader engines and their CUs, in turn: smaller groups would give each kind to some
+    // of them alone.
+    constexpr uint32_t GROUP = 256;
+    const uint32_t wide = wide_x * w.n_chunks, w0 = min(wide, (uint32_t)CUS), d0 = min(shares, (uint32_t)CUS);
+    uint32_t i = blockIdx.x;
+    bool is_wide = i < w0;
+    if (!is_wide) {
+        i -= w0;
+        if (i >= d0) {
+            i -= d0;
+            const uint32_t both = min(wide - w0, shares - d0) & ~(GROUP - 1);
+            if (i < 2 * both) {
+                is_wide = (i / GROUP & 1) == 0;
+                i = i / (2 * GROUP) * GROUP + (i & (GROUP - 1)) + (is_wide ? w0 : d0);
+            } else {
+                i -= 2 * both;
+                is_wide = i < wide - w0 - both;
+                i = is_wide ? i + w0 + both : i - (wide - w0 - both) + d0 + both;
+            }
+        }
+    }
+    if (is_wide)
+        attn_wide_body<D, SRC, 1>(w, (int)(i % wide_x), (int)(i / wide_x), smem);
+    else
+        attn_decode_body<D, 1, FP8>(d, i, shares, smem);
+}
+
+hipError_t launch_attn_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int shares, hipStream_t stream)
+{
+    const int64_t wide_x = wide_items(w) * w.hkv, blocks = wide_x * w.n_chunks + shares;
+    if (blocks > 0x7fffffff)
+        return hipErrorInvalidValue;
+#define MIX(D, F) attn_mixed_kernel<D, F><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(w, d, (uint32_t)wide_x, (uint32_t)shares)
+    if (head_dim == 64)
+        d.cache.fp8 ? MIX(64, true) : MIX(64, false);
+    else
+        d.cache.fp8 ? MIX(128, true) : MIX(128, false);
+#undef MIX
+    return hipGetLastError();
+}
+
+}  // namespace mlora
