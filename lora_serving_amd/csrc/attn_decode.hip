@@ -27,7 +27,7 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs a, int share
         return;
     const int end = (int)cut.of(u1 - at.f + at.sq.units - 1) + 1, rows = at.sq.n * a.group;
     for (int row = threadIdx.x >> 6; row < rows; row += 4) {
-        const int i = row / a.group, hd = at.h * a.group + row - i * a.group;
+        const int i = row / a.group, hd = turned_head(a, at.b, at.h) * a.group + row - i * a.group;
         join_parts<D>(a, w0, end, [&](int w) { return part_slot(a, w, w > w0, row); }, at.sq.q0 + i, hd);
     }
 }

@@ -81,7 +81,16 @@ struct Shares {
     }
 };
 
-// The (sequence, head) that holds unit `at`, and the unit's number in it.
+// The head at place h among those of sequence b.  The order of the heads turns with the sequence: shares of equal
+// contexts that are whole heads long would else all read the same few heads of their pages at a time (e4m3, 256
+// contexts of 2048: 256 us, turned 200; of 600: 79, turned 68; other batches: 0.5% slower at the median, 2.4% at most).
+__device__ __forceinline__ int turned_head(const AttnArgs &a, int b, int h)
+{
+    const int t = h + (int)((unsigned)b % (unsigned)a.hkv);
+    return t < a.hkv ? t : t - a.hkv;
+}
+
+// The (sequence, head's place) that holds unit `at`, and the unit's number in it.
 struct UnitPlace {
     int b, h, f;
     SeqUnits sq;
@@ -177,7 +186,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
 
     while (left > 0) {
         const int end = min(sq.units, f + left);
-        const int rows = sq.n * a.group, L = sq.L;
+        const int rows = sq.n * a.group, L = sq.L, head = turned_head(a, b, h);
         const int k0 = max((sq.first + f) * DECODE_UNIT, sq.lo & ~31), k1 = min(L, (sq.first + end) * DECODE_UNIT);
         const int32_t *__restrict__ table = a.table + (int64_t)b * a.table_stride;
 
@@ -195,7 +204,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         auto load = [&](int kb) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int64_t at = (((int64_t)clamp_page(uniform(pg[u]), a.cache.n_pages) * a.cache.hkv + h) << ps) + ((kb + 16 * u) & pm);
+                const int64_t at = (((int64_t)clamp_page(uniform(pg[u]), a.cache.n_pages) * a.cache.hkv + head) << ps) + ((kb + 16 * u) & pm);
                 const uint8_t *kp = a.cache.k + at * D * ESZ, *vp = a.cache.v + at * D * ESZ;
 #pragma unroll
                 for (int s = 0; s < LD; ++s)
@@ -225,7 +234,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         auto qpiece = [&](int s) { return FP8 ? 8 * (s >> 1) + 2 * g + (s & 1) : 4 * s + g; };
 #pragma unroll
         for (int j = 0; j < NQ; ++j) {
-            const int r = min(16 * j + col, rows - 1), i = r / a.group, hd = h * a.group + r - i * a.group;
+            const int r = min(16 * j + col, rows - 1), i = r / a.group, hd = head * a.group + r - i * a.group;
             pos[j] = L - sq.n + i;
             const uint16_t *qr = a.q + (sq.q0 + i) * a.q_stride + (int64_t)hd * D;
             if (NQ == 1) {
@@ -484,7 +493,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                             acc[e + i] += f * x[i];
                     }
                 }
-                const int i = row / a.group, hd = h * a.group + row - i * a.group;
+                const int i = row / a.group, hd = head * a.group + row - i * a.group;
                 if (f == 0 && end == sq.units) {
                     const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
                     uint16_t *dst = a.out + (sq.q0 + i) * a.out_stride + (int64_t)hd * D + part * VPT;
