@@ -622,3 +622,21 @@ def test_streams_and_graph(m):
         assert all(torch.equal(a, b) for a, b in zip(eager, held))
         ws.fill_(255)
         torch.cuda.synchronize()
+
+
+WHOLE_OR_SHARED = [
+    # contexts of 5 to 9 units of 128 keys, with fewer (sequence, kv head) pairs than CUs and with as many; odd head
+    # counts, for the heads' order turns with the sequence
+    ([(1, 1 + 97 * i % 1024) for i in range(63)] + [(1, 1024)], 4, 4, 64, 16, False, True, 0),      # 256, whole
+    ([(1, 1 + 97 * i % 1024) for i in range(84)] + [(1, 1024)], 3, 3, 64, 16, True, True, 0),       # 255, shared
+    ([(1, 1 + 97 * i % 1024) for i in range(63)] + [(1, 1025)], 8, 4, 128, 16, True, True, 0),      # 256, 9 units
+    ([(2, 2 + 61 * i % 900) for i in range(52)], 10, 5, 128, 32, False, True, 700),                 # 260, whole
+    ([(1, 1280)] * 7, 14, 7, 128, 64, False, True, 0),                                              # equal, shared
+    ([(1, 640)] * 40 + [(200, 900)], 14, 7, 64, 16, True, True, 0),                                 # and a chunk
+]
+
+
+@pytest.mark.parametrize("poison", [False, True], ids=["", "poison"])
+@pytest.mark.parametrize("case", WHOLE_OR_SHARED, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-60:])
+def test_paged_whole_or_shared(m, case, poison):
+    test_paged(m, case, poison)
