@@ -11,7 +11,9 @@ __global__ __launch_bounds__(256, decode_slots(D, NQ)) void attn_decode_kernel(A
     attn_decode_body<D, NQ, FP8>(a, blockIdx.x, gridDim.x, smem);
 }
 
-// The join, a workgroup a cut between shares: the first cut within a sequence and head joins its parts, one wave a row.
+// The join, a workgroup a cut between shares: the first cut within a sequence and head joins its parts, one wave a
+// row.  A few MB that the shares just wrote: bound by the latency of a launch and its chain of loads (one context of
+// 1003 keys 3.8 us; 511 cuts 6 to 8 us).
 template <int D>
 __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs a, int shares)
 {

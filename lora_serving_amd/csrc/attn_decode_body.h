@@ -9,7 +9,9 @@
 // own running maximum, sums and accumulators, joined in LDS at the end of a piece.  K goes from
 // memory straight into the fragments; V through a wave's own piece of LDS, written by rows and
 // read transposed, so the loop has no barrier.  The next step's loads are issued while this
-// one's softmax and second product run.  Bound by HBM (or, for a short batch, by latency).
+// one's softmax and second product run.  Bound by HBM (or, for a short batch, by latency).  Measured
+// (D = 128, 32 heads on 8, with the join): 64 contexts of 1 to 8192 225 to 232 us (5.6 to 5.7 TB/s), 64 of
+// 4096 184 us (5.8), 256 of an e4m3 cache 231 us (5.1), one of 1003 10.5 us (7 the shares, 4 the join).
 #pragma once
 
 #include <type_traits>

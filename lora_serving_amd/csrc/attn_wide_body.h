@@ -2,12 +2,20 @@
 // over a paged cache.
 //
 // Rows are (query, head of the kv head's group) pairs of one sequence, so that the heads of a group
-// share each tile of K and V and a workgroup's causal edge is only its 256 / group queries wide.  A
+// share each tile of K and V and a workgroup's causal edge is only its 128 / group queries wide.  A
 // wave owns 32 rows as the columns of 32x32x16 MFMA tiles (S^T = K Q^T, O^T = V^T P^T, see
-// attention_device.h); all waves of the workgroup share 64-key tiles of K and V in LDS, double
+// attention_device.h); the four waves of a workgroup share 64-key tiles of K and V in LDS, double
 // buffered: the next tile is copied straight into LDS while this one is computed, one barrier a
 // tile.  e4m3 tiles are converted to bf16 (exactly) on their way into LDS, their scales applied to
-// the scores and the probabilities.  Bound by the matrix cores together with the exponentials.
+// the scores and the probabilities.
+//
+// Two workgroups of 128 rows a CU, which wait at barriers of their own, rather than one of 256 rows
+// (8 causal prompts of 2048, 32 heads of 128 on 8: 338 us against 357 when that was chosen).  Bound by
+// the issue of products and exponentials together: on a prompt of 16384 tokens a SIMD's matrix core
+// is busy for 61 to 63% of the cycles and its vector unit for 53 to 54%, at 1.7 to 1.8 GHz.  Measured
+// (D = 128, 32 heads on 8): 8 prompts of 2048 308 us (890 TFLOP/s), one of 16384 1.91 to 1.96 ms (1120
+// to 1150), 2048 tokens over 8192 keys in bf16 pages 229 us (1050), in e4m3 pages 286 us (840: the
+// conversions take the issue), D = 64 155 us (770: the same exponentials for half the products).
 #pragma once
 
 #include <type_traits>
