@@ -202,12 +202,15 @@ __device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by
     }
     const uint16_t *kp = a.k + ((int64_t)key0 + (int64_t)t0 * BN) * a.k_stride + (int64_t)h * D;   // rows: the next tile
     const uint16_t *vp = a.v + ((int64_t)key0 + (int64_t)t0 * BN) * a.v_stride + (int64_t)h * D;
-    int pgk = 0, pgv = 0;
+    int pgs = 0, pgk = 0, pgv = 0;
     u32x4 kr[IPW], vr[IPW];
     float scr = 0.f;
-    auto lookup = [&](int t) {      // the page of this wave's rows of tile t
+    // pages of this wave's rows of the 64 tiles around t, one a lane: a scalar load a tile comes late when memory is
+    // busy, and its wait drains the reads of LDS with it (256 single tokens and a chunk of 2048 392 us, so 367; a
+    // chunk split into pieces of a few tiles waits longer for its first: 100 tokens over 8192 39.4 us, so 40.1)
+    auto lookup = [&](int t) {
         if (SRC != AW_ROWS)
-            pgk = clamp_page(table[min(t * BN + w16, L - 1) >> ps], a.cache.n_pages);
+            pgs = table[min(((t & ~63) + lane) * BN + w16, L - 1) >> ps];
     };
     // (to: where the tile goes, bytes of LDS, this wave's rows)
     auto copy = [&](int t, const uint16_t *&rows, int64_t stride, const uint8_t *pages, int pg, const uint32_t (&off)[IPW],
@@ -239,12 +242,13 @@ __device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by
                           (uint32_t)(kg * GROUP + w16 * D) * 2, to_v = to_k + 4 * TILE;
     // K of tile t + 1 on its way (pgk: its page), and V of tile t (pgv: its page); K first
     auto issue_k = [&](int t) __attribute__((always_inline)) {
-        if (t + 1 < t1)
+        if (t + 1 < t1) {
+            if (SRC != AW_ROWS)
+                pgk = clamp_page(__builtin_amdgcn_readlane(pgs, (t + 1) & 63), a.cache.n_pages);
             copy(t + 1, kp, a.k_stride, a.cache.k, pgk, off_k, to_k + ((t + 1) & 1) * (2 * TILE), kr);
-        if (FP8 && threadIdx.x < 2 * BN) {      // scales of K and of V, both of tile t + 1
-            const int key = min((t + 1) * BN + (int)(threadIdx.x & (BN - 1)), L - 1);
-            const int page = clamp_page(table[key >> ps], a.cache.n_pages);
-            scr = (threadIdx.x < BN ? a.cache.k_scale : a.cache.v_scale)[(((int64_t)page * a.cache.hkv + h) << ps) + (key & pm)];
+            if (FP8 && lane < 32)       // scales of K and of V, both of tile t + 1 (this wave's rows)
+                scr = (lane < 16 ? a.cache.k_scale : a.cache.v_scale)[(((int64_t)pgk * a.cache.hkv + h) << ps) +
+                                                                      (((t + 1) * BN + w16 + (lane & 15)) & pm)];
         }
     };
     auto issue_v = [&](int t) __attribute__((always_inline)) {
@@ -252,7 +256,7 @@ __device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by
             copy(t, vp, a.v_stride, a.cache.v, pgv, off_v, to_v + (t & 1) * (2 * TILE), vr);
         if (SRC != AW_ROWS) {
             pgv = pgk;
-            if (t + 2 < t1)
+            if (t + 2 < t1 && ((t + 2) & 63) == 0)
                 lookup(t + 2);
         }
     };
@@ -276,8 +280,8 @@ __device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by
                         *(u32x4 *)(vl + (nb ^ 1) * TILE + r * D + p) = e4m3_to_bf16x8(vr[i][2 * e], vr[i][2 * e + 1]);
                 }
             }
-            if (threadIdx.x < 2 * BN)
-                sc[(t + 1) & 3][threadIdx.x / BN][threadIdx.x & (BN - 1)] = scr;
+            if (lane < 32)
+                sc[(t + 1) & 3][lane >> 4][w16 + (lane & 15)] = scr;
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
         } else {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
