@@ -59,11 +59,21 @@ struct AttnArgs {
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream);
 constexpr int64_t CUS = 256;      // of an MI355X
 constexpr int WIDE_ROWS = 128;    // rows (queries x heads of a group) of one workgroup
-// Row blocks that a launch covers: each sequence's last one may be part empty, at most one more a sequence.
+// Row blocks that a launch may have: each sequence's last one may be part empty, at most one more a sequence.
 inline int64_t wide_items(const AttnArgs &a)
 {
-    const int64_t most = (a.max_q * a.group + WIDE_ROWS - 1) / WIDE_ROWS, fill = a.T * a.group / WIDE_ROWS + a.n_seqs;
-    return most * a.n_seqs < fill ? most * a.n_seqs : fill;
+    const int64_t least = a.min_rows > a.group ? a.min_rows : a.group, seqs = a.T * a.group / least;
+    const int64_t most = (a.max_q * a.group + WIDE_ROWS - 1) / WIDE_ROWS * a.n_seqs;
+    const int64_t fill = a.T * a.group / WIDE_ROWS + (seqs < a.n_seqs ? seqs : a.n_seqs);
+    return most < fill ? most : fill;
+}
+// Row blocks that workgroups are launched for over pages (a workgroup takes further ones where there are more): those
+// that the rows fill and two workgroups a CU, unless all sequences may be wide.
+inline int64_t wide_launched(const AttnArgs &a)
+{
+    const int64_t items = wide_items(a), card = 2 * CUS / ((int64_t)a.hkv * a.n_chunks);
+    const int64_t few = (a.T * a.group + WIDE_ROWS - 1) / WIDE_ROWS + (card > 1 ? card : 1);
+    return a.T * a.group > (int64_t)a.n_seqs * (a.min_rows - 1) || items < few ? items : few;
 }
 hipError_t launch_attn_wide_combine(const AttnArgs &a, int head_dim, hipStream_t stream);
 // Sequences of up to 16 * nq rows (nq 1 or 2) over pages, their keys cut into `shares` equal shares, or (part_o ==

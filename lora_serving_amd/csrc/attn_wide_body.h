@@ -49,6 +49,7 @@ __device__ __forceinline__ int aw_swz(int key)
 // A workgroup's work: row block `block` of a sequence's query rows [q0, q0 + n), its L keys (rows: from key0 on).
 struct WideItem {
     int seq, block, q0, n, key0, L;
+    int total;              // items of all sequences
 };
 
 // The sequence and row block of an item: the longest row blocks (the last ones of a causal prompt) first, of
@@ -84,7 +85,8 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, W
         const int nb = load(lane);
         // items of block numbers >= r
         auto count = [&](int r) { return wave_total(max(nb - r, 0)); };
-        if (item >= count(0))
+        w->total = count(0);
+        if (item >= w->total)
             return false;
         // count(lo) > item >= count(hi)
         int lo = 0, hi = (int)((a.max_q * a.group + WIDE_ROWS - 1) / WIDE_ROWS);
@@ -101,28 +103,37 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, W
         take(0, uniform(__ffsll((unsigned long long)ballot64(nb > lo && rank == nth)) - 1), lo);
         return true;
     }
-    for (int s0 = 0, base = 0; s0 < a.n_seqs; s0 += 64) {
-        const int nb = load(s0 + lane);
-        int total;
-        const int ex = wave_exclusive_scan(nb, &total);
-        total = uniform(total);
-        if (item < base + total) {
-            const uint64_t hit = ballot64(item >= base + ex && item < base + ex + nb);
-            const int src = uniform(__ffsll((unsigned long long)hit) - 1);
-            take(s0, src, __builtin_amdgcn_readlane(nb, src) - 1 - (item - base - __builtin_amdgcn_readlane(ex, src)));
+    // a lane counts `per` consecutive sequences; then those of the lane that has the item, a lane each
+    const int per = (a.n_seqs + 63) / 64;
+    int mine = 0;
+#pragma unroll 4
+    for (int i = 0; i < per; ++i)
+        mine += load(lane * per + i);
+    const int upto = wave_prefix(mine);
+    w->total = __builtin_amdgcn_readlane(upto, 63);
+    if (item >= w->total)
+        return false;
+    const int owner = uniform(__ffsll((unsigned long long)ballot64(item < upto)) - 1);
+    int rest = item - (__builtin_amdgcn_readlane(upto, owner) - __builtin_amdgcn_readlane(mine, owner));
+    for (int s0 = owner * per;; s0 += 64) {
+        const int nb = s0 + lane < owner * per + per ? load(s0 + lane) : 0;
+        const int up = wave_prefix(nb), total = __builtin_amdgcn_readlane(up, 63);
+        if (rest < total) {
+            const int src = uniform(__ffsll((unsigned long long)ballot64(rest < up)) - 1);
+            take(s0, src, __builtin_amdgcn_readlane(up, src) - 1 - rest);
             return true;
         }
-        base += total;
+        rest -= total;
     }
-    return false;
 }
 
 template <int D, int SRC, int KG>
 constexpr int wide_lds = KG * 4 * AW_BN * D * 2 + (SRC == AW_PAGES_E4M3 ? 4 * 2 * AW_BN * 4 : 0) + (KG > 1 ? 4 * 64 * 2 * 4 : 0);
 
-// Workgroup (bx, by) of the launch: an item and kv head, and a chunk of keys; smem: wide_lds bytes.
-template <int D, int SRC, int KG>
-__device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by, uint8_t *smem)
+// Item and kv head bx, and chunk of keys by; smem: wide_lds bytes.  Returns how many items there are.  (MORE: called
+// for several items.)
+template <int D, int SRC, int KG, bool MORE = false>
+__device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by, uint8_t *smem)
 {
     constexpr bool FP8 = SRC == AW_PAGES_E4M3;
     constexpr int NW = 4, BM = WIDE_ROWS, BN = AW_BN;
@@ -139,14 +150,17 @@ __device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by
     float (*const joint)[64][2] = (float (*)[64][2])(smem + KG * GROUP * 2);        // KG = 2: maxima and sums
 
     static_assert(KG == 1 || !FP8, "one set of scales");
-    const int kg = KG > 1 ? uniform(threadIdx.x >> 8) : 0, wave = uniform((threadIdx.x >> 6) & 3);
+    int thread = threadIdx.x;
+    if (MORE)           // (opaque: what the items of a workgroup have in common is not kept, and spilled, between)
+        asm volatile("" : "+v"(thread));
+    const int kg = KG > 1 ? uniform(thread >> 8) : 0, wave = uniform((thread >> 6) & 3);
     uint16_t *const kl = lds + kg * GROUP, *const vl = kl + 2 * TILE;
-    const int lane = threadIdx.x & 63, col = lane & 31, hh = lane >> 5;
+    const int lane = thread & 63, col = lane & 31, hh = lane >> 5;
     const int item = (int)((unsigned)bx / a.hkv), h = (int)((unsigned)bx - (unsigned)item * a.hkv);
 
     WideItem it;
     if (!aw_item<SRC == AW_ROWS>(a, item, lane, &it))
-        return;
+        return it.total;
     const int b = it.seq, rb = it.block, q0 = it.q0, n = it.n, L = it.L, key0 = it.key0;
     const int rows = n * a.group;
 
@@ -160,7 +174,7 @@ __device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by
     const int kmin = max(first_key(rb * BM), c0);
     const int kmax = (int)min((int64_t)end_key(rb * BM + BM - 1), (int64_t)c0 + a.chunk);
     if (by > 0 && kmin >= kmax)
-        return;
+        return it.total;
     const int wrow = rb * BM + wave * 32;
     const int wmin = first_key(wrow), wmax = wrow < rows ? end_key(wrow + 31) : 0;
     // the tiles, or this half's of them
@@ -611,7 +625,7 @@ __device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by
         }
         __syncthreads();
         if (kg)
-            return;
+            return it.total;
         const float m1 = joint[wave][lane][0], l1 = joint[wave][lane][1], mx = fmaxf(m, m1);
         const float s0 = __builtin_amdgcn_exp2f(m - mx), s1 = __builtin_amdgcn_exp2f(m1 - mx);
         m = mx;
@@ -648,9 +662,7 @@ __device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by
             if (wrow + r < rows)
                 *(u32x4 *)(a.out + at + 8 * piece) = w;
         }
-        if (row >= rows)
-            return;
-        if (a.lse && hh == 0)
+        if (row < rows && a.lse && hh == 0)
             a.lse[(int64_t)(q0 + ri) * a.hq + hd] =
                 l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * (1.f / ATTN_LOG2E);
     } else if (row < rows) {
@@ -663,6 +675,19 @@ __device__ __forceinline__ void attn_wide_body(const AttnArgs &a, int bx, int by
                     f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
         if (hh == 0)
             *(f32x2 *)(a.part_ml + 2 * slot) = f32x2{m, l};
+    }
+    return it.total;
+}
+
+// Over pages: item and kv head bx, and every wide_x-th after it (wide_x: a multiple of the kv heads).
+template <int D, int SRC>
+__device__ __forceinline__ void attn_wide_pages(const AttnArgs &a, int bx, int by, int wide_x, uint8_t *smem)
+{
+    for (int64_t x = bx;; x += wide_x) {
+        const int total = attn_wide_body<D, SRC, 1, true>(a, (int)x, by, smem);
+        if (x + wide_x >= (int64_t)total * a.hkv)
+            return;
+        __syncthreads();
     }
 }
 

@@ -640,3 +640,25 @@ WHOLE_OR_SHARED = [
 @pytest.mark.parametrize("case", WHOLE_OR_SHARED, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-60:])
 def test_paged_whole_or_shared(m, case, poison):
     test_paged(m, case, poison)
+
+
+MANY_ITEMS = [
+    # more row blocks than workgroups launched for them: 100 sequences of 5 tokens among 300 of one (in one kernel),
+    # their keys cut into chunks or not, and with windows
+    ([(1, 1 + i % 50) for i in range(300)] + [(5, 5 + i % 60) for i in range(100)], 64, 16, 64, 16, False, True, 0),
+    ([(1, 1 + i % 50) for i in range(300)] + [(5, 5 + i % 60) for i in range(100)], 64, 16, 64, 16, True, True, 0),
+    ([(17, 17 + 3 * i) if i % 5 == 0 else (1, 1 + i % 40) for i in range(200)], 32, 32, 128, 32, False, True, 0),
+    ([(17, 17 + 7 * i % 400) if i % 9 == 4 else (1, 900) for i in range(170)], 24, 24, 64, 16, False, True, 150),
+    ([(130, 300), (0, 0), (1, 40)] + [(1, 1 + i) for i in range(90)] + [(260, 260), (1, 7)], 8, 2, 128, 16, True, True, 0),
+]
+
+
+@pytest.mark.parametrize("poison", [False, True], ids=["", "poison"])
+@pytest.mark.parametrize("case", MANY_ITEMS, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-60:])
+def test_paged_many_items(m, case, poison):
+    test_paged(m, case, poison)
+
+
+def test_many_prompts(m):
+    """More than 64 x 64 sequences: a lane counts more than one wave's worth."""
+    test_prompts(m, ([1 + i % 3 for i in range(4200)] + [140], None, 1, 1, 64, True, 0))
