@@ -1,8 +1,8 @@
 // The mixed batch over pages: chunks of new tokens (attn_wide_body.h) and decode rows (attn_decode_body.h) in one
 // launch.  The former are bound by the matrix cores, the latter by memory, and a CU holds two workgroups of either
 // kind; so the launch begins with one of each on every CU and goes on with both in turn (256 tokens with contexts of
-// 64 to 2048 and a chunk of 2048 tokens after 6000: 391 us, one kernel after the other 449; with contexts of 1000
-// and a chunk over 8192 379 us against 438).
+// 64 to 2048 and a chunk of 2048 tokens after 6000: 364 us, one kernel after the other 447; with contexts of 1000
+// and a chunk over 8192 357 us against 432).
 #include "attn_decode_body.h"
 #include "attn_wide_body.h"
 
@@ -20,7 +20,7 @@ __global__ __launch_bounds__(256, 2) void attn_mixed_kernel(AttnArgs w, AttnArgs
     __shared__ __attribute__((aligned(16))) uint8_t smem[LDS];
     // the first 256 of the wide ones, the first 256 of the others, then groups of each in turn.  Workgroups go to the 8
     // XCDs, and within one to its shader engines and their CUs, in turn: smaller groups would give each kind to some
-    // of them alone.
+    // of them alone (groups of 8: a chunk of 2048 with empty shares between 319 us, groups of 256 232).
     constexpr uint32_t GROUP = 256;
     const uint32_t wide = wide_x * w.n_chunks, w0 = min(wide, (uint32_t)CUS), d0 = min(shares, (uint32_t)CUS);
     uint32_t i = blockIdx.x;
