@@ -139,7 +139,8 @@ __device__ __forceinline__ int ad_swz(int key)
 }
 
 template <int D, int NQ>
-constexpr int decode_lds = 4 * 2 * (32 * D > 32 * (D + 4) ? 32 * D : 32 * (D + 4)) + 4 * 16 * 2 * 4 + (NQ > 1 ? 16 * NQ * D * 2 : 0);
+constexpr int decode_lds = 4 * 2 * (32 * D > 32 * (D + 4) ? 32 * D : 32 * (D + 4)) + 4 * 16 * 2 * 4 +
+                           (NQ > 1 ? 16 * NQ * D * 2 : 0);
 
 // Share `share` of `shares` (or sequence and head `share`, see launch_attn_decode); smem: decode_lds bytes.
 template <int D, int NQ, bool FP8>
@@ -206,7 +207,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         auto load = [&](int kb) {
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const int64_t at = (((int64_t)clamp_page(uniform(pg[u]), a.cache.n_pages) * a.cache.hkv + head) << ps) + ((kb + 16 * u) & pm);
+                const int page = clamp_page(uniform(pg[u]), a.cache.n_pages);
+                const int64_t at = (((int64_t)page * a.cache.hkv + head) << ps) + ((kb + 16 * u) & pm);
                 const uint8_t *kp = a.cache.k + at * D * ESZ, *vp = a.cache.v + at * D * ESZ;
 #pragma unroll
                 for (int s = 0; s < LD; ++s)
@@ -246,7 +248,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
             } else if (wave == j) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
-                    *(u32x4 *)(ql + (16 * j + col) * D + 8 * (qpiece(s) ^ (col & (D / 8 - 1)))) = *(const u32x4 *)(qr + 8 * qpiece(s));
+                    *(u32x4 *)(ql + (16 * j + col) * D + 8 * (qpiece(s) ^ (col & (D / 8 - 1)))) =
+                        *(const u32x4 *)(qr + 8 * qpiece(s));
             }
         }
         if (NQ > 1)
@@ -421,7 +424,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                             f[i] &= i == (e >> 1) ? half : 0u;
 #pragma unroll
                         for (int j = 0; j < NQ; ++j) {
-                            const f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f), as_bf16x8(pf[j]), o[j][d], 0, 0, 0);
+                            const f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f), as_bf16x8(pf[j]),
+                                                                                    o[j][d], 0, 0, 0);
                             const bool see = ka < L && (!a.causal || ka <= pos[j]) &&
                                              (a.window <= 0 || ka > pos[j] - a.window);
 #pragma unroll

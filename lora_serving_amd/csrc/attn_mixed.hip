@@ -54,7 +54,8 @@ hipError_t launch_attn_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim,
     if (blocks > 0x7fffffff)
         return hipErrorInvalidValue;
     const bool more = wide_launched(w) < wide_items(w);
-#define MIX(D, F, M) attn_mixed_kernel<D, F, M><<<dim3((unsigned)blocks), dim3(256), 0, stream>>>(w, d, (uint32_t)wide_x, (uint32_t)shares)
+    const dim3 grid((unsigned)blocks);
+#define MIX(D, F, M) attn_mixed_kernel<D, F, M><<<grid, dim3(256), 0, stream>>>(w, d, (uint32_t)wide_x, (uint32_t)shares)
 #define MIX_M(D, F) (more ? MIX(D, F, true) : MIX(D, F, false))
 #define MIX_F(D) (d.cache.fp8 ? MIX_M(D, true) : MIX_M(D, false))
     head_dim == 64 ? MIX_F(64) : MIX_F(128);

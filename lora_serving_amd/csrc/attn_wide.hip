@@ -56,9 +56,13 @@ hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStre
     const int64_t keys = a.cu_k ? a.Tk : a.max_q, span = a.window > 0 ? std::min<int64_t>(keys, a.window) : keys;
     const bool halves = items * a.hkv <= CUS && span >= 8 * AW_BN;
 #define AW(D, SRC, KG) attn_wide_kernel<D, SRC, KG><<<grid, dim3(KG * 256), 0, stream>>>(a)
-#define AW_S(D) (!pages ? halves ? AW(D, AW_ROWS, 2) : AW(D, AW_ROWS, 1) : a.cache.fp8 ? AW(D, AW_PAGES_E4M3, 1) : AW(D, AW_PAGES, 1))
+#define AW_R(D) (halves ? AW(D, AW_ROWS, 2) : AW(D, AW_ROWS, 1))
+#define AW_P(D) (a.cache.fp8 ? AW(D, AW_PAGES_E4M3, 1) : AW(D, AW_PAGES, 1))
+#define AW_S(D) (pages ? AW_P(D) : AW_R(D))
     head_dim == 64 ? AW_S(64) : AW_S(128);
 #undef AW_S
+#undef AW_P
+#undef AW_R
 #undef AW
     return hipGetLastError();
 }

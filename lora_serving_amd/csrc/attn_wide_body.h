@@ -211,7 +211,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     for (int i = 0; i < IPW; ++i) {
         const int r = RPI * i + crow;
         piece[i] = 16 * (FP8 ? cpiece : cpiece ^ aw_swz<D>(r));
-        off_k[i] = piece[i] + (SRC == AW_ROWS ? (uint32_t)(w16 + r) * (uint32_t)(2 * a.k_stride) : (uint32_t)r * D * (FP8 ? 1 : 2));
+        off_k[i] = piece[i] + (SRC == AW_ROWS ? (uint32_t)(w16 + r) * (uint32_t)(2 * a.k_stride)
+                                              : (uint32_t)r * D * (FP8 ? 1 : 2));
         off_v[i] = SRC == AW_ROWS ? piece[i] + (uint32_t)(w16 + r) * (uint32_t)(2 * a.v_stride) : off_k[i];
     }
     const uint16_t *kp = a.k + ((int64_t)key0 + (int64_t)t0 * BN) * a.k_stride + (int64_t)h * D;   // rows: the next tile
@@ -407,7 +408,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
         u32x4 f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {       // keys 16 s + 8 u + vk, values 32 d ..
-            const u32x2 w = lds_read_tr((const uint16_t *)((const uint8_t *)(lds + 2 * TILE) + (at ^ (64 * d + 32 * u)) + (16 * u + 32 * s) * D));
+            const uint8_t *v = (const uint8_t *)(lds + 2 * TILE) + (at ^ (64 * d + 32 * u)) + (16 * u + 32 * s) * D;
+            const u32x2 w = lds_read_tr((const uint16_t *)v);
             f[2 * u] = w[0];
             f[2 * u + 1] = w[1];
         }
@@ -438,7 +440,10 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
                 f[i % AHEAD][e] = i < KS ? kfrag(ka, i, e) : vfrag(va, 2 * (i - KS) / DB, 2 * (i - KS) % DB + e);
         };
         // powers that are done after step i
-        auto done = [](int i) { return D == 128 ? (i < 8 ? (i + 1) / 2 * 2 : i < 12 ? 2 * i - 6 : 16) : i < 4 ? 2 * i + 2 : i < 6 ? 4 * i - 4 : 16; };
+        auto done = [](int i) {
+            return D == 128 ? (i < 8 ? (i + 1) / 2 * 2 : i < 12 ? 2 * i - 6 : 16)
+                            : (i < 4 ? 2 * i + 2 : i < 6 ? 4 * i - 4 : 16);
+        };
 #pragma unroll
         for (int i = 0; i < AHEAD; ++i)
             read(i);
@@ -538,7 +543,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
                 keep[i] = ((mine >> (8 * s + 2 * i)) & 1 ? 0u : 0xffffu) | ((mine >> (8 * s + 2 * i + 1)) & 1 ? 0u : 0xffff0000u);
 #pragma unroll
             for (int d = 0; d < DB; ++d)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d) & keep), as_bf16x8(pf[s]), o[d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d) & keep), as_bf16x8(pf[s]), o[d],
+                                                               0, 0, 0);
         }
     };
     // a tile on its own (K of it in place before; afterwards K of the next)
@@ -658,7 +664,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
         for (int j = 0; j < 32 * CPR / 64; ++j) {
             const int r = j * (64 / CPR) + lane / CPR, piece = lane & (CPR - 1);
             const u32x4 w = *(const u32x4 *)(part + r * D + 8 * (piece ^ (r & (CPR - 1))));
-            const int64_t at = (int64_t)((uint64_t)(uint32_t)__shfl((int)(to >> 32), r, 64) << 32 | (uint32_t)__shfl((int)to, r, 64));
+            const int64_t at = (int64_t)((uint64_t)(uint32_t)__shfl((int)(to >> 32), r, 64) << 32 |
+                                         (uint32_t)__shfl((int)to, r, 64));
             if (wrow + r < rows)
                 *(u32x4 *)(a.out + at + 8 * piece) = w;
         }
