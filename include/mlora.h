@@ -403,7 +403,9 @@ mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int
  * Attention of new tokens over a paged cache that already holds them (mlora_qk_rope first):
  * sequence b owns query rows [cu_q[b], cu_q[b+1]) and kv_len[b] cached tokens, token j in page
  * page_table[b][j / page_size].  Semantics as mlora_attention with L = kv_len[b]; decode is one
- * query row a sequence, and decode rows and prefill chunks may share a call.
+ * query row a sequence, and decode rows and prefill chunks may share a call.  Sequences of up to 16
+ * rows (queries x heads of a kv head's group) keep 2^-15 of a probability instead of bf16's 2^-8,
+ * but in calls whose max_q gives 17 to 32 rows.
  *   page_table int32 [n_seqs][table_stride] device; kv_len int32 [n_seqs] device, read as at
  *       most table_stride * page_size and max_kv
  *   max_q, max_kv  host upper bounds of the query counts and of kv_len (they size the launch;

@@ -150,6 +150,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
     constexpr int KS = D / 32;          // k-steps of the first product
     constexpr int DB = D / 16;          // row blocks of the second
     constexpr int LD = FP8 ? D / 64 : D / 32;   // 16-byte loads per lane and 16-key block
+    constexpr int PARTS = NQ == 1 ? 2 : 1;      // bf16 parts of a probability
     constexpr int OS = D + 4;           // row stride of the joined accumulators in LDS
     constexpr int VW = 32 * D;          // a wave's V rows in LDS
     constexpr int NW = 4, STEP = 32 * NW;       // waves; keys they take at a time
@@ -344,7 +345,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                 if (kb + 2 * STEP < k1)
                     lookup(kb + 2 * STEP);
             }
-            u32x4 pf[NQ];
+            u32x4 pf[PARTS][NQ];
 #pragma unroll
             for (int j = 0; j < NQ; ++j) {
                 if (edge)
@@ -384,10 +385,27 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                         // (a masked key's scale may be anything)
                         p[4 * u + i] = !FP8 ? e : edge && st[j][u][i] == -INFINITY ? 0.f : e * vss[u][i];
                     }
-                // P^T rounded to bf16 (half a step: 2^-8 relative) for the matrix cores; the sum keeps fp32
+                // P^T for the matrix cores; the sum keeps fp32.  One column tile: as two bf16 parts, which memory leaves
+                // the time for (48 batches: 0.6% slower at the median, long ones 2% at most), the first cut off below p (a step
+                // of 2^-7), the rest rounded (2^-15 of p); both are positive where p is, so an infinite V stays that
+                // infinity.  Two tiles: rounded to bf16 (half a step: 2^-8 relative), for two parts take registers and
+                // products that are not there (32 x 8 tokens over 4096 keys 156 us, so 137; e4m3 75 and 70).
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    pf[j][i] = cvt_bf16x2(p[2 * i], p[2 * i + 1]);
+                for (int i = 0; i < 4; ++i) {
+                    if (PARTS == 1) {
+                        pf[0][j][i] = cvt_bf16x2(p[2 * i], p[2 * i + 1]);
+                        continue;
+                    }
+                    uint32_t hi[2];
+                    float lo[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        hi[e] = __builtin_elementwise_sub_sat(__float_as_uint(p[2 * i + e]), 1u) & 0xffff0000u;
+                        lo[e] = p[2 * i + e] - __uint_as_float(hi[e]);
+                    }
+                    pf[0][j][i] = hi[0] >> 16 | hi[1];
+                    pf[PARTS - 1][j][i] = cvt_bf16x2(lo[0], lo[1]);
+                }
             }
             // O^T += V^T P^T; k index (g, e) is key 16 (e / 4) + 4 g + e % 4
             uint32_t rl = rlane;
@@ -424,8 +442,10 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                             f[i] &= i == (e >> 1) ? half : 0u;
 #pragma unroll
                         for (int j = 0; j < NQ; ++j) {
-                            const f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f), as_bf16x8(pf[j]),
-                                                                                    o[j][d], 0, 0, 0);
+                            f32x4 t = o[j][d];
+#pragma unroll
+                            for (int w = 0; w < PARTS; ++w)
+                                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f), as_bf16x8(pf[w][j]), t, 0, 0, 0);
                             const bool see = ka < L && (!a.causal || ka <= pos[j]) &&
                                              (a.window <= 0 || ka > pos[j] - a.window);
 #pragma unroll
@@ -441,8 +461,10 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
             for (int d = 0; d < DB; ++d) {
                 const bf16x8 vf = as_bf16x8(vfrag(d));
 #pragma unroll
-                for (int j = 0; j < NQ; ++j)
-                    o[j][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, as_bf16x8(pf[j]), o[j][d], 0, 0, 0);
+                for (int w = 0; w < PARTS; ++w)
+#pragma unroll
+                    for (int j = 0; j < NQ; ++j)
+                        o[j][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, as_bf16x8(pf[w][j]), o[j][d], 0, 0, 0);
                 if (d & 1)
                     __builtin_amdgcn_sched_barrier(0);      // (not all fragments at once: registers)
             }
