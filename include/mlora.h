@@ -411,7 +411,8 @@ mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int
  *   max_q, max_kv  host upper bounds of the query counts and of kv_len (they size the launch;
  *       sequences with more queries than max_q are left unanswered)
  *   ws  mlora_paged_workspace_size() bytes for the same sizes
- * max_kv and T are below 2^30, T * n_q_heads and n_seqs * n_kv_heads * (max_kv / 128 + 1) below 2^31.
+ * max_kv and T are below 2^30, T * n_q_heads and n_seqs * n_kv_heads * (max_kv / 128 + 1) below 2^31;
+ * mlora_paged_workspace_size gives 0 where the call would refuse its sizes.
  * A page number outside the cache is read as its nearest valid page (no fault; such sequences'
  * results are meaningless): mlora_validate_pages checks a batch's tables on the host.
  */

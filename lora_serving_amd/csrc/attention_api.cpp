@@ -64,6 +64,13 @@ mlora_status check_cache(const mlora_cache *c, CacheGeom *g)
     return MLORA_OK;
 }
 
+// Sizes of a paged call (none negative) that the plan and the kernels hold in 32 bits.
+bool paged_sizes_ok(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int64_t max_kv)
+{
+    return T < MAX_KEYS && T * hq < MAX_ROWS && max_kv < MAX_KEYS && (int64_t)n_seqs * hkv < MAX_ROWS &&
+           (int64_t)n_seqs * hkv * (max_kv / DECODE_UNIT + 1) < MAX_ROWS;
+}
+
 bool rows_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
 
 // A window that no sequence is longer than hides nothing (and is left out, so that positions minus the window
@@ -312,7 +319,8 @@ size_t mlora_paged_workspace_size(int64_t T, int32_t n_seqs, int32_t n_q_heads, 
                                   int32_t head_dim, int64_t max_q, int64_t max_kv)
 {
     if (T < 0 || n_seqs < 0 || max_q < 0 || max_kv < 0 ||
-        check_heads(n_q_heads, n_kv_heads, head_dim) != MLORA_OK || T * n_q_heads >= MAX_ROWS)
+        check_heads(n_q_heads, n_kv_heads, head_dim) != MLORA_OK ||
+        !paged_sizes_ok(T, n_seqs, n_q_heads, n_kv_heads, max_kv))
         return 0;
     return paged_plan(T, n_seqs, n_q_heads, n_kv_heads, head_dim, std::min(max_q, T), max_kv).total() + 256;
 }
@@ -336,9 +344,7 @@ mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, i
         return st;
     if (!rows_ok(q_stride, (int64_t)n_q_heads * d) || !rows_ok(out_stride, (int64_t)n_q_heads * d))
         return MLORA_ERR_SHAPE;
-    if (T >= MAX_KEYS || T * n_q_heads >= MAX_ROWS || max_kv >= MAX_KEYS ||
-        (int64_t)n_seqs * cache->n_kv_heads >= MAX_ROWS || table_stride >= MAX_ROWS ||
-        (int64_t)n_seqs * cache->n_kv_heads * (max_kv / DECODE_UNIT + 1) >= MAX_ROWS)
+    if (!paged_sizes_ok(T, n_seqs, n_q_heads, cache->n_kv_heads, max_kv) || table_stride >= MAX_ROWS)
         return MLORA_ERR_UNSUPPORTED;
     if (T == 0 || n_seqs == 0 || max_q == 0)
         return MLORA_OK;

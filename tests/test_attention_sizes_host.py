@@ -1,0 +1,34 @@
+"""Sizes of the attention step's host helpers (nothing here touches a GPU)."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def m():
+    from lora_serving_amd import mlora
+    return mlora
+
+
+def paged_call(m, T, n_seqs, hq, hkv, d, max_q, max_kv):
+    """The paged call for these sizes with a workspace of no bytes: refused before any launch."""
+    c = m.mlora_cache(0x10000, 0x10000, None, None, 8, hkv, 16, d, 0)
+    return m._lib.mlora_paged_attention(0x10000, hq * d, T, hq, ctypes.byref(c), 0x10000, 1 << 26, n_seqs, 0x10000,
+                                        0x10000, max_q, max_kv, 1, 0, 0.0, 0x10000, hq * d, None, None, 0, None)
+
+
+# T, n_seqs, max_q, max_kv at 32 heads on 8 that the call does not take, some past 64-bit products
+REFUSED = [(1 << 30, 4, 1, 64), (1 << 26, 4, 1, 64), (1 << 61, 4, 1, 64), (1 << 58, 1, 1, 64), (4, 4, 1, 1 << 30),
+           (4, 4, 1, 1 << 40), (4, 4, 1, 2 ** 63 - 1), (2 ** 63 - 1, 4, 2 ** 63 - 1, 2 ** 63 - 1),
+           (4, 1 << 28, 1, 64), (4, 2 ** 31 - 1, 1, 64), (4, 1 << 20, 1, (1 << 30) - 1)]
+
+
+@pytest.mark.parametrize("T,n,mq,mk", REFUSED)
+def test_no_workspace_size_for_refused_sizes(m, T, n, mq, mk):
+    assert paged_call(m, T, n, 32, 8, 128, mq, mk) == m.MLORA_ERR_UNSUPPORTED
+    assert m._lib.mlora_paged_workspace_size(T, n, 32, 8, 128, mq, mk) == 0
+
+
+def test_workspace_size_at_the_limits(m):
+    for T, n, mq, mk in ((4, 4, 1, (1 << 30) - 1), ((1 << 26) - 1, 1, 1, 64), (4, (1 << 27) - 1, 1, 1)):
+        assert m._lib.mlora_paged_workspace_size(T, n, 32, 8, 128, mq, mk) >= 256
