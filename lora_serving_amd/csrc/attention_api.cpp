@@ -33,7 +33,7 @@ mlora_status check_cache_sizes(int64_t n_pages, int32_t hkv, int32_t page_size, 
         return MLORA_ERR_ARG;
     if (page_size < 16 || page_size > MLORA_MAX_PAGE || (page_size & (page_size - 1)) || !head_dim_ok(d) ||
         hkv > MLORA_MAX_HEADS || (dtype != MLORA_CACHE_BF16 && dtype != MLORA_CACHE_E4M3) ||
-        n_pages * page_size >= MAX_ROWS)
+        n_pages >= MAX_ROWS / page_size)
         return MLORA_ERR_UNSUPPORTED;
     return MLORA_OK;
 }

@@ -32,3 +32,10 @@ def test_no_workspace_size_for_refused_sizes(m, T, n, mq, mk):
 def test_workspace_size_at_the_limits(m):
     for T, n, mq, mk in ((4, 4, 1, (1 << 30) - 1), ((1 << 26) - 1, 1, 1, 64), (4, (1 << 27) - 1, 1, 1)):
         assert m._lib.mlora_paged_workspace_size(T, n, 32, 8, 128, mq, mk) >= 256
+
+
+def test_cache_bytes_of_too_many_pages(m):
+    assert m.mlora_cache_bytes((1 << 27) - 1, 8, 16, 128) == 2 * ((1 << 27) - 1) * 8 * 16 * 128 * 2
+    for pages in (1 << 27, 1 << 59, 1 << 60, (1 << 60) + 1, 2 ** 63 - 1):
+        assert m.mlora_cache_bytes(pages, 8, 16, 128) == -1
+        assert m.mlora_cache_bytes(pages, 8, 256, 64, m.MLORA_CACHE_E4M3) == -1
