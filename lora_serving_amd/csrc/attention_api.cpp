@@ -413,6 +413,8 @@ mlora_status mlora_validate_pages(const mlora_cache *cache, const int32_t *page_
         check_cache_sizes(cache->n_pages, cache->n_kv_heads, cache->page_size, cache->head_dim, cache->dtype);
     if (st != MLORA_OK)
         return st;
+    if (table_stride >= MAX_ROWS)
+        return MLORA_ERR_UNSUPPORTED;
     if (cu_q == nullptr || (n_seqs > 0 && kv_len == nullptr))
         return MLORA_ERR_ARG;
     const auto bad = [bad_value](mlora_status s, int64_t v) {

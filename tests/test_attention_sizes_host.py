@@ -1,6 +1,7 @@
 """Sizes of the attention step's host helpers (nothing here touches a GPU)."""
 import ctypes
 
+import numpy as np
 import pytest
 
 
@@ -39,3 +40,15 @@ def test_cache_bytes_of_too_many_pages(m):
     for pages in (1 << 27, 1 << 59, 1 << 60, (1 << 60) + 1, 2 ** 63 - 1):
         assert m.mlora_cache_bytes(pages, 8, 16, 128) == -1
         assert m.mlora_cache_bytes(pages, 8, 256, 64, m.MLORA_CACHE_E4M3) == -1
+
+
+def test_validate_pages_of_too_wide_tables(m):
+    """A table stride that the call refuses is refused, not multiplied past 64 bits."""
+    c = m.mlora_cache(0x10000, 0x10000, None, None, 8, 2, 256, 64, 0)
+    table, cu, lens = np.zeros(4, np.int32), np.array([0, 1], np.int32), np.array([5], np.int32)
+    p = lambda a: a.ctypes.data_as(ctypes.c_void_p)  # noqa: E731
+    for stride in (1 << 31, 1 << 55, 1 << 56, 1 << 60):
+        assert m._lib.mlora_validate_pages(ctypes.byref(c), p(table), stride, 1, p(cu), p(lens), 1, 1, 64,
+                                           None) == m.MLORA_ERR_UNSUPPORTED
+    assert m._lib.mlora_validate_pages(ctypes.byref(c), p(table), (1 << 31) - 1, 1, p(cu), p(lens), 1, 1, 64,
+                                       None) == m.MLORA_OK
