@@ -79,6 +79,30 @@ int32_t seen_window(int32_t window, int64_t max_keys) { return window >= max_key
 
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
+// Bytes of the parts of the decode kernel: two slots of `rows` rows a share.
+void decode_parts(int64_t shares, int64_t rows, int32_t d, size_t *o, size_t *ml)
+{
+    const size_t slots = (size_t)shares * 2 * rows;
+    *o = align_up(slots * d * 4);
+    *ml = align_up(slots * 8);
+}
+
+// And of the wide kernel's: one row a token, head and chunk of keys.
+void wide_parts(int64_t T, int32_t hq, int64_t chunks, int32_t d, size_t *o, size_t *ml)
+{
+    const size_t slots = (size_t)T * hq * chunks;
+    *o = align_up(slots * d * 4);
+    *ml = align_up(slots * 8);
+}
+
+// Chunks of keys of the wide kernel: as many as make WIDE_WANT workgroups, of WIDE_LEAST keys or more; not cut from
+// WIDE_WHOLE workgroups on.
+constexpr int64_t WIDE_WHOLE = 192, WIDE_WANT = 512, WIDE_LEAST = 256;
+int64_t wide_cuts(int64_t items, int64_t max_kv)
+{
+    return std::max<int64_t>(1, std::min((WIDE_WANT + items - 1) / items, (max_kv + WIDE_LEAST - 1) / WIDE_LEAST));
+}
+
 // How a paged call is cut: which kernels run, and the chunks of keys that give each enough
 // workgroups.  Made from the sizes alone, so that the workspace can be sized before the call.
 struct PagedPlan {
@@ -96,12 +120,6 @@ PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t
     PagedPlan p;
     const int64_t group = hq / hkv, most = max_q * group;
     max_kv = std::max<int64_t>(max_kv, 1);
-    const auto cut = [max_kv](int64_t items, int64_t want, int64_t least, int64_t *chunk, int64_t *count) {
-        // the fewest chunks that make `want` workgroups, of at least `least` keys
-        const int64_t n = std::max<int64_t>(1, std::min((want + items - 1) / items, (max_kv + least - 1) / least));
-        *chunk = ((max_kv + n - 1) / n + 127) & ~INT64_C(127);
-        *count = (max_kv + *chunk - 1) / *chunk;
-    };
     if (most <= 32) {
         p.dec_rows = most;
         p.nq = most <= 16 ? 1 : 2;
@@ -120,28 +138,45 @@ PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t
         const int64_t items = (int64_t)n_seqs * hkv, units = (max_kv + DECODE_UNIT - 1) / DECODE_UNIT;
         p.split = units > (items >= CUS ? 8 : 4);
         p.shares = (int)(p.split ? std::min(items * units, (int64_t)decode_slots(d, p.nq) * CUS) : items);
-        if (p.split) {
-            const size_t slots = (size_t)p.shares * 2 * p.dec_rows;
-            p.dec_o = align_up(slots * d * 4);
-            p.dec_ml = align_up(slots * 8);
-        }
+        if (p.split)
+            decode_parts(p.shares, p.dec_rows, d, &p.dec_o, &p.dec_ml);
     }
     if (p.wide) {
         // row blocks: as many as the rows fill, or one a sequence where there are rows enough for all of them to
         // come here (100 sequences of 40 rows over 1500 keys: 94 us in chunks, 67 whole)
         const bool all = T * group > n_seqs * p.dec_rows;
         const int64_t items = std::max<int64_t>((T * group + WIDE_ROWS - 1) / WIDE_ROWS, all ? n_seqs : 0) * hkv;
-        if (items >= 192)
-            p.wide_chunk = (max_kv + 127) & ~INT64_C(127), p.wide_chunks = 1;
-        else
-            cut(items, 512, 256, &p.wide_chunk, &p.wide_chunks);
-        if (p.wide_chunks > 1) {
-            const size_t slots = (size_t)T * hq * p.wide_chunks;
-            p.wide_o = align_up(slots * d * 4);
-            p.wide_ml = align_up(slots * 8);
-        }
+        const int64_t n = items >= WIDE_WHOLE ? 1 : wide_cuts(items, max_kv);
+        p.wide_chunk = ((max_kv + n - 1) / n + 127) & ~INT64_C(127);
+        p.wide_chunks = (max_kv + p.wide_chunk - 1) / p.wide_chunk;
+        if (p.wide_chunks > 1)
+            wide_parts(T, hq, p.wide_chunks, d, &p.wide_o, &p.wide_ml);
     }
     return p;
+}
+
+// The most that paged_plan asks for over all T, n_seqs, max_q and max_kv up to these: a larger batch is cut less, and
+// needs fewer parts, so that the plan's own bytes fall here and there as a size rises.
+size_t paged_room(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv)
+{
+    const int64_t group = hq / hkv, most = max_q * group, units = (max_kv + DECODE_UNIT - 1) / DECODE_UNIT;
+    size_t dec = 0, wide = 0, o, ml;
+    for (int nq = 1; nq <= 2 && units > 4; ++nq) {
+        if (nq == 2 && most <= 16)
+            break;
+        decode_parts(std::min((int64_t)n_seqs * hkv * units, (int64_t)decode_slots(d, nq) * CUS),
+                     std::min<int64_t>(most, 16 * nq), d, &o, &ml);
+        dec = std::max(dec, o + ml);
+    }
+    // r row blocks: the tokens that fill them, cut the finer the fewer they are
+    for (int64_t r = 1; most > 32 && r * hkv < WIDE_WHOLE && (r - 1) * WIDE_ROWS < T * group; ++r) {
+        const int64_t cuts = wide_cuts(r * hkv, max_kv);
+        if (cuts > 1) {
+            wide_parts(std::min(T, r * WIDE_ROWS / group), hq, cuts, d, &o, &ml);
+            wide = std::max(wide, o + ml);
+        }
+    }
+    return dec + wide;
 }
 
 }  // namespace
@@ -322,7 +357,7 @@ size_t mlora_paged_workspace_size(int64_t T, int32_t n_seqs, int32_t n_q_heads, 
         check_heads(n_q_heads, n_kv_heads, head_dim) != MLORA_OK ||
         !paged_sizes_ok(T, n_seqs, n_q_heads, n_kv_heads, max_kv))
         return 0;
-    return paged_plan(T, n_seqs, n_q_heads, n_kv_heads, head_dim, std::min(max_q, T), max_kv).total() + 256;
+    return paged_room(T, n_seqs, n_q_heads, n_kv_heads, head_dim, std::min(max_q, T), max_kv) + 256;
 }
 
 mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads,

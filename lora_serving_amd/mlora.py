@@ -503,7 +503,7 @@ def mlora_paged_workspace_size(T: int, n_seqs: int, n_q_heads: int, n_kv_heads: 
 
 def paged_workspace(T: int, n_seqs: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
                     max_q: int, max_kv: int, device="cuda"):
-    """A workspace of mlora_paged_workspace_size() bytes."""
+    """A workspace of mlora_paged_workspace_size() bytes, for calls of these sizes and of smaller ones."""
     import torch
     n = mlora_paged_workspace_size(T, n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_kv)
     if n == 0:

@@ -52,3 +52,28 @@ def test_validate_pages_of_too_wide_tables(m):
                                            None) == m.MLORA_ERR_UNSUPPORTED
     assert m._lib.mlora_validate_pages(ctypes.byref(c), p(table), (1 << 31) - 1, 1, p(cu), p(lens), 1, 1, 64,
                                        None) == m.MLORA_OK
+
+
+HEADS = [(32, 8, 128), (32, 8, 64), (8, 8, 128), (64, 2, 64), (40, 1, 128), (1024, 1, 64), (6, 3, 128), (16, 1, 64)]
+
+
+@pytest.mark.parametrize("hq,hkv,d", HEADS)
+def test_workspace_of_the_largest_batch_serves_smaller_ones(m, hq, hkv, d):
+    """The size does not fall as any of T, n_seqs, max_q or max_kv rises."""
+    size = lambda *a: m._lib.mlora_paged_workspace_size(a[0], a[1], hq, hkv, d, a[2], a[3])  # noqa: E731
+    r = np.random.default_rng(hq * 7 + hkv + d)
+    log = lambda hi: int(np.exp(r.uniform(0, np.log(hi + 1))))  # noqa: E731
+    for _ in range(300):
+        T, n, mk = log(20000), log(2000), log(200000)
+        mq = log(T)
+        top = size(T, n, mq, mk)
+        assert top > 0
+        for _ in range(40):
+            low = [min(v, log(v)) if r.random() < 0.7 else v for v in (T, n, mq, mk)]
+            assert size(*low) <= top, (T, n, mq, mk, low)
+
+
+def test_workspace_sizes_stay_small(m):
+    """A bound over all smaller batches, not a product of the largest sizes."""
+    for hq, hkv, d in HEADS:
+        assert m._lib.mlora_paged_workspace_size(100000, 4096, hq, hkv, d, 100000, 200000) < 192 << 20
