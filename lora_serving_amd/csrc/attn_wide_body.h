@@ -31,11 +31,11 @@ enum { AW_ROWS = 0, AW_PAGES = 1, AW_PAGES_E4M3 = 2 };
 // One 16-byte copy a lane from global memory (a scalar base and a byte offset of the lane) straight into
 // LDS: 64 lanes fill 1 KB at byte `to` + `more` of it.  In asm, so that the compiler does not drain the
 // copies in flight before each LDS read (it cannot tell the buffers apart); every copy is waited for by
-// hand.  (Nothing else here uses m0.)
+// hand.
 __device__ __forceinline__ void aw_dma(const void *base, uint32_t off, uint32_t to, int more)
 {
     asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-                 :: "v"(off), "s"(base), "s"(to), "i"(more) : "memory", "scc");
+                 :: "v"(off), "s"(base), "s"(to), "i"(more) : "memory", "scc", "m0");
 }
 
 // Swizzle of the 16-byte pieces of a row by its key, a bijection for reads of one piece over 16 keys
