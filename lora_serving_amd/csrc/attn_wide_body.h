@@ -31,12 +31,16 @@ enum { AW_ROWS = 0, AW_PAGES = 1, AW_PAGES_E4M3 = 2 };
 // One 16-byte copy a lane from global memory (a scalar base and a byte offset of the lane) straight into
 // LDS: 64 lanes fill 1 KB at byte `to` + `more` of it.  In asm, so that the compiler does not drain the
 // copies in flight before each LDS read (it cannot tell the buffers apart); every copy is waited for by
-// hand.
+// hand.  The compiler keeps no value in m0 but sets it before each use of its own: naming it orders the
+// statement against those (clang 22 of ROCm 7.2 warns of the name as of any reserved register).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void aw_dma(const void *base, uint32_t off, uint32_t to, int more)
 {
     asm volatile("s_add_u32 m0, %2, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
                  :: "v"(off), "s"(base), "s"(to), "i"(more) : "memory", "scc", "m0");
 }
+#pragma clang diagnostic pop
 
 // Swizzle of the 16-byte pieces of a row by its key, a bijection for reads of one piece over 16 keys
 // (K, ds_read_b128) that also spreads a transposing read's 4 keys x 64 bytes (V) over all banks.
