@@ -54,8 +54,24 @@ int32_t int32(PyObject *o, const char *name)
     return (int32_t)v;
 }
 
-template <class T> const T *address(PyObject *o) { return o == Py_None ? nullptr : (const T *)PyLong_AsVoidPtr(o); }
-hipStream_t stream(PyObject *o) { return (hipStream_t)PyLong_AsVoidPtr(o); }
+bool truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw std::runtime_error("");
+    return v != 0;
+}
+
+void *pointer(PyObject *o)
+{
+    void *p = PyLong_AsVoidPtr(o);
+    if (p == nullptr && PyErr_Occurred())
+        throw std::runtime_error("");
+    return p;
+}
+
+template <class T> const T *address(PyObject *o) { return o == Py_None ? nullptr : (const T *)pointer(o); }
+hipStream_t stream(PyObject *o) { return (hipStream_t)pointer(o); }
 
 void *dense(PyObject *o, const char *name, ScalarType type, const char *type_name)
 {
@@ -172,7 +188,7 @@ mlora_status attention(PyObject *const *a)
     const int64_t n = tensor(a[3], "cu_q").numel() - 1;
     return mlora_attention(q.p, q.stride, k.p, k.stride, v.p, v.stride, q.n, k.n, (int32_t)n, ints(a[3], "cu_q", n + 1),
                            a[5] == Py_None ? nullptr : ints(a[5], "cu_k", n + 1), (int32_t)q.heads, (int32_t)k.heads, (int32_t)q.d,
-                           a[6] == Py_None ? q.n : integer(a[6]), PyObject_IsTrue(a[7]), int32(a[8], "window"), (float)real(a[9]),
+                           a[6] == Py_None ? q.n : integer(a[6]), truth(a[7]), int32(a[8], "window"), (float)real(a[9]),
                            out.p, out.stride, lse_of(a[10], q.n, q.heads), stream(a[11]));
 }
 
@@ -198,7 +214,7 @@ mlora_status paged_attention(PyObject *const *a)
     }
     return mlora_paged_attention(q.p, q.stride, q.n, (int32_t)q.heads, c, ints(a[2], "page_table", table.numel()), table.size(1),
                                  (int32_t)n, ints(a[3], "cu_q", n + 1), ints(a[4], "kv_len", n), integer(a[6]), integer(a[7]),
-                                 PyObject_IsTrue(a[8]), int32(a[9], "window"), (float)real(a[10]), out.p, out.stride,
+                                 truth(a[8]), int32(a[9], "window"), (float)real(a[10]), out.p, out.stride,
                                  lse_of(a[11], q.n, q.heads), ws, ws_bytes, stream(a[13]));
 }
 
@@ -209,10 +225,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
     if (n != N)
         return PyErr_Format(PyExc_TypeError, "expected %d arguments", N);
     try {
-        const mlora_status st = F(args);
-        if (PyErr_Occurred())
-            return nullptr;
-        return PyLong_FromLong((long)st);
+        return PyLong_FromLong((long)F(args));
     } catch (const std::invalid_argument &e) {
         PyErr_SetString(PyExc_ValueError, e.what());
     } catch (const std::exception &e) {
