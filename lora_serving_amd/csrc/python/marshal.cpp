@@ -140,6 +140,17 @@ const void *weight(PyObject *o, const char *name, int64_t d)
     return t.data_ptr();
 }
 
+// The entry point itself runs without the interpreter's lock, as ctypes calls do: a launch waits where the queue is
+// full.  Its arguments have been taken from their objects, which the caller holds.
+template <class Call> mlora_status unlocked(Call call)
+{
+    struct Released {
+        PyThreadState *state = PyEval_SaveThread();
+        ~Released() { PyEval_RestoreThread(state); }
+    } released;
+    return call();
+}
+
 // (qkv, n_q_heads, n_kv_heads, head_dim, pos, rope, q_out, k_out, q_weight, k_weight, eps, cache, slot, stream)
 mlora_status qk_rope(PyObject *const *a)
 {
@@ -155,10 +166,16 @@ mlora_status qk_rope(PyObject *const *a)
     Rows k{};
     if (a[7] != Py_None)
         k = rows(a[7], "k_out", &want_k);
-    const void *qw = weight(a[8], "q_weight", d), *kw = weight(a[9], "k_weight", d);
-    return mlora_qk_rope(x.data_ptr(), T, T > 1 ? x.stride(0) : width, hq, hkv, d, ints(a[4], "pos", T), address<mlora_rope>(a[5]),
-                         qw, kw, (float)real(a[10]), q.p, q.stride, k.p, k.stride, address<mlora_cache>(a[11]),
-                         a[12] == Py_None ? nullptr : ints(a[12], "slot", T), stream(a[13]));
+    const void *const px = x.data_ptr(), *const qw = weight(a[8], "q_weight", d), *const kw = weight(a[9], "k_weight", d);
+    const int64_t x_stride = T > 1 ? x.stride(0) : width;
+    const int32_t *const pos = ints(a[4], "pos", T), *const slot = a[12] == Py_None ? nullptr : ints(a[12], "slot", T);
+    const mlora_rope *const rope = address<mlora_rope>(a[5]);
+    const mlora_cache *const cache = address<mlora_cache>(a[11]);
+    const float eps = (float)real(a[10]);
+    const hipStream_t s = stream(a[13]);
+    return unlocked([&] {
+        return mlora_qk_rope(px, T, x_stride, hq, hkv, d, pos, rope, qw, kw, eps, q.p, q.stride, k.p, k.stride, cache, slot, s);
+    });
 }
 
 // (cache, slot, k, v, stream)
@@ -176,7 +193,9 @@ mlora_status cache_read(PyObject *const *a)
         if (t.dim() != 3 || t.size(0) != T || t.size(1) != c->n_kv_heads || t.size(2) != c->head_dim)
             fail(name, "must have shape (" + std::to_string(T) + ", " + std::to_string(c->n_kv_heads) + ", " + std::to_string(c->head_dim) + ")");
     }
-    return mlora_cache_read(c, ints(a[1], "slot", T), T, out[0], out[1], stream(a[4]));
+    const int32_t *const slot = ints(a[1], "slot", T);
+    const hipStream_t s = stream(a[4]);
+    return unlocked([&] { return mlora_cache_read(c, slot, T, out[0], out[1], s); });
 }
 
 // (q, k, v, cu_q, out, cu_k, max_q, causal, window, scale, lse, stream)
@@ -186,10 +205,16 @@ mlora_status attention(PyObject *const *a)
     if (k.d != q.d)
         fail("k", "must have the head_dim of q");
     const int64_t n = tensor(a[3], "cu_q").numel() - 1;
-    return mlora_attention(q.p, q.stride, k.p, k.stride, v.p, v.stride, q.n, k.n, (int32_t)n, ints(a[3], "cu_q", n + 1),
-                           a[5] == Py_None ? nullptr : ints(a[5], "cu_k", n + 1), (int32_t)q.heads, (int32_t)k.heads, (int32_t)q.d,
-                           a[6] == Py_None ? q.n : integer(a[6]), truth(a[7]), int32(a[8], "window"), (float)real(a[9]),
-                           out.p, out.stride, lse_of(a[10], q.n, q.heads), stream(a[11]));
+    const int32_t *const cu_q = ints(a[3], "cu_q", n + 1), *const cu_k = a[5] == Py_None ? nullptr : ints(a[5], "cu_k", n + 1);
+    const int64_t max_q = a[6] == Py_None ? q.n : integer(a[6]);
+    const int32_t causal = truth(a[7]), window = int32(a[8], "window");
+    const float scale = (float)real(a[9]);
+    float *const lse = lse_of(a[10], q.n, q.heads);
+    const hipStream_t s = stream(a[11]);
+    return unlocked([&] {
+        return mlora_attention(q.p, q.stride, k.p, k.stride, v.p, v.stride, q.n, k.n, (int32_t)n, cu_q, cu_k, (int32_t)q.heads,
+                               (int32_t)k.heads, (int32_t)q.d, max_q, causal, window, scale, out.p, out.stride, lse, s);
+    });
 }
 
 // (q, cache, page_table, cu_q, kv_len, out, max_q, max_kv, causal, window, scale, lse, ws, stream)
@@ -212,10 +237,17 @@ mlora_status paged_attention(PyObject *const *a)
         ws = w.data_ptr();
         ws_bytes = w.nbytes();
     }
-    return mlora_paged_attention(q.p, q.stride, q.n, (int32_t)q.heads, c, ints(a[2], "page_table", table.numel()), table.size(1),
-                                 (int32_t)n, ints(a[3], "cu_q", n + 1), ints(a[4], "kv_len", n), integer(a[6]), integer(a[7]),
-                                 truth(a[8]), int32(a[9], "window"), (float)real(a[10]), out.p, out.stride,
-                                 lse_of(a[11], q.n, q.heads), ws, ws_bytes, stream(a[13]));
+    const int32_t *const pages = ints(a[2], "page_table", table.numel()), *const cu_q = ints(a[3], "cu_q", n + 1),
+                  *const kv_len = ints(a[4], "kv_len", n);
+    const int64_t width = table.size(1), max_q = integer(a[6]), max_kv = integer(a[7]);
+    const int32_t causal = truth(a[8]), window = int32(a[9], "window");
+    const float scale = (float)real(a[10]);
+    float *const lse = lse_of(a[11], q.n, q.heads);
+    const hipStream_t s = stream(a[13]);
+    return unlocked([&] {
+        return mlora_paged_attention(q.p, q.stride, q.n, (int32_t)q.heads, c, pages, width, (int32_t)n, cu_q, kv_len, max_q, max_kv,
+                                     causal, window, scale, out.p, out.stride, lse, ws, ws_bytes, s);
+    });
 }
 
 // no C++ exception leaves a call
