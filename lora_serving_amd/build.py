@@ -59,19 +59,27 @@ def build(jobs: int = 8) -> str:
     return LIB
 
 
-def build_marshal() -> str:
-    """The binding's marshalling (csrc/python/marshal.cpp): host code over torch's tensor API."""
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+def build_marshal() -> str | None:
+    """The binding's marshalling (csrc/python/marshal.cpp): host code over torch's tensor API.  None, and no
+    module, where torch is not installed: the C library stands without it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
+        print("torch is not installed: libmlora.so without its Python binding", file=sys.stderr)
+        return None
+    torch = os.path.dirname(spec.origin)
     tmp = MARSHAL + f".tmp{os.getpid()}"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE,
-           "-isystem", "/opt/rocm/include", "-isystem", os.path.join(torch, "include"), "-isystem",
+    cmd = [HIPCC, "-x", "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-no-hip-rt",
+           "-D__HIP_PLATFORM_AMD__", "-I", INCLUDE, "-isystem", "/opt/rocm/include", "-isystem",
+           os.path.join(torch, "include"), "-isystem",
            os.path.join(torch, "include", "torch", "csrc", "api", "include"), "-isystem",
            sysconfig.get_paths()["include"], os.path.join(CSRC, "python", "marshal.cpp"), "-o", tmp,
            "-L", PKG, "-lmlora", "-Wl,-rpath,$ORIGIN", "-L", os.path.join(torch, "lib"), "-lc10",
            "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed on marshal.cpp:\n{r.stdout + r.stderr}")
+        raise RuntimeError(f"hipcc failed on marshal.cpp:\n{r.stdout + r.stderr}")
     os.replace(tmp, MARSHAL)
     return MARSHAL
 
