@@ -132,7 +132,10 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a, int wpt_log)
             w[e] = p[e] = 1.f;
         if (weight) {
             unpack8(*(const u32x4 *)(weight + 8 * c), w);
-            unpack8(*(const u32x4 *)(weight + 8 * pc), p);
+            u32x4 bits = {0, 0, 0, 0};      // (no partner: an infinite weight times sn = 0 would not be zero)
+            if (turned)
+                bits = *(const u32x4 *)(weight + 8 * pc);
+            unpack8(bits, p);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
