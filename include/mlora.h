@@ -331,6 +331,8 @@ typedef struct {
  * (2 pi) turns per position, computed in long double.  MLORA_ROPE_LINEAR divides f_i by factor.
  * MLORA_ROPE_PARTS keeps pairs with at least `fast` turns in orig_len positions, divides those
  * with at most `slow` by factor, and ramps linearly in the number of turns between.
+ * (The ramp is over turns.  Models that ramp over the pair's number have other frequencies: they
+ * fill turns themselves.)
  * MLORA_ERR_ARG on NULL, rot_dim not a positive even number, base <= 1, factor < 1, unknown
  * scaling, or (PARTS) orig_len < 1 or fast <= slow.
  */
