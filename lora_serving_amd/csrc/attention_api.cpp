@@ -130,11 +130,11 @@ PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t
             p.dec_rows = 0;
     }
     if (p.dec_rows > 0) {
-        // Equal shares of all keys, one for each workgroup that the card holds (64 contexts of 1 to 8192 tokens:
-        // 231 us against 247 in chunks of 2048).  Contexts of up to 4 units are not split, for they are answered
-        // sooner than parts are joined (8 of 300 tokens: 8.6 us against 10.5), nor those of up to 8 units where
-        // they give every CU one (32 of 600: 17 against 21.5; 256 of 1 to 1024: 105 against 124; but 16 of 1 to
-        // 1024 18.3 against 16.2, and longer ones wait for the longest: 64 of 1 to 8192 239 against 181).
+        // Equal shares of all keys, one for each workgroup that the card holds (64 contexts of 1 to 8192 tokens,
+        // 314332 together: 230 us, whole 274).  Contexts of up to 4 units are not split, for they are answered
+        // sooner than parts are joined (8 of 300 tokens: 8.6 us, so split 10.6), nor those of up to 8 units where
+        // they give every CU one (32 of 600: 17 us, split 22; 256 of 1 to 1024, 136636 together: 110, split 126, of
+        // an e4m3 cache 64 and 87; but 16 of 1 to 1024, 7644 together, are split: 15, whole 18).
         const int64_t items = (int64_t)n_seqs * hkv, units = (max_kv + DECODE_UNIT - 1) / DECODE_UNIT;
         p.split = units > (items >= CUS ? 8 : 4);
         p.shares = (int)(p.split ? std::min(items * units, (int64_t)decode_slots(d, p.nq) * CUS) : items);

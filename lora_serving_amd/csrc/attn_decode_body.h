@@ -11,7 +11,9 @@
 // read transposed, so the loop has no barrier.  The next step's loads are issued while this
 // one's softmax and second product run.  Bound by HBM (or, for a short batch, by latency).  Measured
 // (D = 128, 32 heads on 8, with the join): 64 contexts of 1 to 8192 225 to 232 us (5.6 to 5.7 TB/s), 64 of
-// 4096 184 us (5.8), 256 of an e4m3 cache 231 us (5.1), one of 1003 10.5 us (7 the shares, 4 the join).
+// 4096 184 to 187 us (5.8), 256 of an e4m3 cache 231 us (5.1), one of 1003 10.5 us (7 the shares, 4 the join).
+// With two column tiles of D = 128 27 registers (e4m3: 15) are spilled, outside the loop over keys: 32 x 8 tokens
+// over 4096 keys 137 us (3.9 TB/s), of an e4m3 cache 69 to 71 us (3.9).
 #pragma once
 
 #include <type_traits>

@@ -1,17 +1,21 @@
 // The mixed batch over pages: chunks of new tokens (attn_wide_body.h) and decode rows (attn_decode_body.h) in one
 // launch.  The former are bound by the matrix cores, the latter by memory, and a CU holds two workgroups of either
 // kind; so the launch begins with one of each on every CU and goes on with both in turn (256 tokens with contexts of
-// 64 to 2048 and a chunk of 2048 tokens after 6000: 364 us, one kernel after the other 447; with contexts of 1000
-// and a chunk over 8192 357 us against 432).
+// 64 to 2048 and a chunk of 2048 tokens after 6000: 361 to 383 us, one kernel after the other 447; with contexts of 1000
+// and a chunk over 8192 356 to 377 us against 432).
 #include "attn_decode_body.h"
 #include "attn_wide_body.h"
 
 namespace mlora {
 
 // MORE: there may be more wide items than workgroups for them, which then go on with further ones.  The host does not
-// know the lengths, and workgroups for the most items that they allow cost more than the work of a short chunk (100
-// single tokens and a chunk of 128 after 1872: 66 us, so 51).  Where there cannot be more the loop is left out (a chunk
-// of 2048 e4m3 tokens over 8192: 279 us, with it 286).
+// know the lengths, and workgroups for the most items that they allow are a cost beside a short chunk, in return for
+// which long ones are spread better.  Of 210 batches (16 to 1000 single tokens over 200 or 2000 keys and a chunk of 33
+// to 2048; 32 heads on 8, 16 on 16, 64 on 8) 40 are more than 3% faster than with a workgroup for each item and 9
+// slower, 1% faster in the mean: 16 tokens over 2000 and a chunk of 33 over 4000 44 us (50), 250 e4m3 ones over 200 and
+// 33 over 4000 66 (74), 100 over 200 and 128 over 2000 51 (54); but 200 over 1000 and 512 over 2000 228 (210), and of
+// 16 heads on 16 250 e4m3 ones over 2000 and 2048 over 8192 540 (486).  Where there cannot be more items the loop is
+// left out (a chunk of 2048 e4m3 tokens over 8192: 279 us, with it 286).
 template <int D, bool FP8, bool MORE>
 __global__ __launch_bounds__(256, 2) void attn_mixed_kernel(AttnArgs w, AttnArgs d, uint32_t wide_x, uint32_t shares)
 {

@@ -13,9 +13,10 @@
 // (8 causal prompts of 2048, 32 heads of 128 on 8: 338 us against 357 when that was chosen).  Bound by
 // the issue of products and exponentials together: on a prompt of 16384 tokens a SIMD's matrix core
 // is busy for 61 to 63% of the cycles and its vector unit for 53 to 54%, at 1.7 to 1.8 GHz.  Measured
-// (D = 128, 32 heads on 8): 8 prompts of 2048 308 us (890 TFLOP/s), one of 16384 1.91 to 1.96 ms (1120
-// to 1150), 2048 tokens over 8192 keys in bf16 pages 228 us (1050), in e4m3 pages 273 us (880: conversions
-// and scales take the issue), D = 64 153 us (780: the same exponentials for half the products).
+// (D = 128, 32 heads on 8): 8 prompts of 2048 308 to 317 us (870 to 890 TFLOP/s), one of 16384 1.91 to 1.97 ms
+// (1120 to 1150), 2048 tokens over 8192 keys in bf16 pages 228 to 234 us (1030 to 1050), in e4m3 pages 273 to
+// 282 us (850 to 880: conversions and scales take the issue), D = 64 148 to 153 us (780 to 810: the same
+// exponentials for half the products).
 #pragma once
 
 #include <type_traits>
