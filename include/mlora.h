@@ -415,8 +415,8 @@ mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int
  *   ws  mlora_paged_workspace_size() bytes for the same sizes, or for larger ones of the same heads: the
  *       size never falls as T, n_seqs, max_q or max_kv rises, so one workspace made for a server's
  *       largest step serves every other
- * max_kv and T are below 2^30, T * n_q_heads and n_seqs * n_kv_heads * (max_kv / 128 + 1) below 2^31;
- * mlora_paged_workspace_size gives 0 where the call would refuse its sizes.
+ * max_kv and T are below 2^30, T * n_q_heads, n_seqs * n_kv_heads * (max_kv / 128 + 1) and table_stride
+ * below 2^31; mlora_paged_workspace_size gives 0 where the call would refuse its sizes.
  * A page number outside the cache is read as its nearest valid page (no fault; such sequences'
  * results are meaningless): mlora_validate_pages checks a batch's tables on the host.
  */

@@ -57,6 +57,9 @@ LONG_KEYS = [
     ([(40, 9000)] * 22, 8, 8, 128, 16, False, STARTS[0]),
     ([(40, 9000)], 8, 2, 64, 16, True, STARTS[3]),
     ([(40, 9000)], 8, 2, 128, 16, False, 130),
+    # more row blocks than workgroups launched for them, beside single tokens
+    ([(20, TILES[i % 8]) for i in range(30)] + [(1, 9000 - 100 * i) for i in range(60)], 16, 8, 64, 16, False, 0),
+    ([(20, TILES[i % 8]) for i in range(30)] + [(1, 9000 - 100 * i) for i in range(60)], 16, 8, 128, 32, True, 0),
 ]
 
 
