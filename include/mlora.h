@@ -402,6 +402,19 @@ mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int
                              void *out, int64_t out_stride, float *lse, hipStream_t stream);
 
 /*
+ * mlora_attention with a few first keys of each sequence that stay visible behind the window: with window > 0, query i
+ * sees key j when j < L, j <= p (if causal) and j > p - window or j < sinks.  sinks >= 0; without a window it hides and
+ * shows nothing.  All else as mlora_attention, which is sinks = 0.
+ */
+mlora_status mlora_attention_sinks(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                   const void *v, int64_t v_stride, int64_t T_q, int64_t T_k,
+                                   int32_t n_seqs, const int32_t *cu_q, const int32_t *cu_k,
+                                   int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                   int64_t max_q, int32_t causal, int32_t window, int32_t sinks,
+                                   float scale, void *out, int64_t out_stride, float *lse,
+                                   hipStream_t stream);
+
+/*
  * Attention of new tokens over a paged cache that already holds them (mlora_qk_rope first):
  * sequence b owns query rows [cu_q[b], cu_q[b+1]) and kv_len[b] cached tokens, token j in page
  * page_table[b][j / page_size].  Semantics as mlora_attention with L = kv_len[b]; decode is one
@@ -432,6 +445,19 @@ mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, i
                                    hipStream_t stream);
 
 /*
+ * mlora_paged_attention with a few first tokens of each sequence that stay visible behind the window (see
+ * mlora_attention_sinks); the workspace is the same.  Pages that hold no token which a query sees may have been given
+ * up: their entries in page_table may be any number, and what they hold has no effect.
+ */
+mlora_status mlora_paged_attention_sinks(const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads,
+                                         const mlora_cache *cache, const int32_t *page_table,
+                                         int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
+                                         const int32_t *kv_len, int64_t max_q, int64_t max_kv,
+                                         int32_t causal, int32_t window, int32_t sinks, float scale,
+                                         void *out, int64_t out_stride, float *lse, void *ws,
+                                         size_t ws_bytes, hipStream_t stream);
+
+/*
  * Host check of a paged batch before its arrays are copied to the GPU (all pointers host):
  * cu_q ascending from 0 to T, 0 <= kv_len[b] <= min(table_stride * page_size, max_kv), query
  * counts at most max_q, and every page that a sequence's kv_len reaches in [0, n_pages).
@@ -442,6 +468,16 @@ mlora_status mlora_validate_pages(const mlora_cache *cache, const int32_t *page_
                                   int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
                                   const int32_t *kv_len, int64_t T, int64_t max_q,
                                   int64_t max_kv, int64_t *bad_value);
+
+/*
+ * The same for mlora_paged_attention_sinks: pages without a token that some query of the sequence sees are not looked
+ * at (window 0: all pages are).
+ */
+mlora_status mlora_validate_pages_sinks(const mlora_cache *cache, const int32_t *page_table,
+                                        int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
+                                        const int32_t *kv_len, int64_t T, int64_t max_q,
+                                        int64_t max_kv, int32_t window, int32_t sinks,
+                                        int64_t *bad_value);
 
 /*
  * Profiling hook (not part of the computation).  mlora_trace_start creates 2*capacity HIP

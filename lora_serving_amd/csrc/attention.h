@@ -54,7 +54,10 @@ struct AttnArgs {
     int32_t chunk, n_chunks;
     float *part_o, *part_ml;       // [..][head_dim], [..][2]
     int32_t min_rows, max_rows;    // sequences this launch answers: rows = queries * group
+    int32_t sinks;                 // first keys that stay visible behind the window (0, or a window is set)
 };
+// Which keys a kernel's queries see, besides the causal limit: all or a window of them; a window and the first ones.
+enum { KEYS_PLAIN = 0, KEYS_SINKS = 1 };
 // Whole prompts (cache unused) or, with pages, chunks of new tokens.
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream);
 constexpr int64_t CUS = 256;      // of an MI355X

@@ -77,6 +77,12 @@ bool rows_ok(int64_t stride, int64_t width) { return stride >= width && stride %
 // stay within 32 bits).
 int32_t seen_window(int32_t window, int64_t max_keys) { return window >= max_keys ? 0 : window; }
 
+// First keys beside a window (as seen_window gives it): none where nothing is hidden, at most all.
+int32_t seen_sinks(int32_t sinks, int32_t window, int64_t max_keys)
+{
+    return window > 0 ? (int32_t)std::min<int64_t>(sinks, max_keys) : 0;
+}
+
 size_t align_up(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Bytes of the parts of the decode kernel: two slots of `rows` rows a share.
@@ -115,11 +121,17 @@ struct PagedPlan {
     size_t total() const { return dec_o + dec_ml + wide_o + wide_ml; }
 };
 
-PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv)
+// (window, sinks: 0, or both as the kernels get them.  A cut is then made of the keys that a sequence's queries or
+// those of a row block may see, never into more than without them.)
+PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv,
+                     int64_t window, int64_t sinks)
 {
     PagedPlan p;
     const int64_t group = hq / hkv, most = max_q * group;
     max_kv = std::max<int64_t>(max_kv, 1);
+    const auto seen = [&](int64_t queries) {
+        return sinks > 0 ? std::min(max_kv, window + queries + (sinks + DECODE_UNIT) / DECODE_UNIT * DECODE_UNIT + DECODE_UNIT) : max_kv;
+    };
     if (most <= 32) {
         p.dec_rows = most;
         p.nq = most <= 16 ? 1 : 2;
@@ -135,7 +147,8 @@ PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t
         // sooner than parts are joined (8 of 300 tokens: 8.6 us, so split 10.6), nor those of up to 8 units where
         // they give every CU one (32 of 600: 17 us, split 22; 256 of 1 to 1024, 136636 together: 110, split 126, of
         // an e4m3 cache 64 and 87; but 16 of 1 to 1024, 7644 together, are split: 15, whole 18).
-        const int64_t items = (int64_t)n_seqs * hkv, units = (max_kv + DECODE_UNIT - 1) / DECODE_UNIT;
+        const int64_t items = (int64_t)n_seqs * hkv, keys = seen(std::min<int64_t>(max_q, 32));
+        const int64_t units = (keys + DECODE_UNIT - 1) / DECODE_UNIT;
         p.split = units > (items >= CUS ? 8 : 4);
         p.shares = (int)(p.split ? std::min(items * units, (int64_t)decode_slots(d, p.nq) * CUS) : items);
         if (p.split)
@@ -146,9 +159,9 @@ PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t
         // come here (100 sequences of 40 rows over 1500 keys: 94 us in chunks, 67 whole)
         const bool all = T * group > n_seqs * p.dec_rows;
         const int64_t items = std::max<int64_t>((T * group + WIDE_ROWS - 1) / WIDE_ROWS, all ? n_seqs : 0) * hkv;
-        const int64_t n = items >= WIDE_WHOLE ? 1 : wide_cuts(items, max_kv);
+        const int64_t n = items >= WIDE_WHOLE ? 1 : wide_cuts(items, seen(WIDE_ROWS / group + 1));
         p.wide_chunk = ((max_kv + n - 1) / n + 127) & ~INT64_C(127);
-        p.wide_chunks = (max_kv + p.wide_chunk - 1) / p.wide_chunk;
+        p.wide_chunks = sinks > 0 ? n : (max_kv + p.wide_chunk - 1) / p.wide_chunk;
         if (p.wide_chunks > 1)
             wide_parts(T, hq, p.wide_chunks, d, &p.wide_o, &p.wide_ml);
     }
@@ -177,6 +190,188 @@ size_t paged_room(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d,
         }
     }
     return dec + wide;
+}
+
+mlora_status attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                       int64_t v_stride, int64_t T_q, int64_t T_k, int32_t n_seqs, const int32_t *cu_q,
+                       const int32_t *cu_k, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int64_t max_q,
+                       int32_t causal, int32_t window, int32_t sinks, float scale, void *out, int64_t out_stride,
+                       float *lse, hipStream_t stream)
+{
+    if (T_q < 0 || T_k < 0 || n_seqs < 0 || max_q < 0 || window < 0 || sinks < 0 || !(scale >= 0.f) ||
+        std::isinf(scale))
+        return MLORA_ERR_ARG;
+    const mlora_status st = check_heads(n_q_heads, n_kv_heads, head_dim);
+    if (st != MLORA_OK)
+        return st;
+    const int64_t qw = (int64_t)n_q_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
+    if (!rows_ok(q_stride, qw) || !rows_ok(out_stride, qw) || !rows_ok(k_stride, kw) || !rows_ok(v_stride, kw) ||
+        (cu_k == nullptr && T_k != T_q))
+        return MLORA_ERR_SHAPE;
+    if (T_q >= MAX_KEYS || T_k >= MAX_KEYS || T_q * n_q_heads >= MAX_ROWS || k_stride >= MAX_STRIDE ||
+        v_stride >= MAX_STRIDE)
+        return MLORA_ERR_UNSUPPORTED;
+    if (T_q == 0 || n_seqs == 0 || max_q == 0)
+        return MLORA_OK;
+    if (q == nullptr || out == nullptr || cu_q == nullptr || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(out) || (T_k > 0 && (k == nullptr || v == nullptr)))
+        return MLORA_ERR_ARG;
+    AttnArgs a{};
+    a.q = (const uint16_t *)q;
+    a.k = (const uint16_t *)k;
+    a.v = (const uint16_t *)v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.out_stride = out_stride;
+    a.T = T_q;
+    a.Tk = T_k;
+    a.n_seqs = n_seqs;
+    a.hq = n_q_heads;
+    a.hkv = n_kv_heads;
+    a.group = n_q_heads / n_kv_heads;
+    a.cu_q = cu_q;
+    a.cu_k = cu_k;
+    a.max_q = std::min(max_q, T_q);
+    a.causal = causal;
+    a.window = seen_window(window, T_k);
+    a.sinks = seen_sinks(sinks, a.window, T_k);
+    a.scale = scale == 0.f ? (float)(1.0 / std::sqrt((double)head_dim)) : scale;
+    a.out = (uint16_t *)out;
+    a.lse = lse;
+    a.chunk = 1 << 30;
+    a.n_chunks = 1;
+    a.max_rows = 0x7fffffff;
+    trace_mark(stream, true);
+    const hipError_t e = launch_attn_wide(a, head_dim, false, stream);
+    trace_mark(stream, false);
+    return hip_status(e);
+}
+
+mlora_status paged_attention(const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads, const mlora_cache *cache,
+                             const int32_t *page_table, int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
+                             const int32_t *kv_len, int64_t max_q, int64_t max_kv, int32_t causal, int32_t window,
+                             int32_t sinks, float scale, void *out, int64_t out_stride, float *lse, void *ws,
+                             size_t ws_bytes, hipStream_t stream)
+{
+    if (T < 0 || n_seqs < 0 || max_q < 0 || max_kv < 0 || table_stride < 0 || window < 0 || sinks < 0 || !(scale >= 0.f) ||
+        std::isinf(scale))
+        return MLORA_ERR_ARG;
+    AttnArgs a{};
+    mlora_status st = check_cache(cache, &a.cache);
+    if (st != MLORA_OK)
+        return st;
+    const int32_t d = cache->head_dim;
+    st = check_heads(n_q_heads, cache->n_kv_heads, d);
+    if (st != MLORA_OK)
+        return st;
+    if (!rows_ok(q_stride, (int64_t)n_q_heads * d) || !rows_ok(out_stride, (int64_t)n_q_heads * d))
+        return MLORA_ERR_SHAPE;
+    if (!paged_sizes_ok(T, n_seqs, n_q_heads, cache->n_kv_heads, max_kv) || table_stride >= MAX_ROWS)
+        return MLORA_ERR_UNSUPPORTED;
+    if (T == 0 || n_seqs == 0 || max_q == 0)
+        return MLORA_OK;
+    if (q == nullptr || out == nullptr || cu_q == nullptr || kv_len == nullptr || !aligned16(q) || !aligned16(out) ||
+        (max_kv > 0 && table_stride > 0 && page_table == nullptr))
+        return MLORA_ERR_ARG;
+    max_q = std::min(max_q, T);
+    a.window = seen_window(window, max_kv);
+    a.sinks = seen_sinks(sinks, a.window, max_kv);
+    const PagedPlan p = paged_plan(T, n_seqs, n_q_heads, cache->n_kv_heads, d, max_q, max_kv, a.window, a.sinks);
+    if (p.wide_chunks > 65535)
+        return MLORA_ERR_UNSUPPORTED;
+    uint8_t *base = (uint8_t *)(((uintptr_t)ws + 255) & ~(uintptr_t)255);
+    if (p.total() > 0 && (ws == nullptr || ws_bytes < p.total() + (size_t)(base - (uint8_t *)ws)))
+        return MLORA_ERR_WORKSPACE;
+    a.q = (const uint16_t *)q;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.T = T;
+    a.n_seqs = n_seqs;
+    a.hq = n_q_heads;
+    a.hkv = cache->n_kv_heads;
+    a.group = n_q_heads / cache->n_kv_heads;
+    a.cu_q = cu_q;
+    a.kv_len = kv_len;
+    a.table = page_table;
+    a.table_stride = table_stride;
+    a.max_q = max_q;
+    a.max_kv = max_kv;
+    a.causal = causal;
+    a.scale = scale == 0.f ? (float)(1.0 / std::sqrt((double)d)) : scale;
+    a.out = (uint16_t *)out;
+    a.lse = lse;
+    AttnArgs w = a;                     // the wide part
+    w.min_rows = (int32_t)p.dec_rows + 1;
+    w.max_rows = 0x7fffffff;
+    w.chunk = (int32_t)p.wide_chunk;
+    w.n_chunks = (int32_t)p.wide_chunks;
+    w.part_o = (float *)(base + p.dec_o + p.dec_ml);
+    w.part_ml = (float *)(base + p.dec_o + p.dec_ml + p.wide_o);
+    a.max_rows = (int32_t)p.dec_rows;   // and the decode rows
+    a.part_o = p.split ? (float *)base : nullptr;
+    a.part_ml = p.split ? (float *)(base + p.dec_o) : nullptr;
+    trace_mark(stream, true);
+    hipError_t e;
+    if (p.wide && p.dec_rows > 0)
+        e = launch_attn_mixed(w, a, d, p.shares, stream);
+    else if (p.wide)
+        e = launch_attn_wide(w, d, true, stream);
+    else
+        e = launch_attn_decode(a, d, p.nq, p.shares, stream);
+    if (e == hipSuccess && p.wide_chunks > 1)
+        e = launch_attn_wide_combine(w, d, stream);
+    if (e == hipSuccess && p.split)
+        e = launch_attn_combine(a, d, p.shares, stream);
+    trace_mark(stream, false);
+    return hip_status(e);
+}
+
+mlora_status validate_pages(const mlora_cache *cache, const int32_t *page_table, int64_t table_stride, int32_t n_seqs,
+                            const int32_t *cu_q, const int32_t *kv_len, int64_t T, int64_t max_q, int64_t max_kv,
+                            int32_t window, int32_t sinks, int64_t *bad_value)
+{
+    if (cache == nullptr || n_seqs < 0 || T < 0 || table_stride < 0 || max_q < 0 || max_kv < 0 ||
+        window < 0 || sinks < 0)
+        return MLORA_ERR_ARG;
+    const mlora_status st =
+        check_cache_sizes(cache->n_pages, cache->n_kv_heads, cache->page_size, cache->head_dim, cache->dtype);
+    if (st != MLORA_OK)
+        return st;
+    if (table_stride >= MAX_ROWS)
+        return MLORA_ERR_UNSUPPORTED;
+    if (cu_q == nullptr || (n_seqs > 0 && kv_len == nullptr))
+        return MLORA_ERR_ARG;
+    const auto bad = [bad_value](mlora_status s, int64_t v) {
+        if (bad_value)
+            *bad_value = v;
+        return s;
+    };
+    if (cu_q[0] != 0)
+        return bad(MLORA_ERR_SHAPE, cu_q[0]);
+    for (int32_t b = 0; b < n_seqs; ++b) {
+        const int64_t n = (int64_t)cu_q[b + 1] - cu_q[b];
+        if (n < 0 || n > max_q)
+            return bad(MLORA_ERR_SHAPE, n);
+        if (kv_len[b] < 0 || kv_len[b] > max_kv || kv_len[b] > table_stride * cache->page_size)
+            return bad(MLORA_ERR_SHAPE, kv_len[b]);
+        if (kv_len[b] > 0 && page_table == nullptr)
+            return MLORA_ERR_ARG;
+        const int64_t pages = ((int64_t)kv_len[b] + cache->page_size - 1) / cache->page_size;
+        // the queries see keys [0, first) and [lo, kv_len[b]) (without a window every page is looked at)
+        const int64_t lo = window <= 0 ? 0 : n > 0 ? std::max<int64_t>(0, kv_len[b] - n - window + 1) : kv_len[b];
+        const int64_t first = n > 0 ? sinks : 0;
+        for (int64_t i = 0; i < pages; ++i) {
+            if (window > 0 && i * cache->page_size >= first && (n == 0 || (i + 1) * cache->page_size <= lo))
+                continue;
+            const int32_t p = page_table[b * table_stride + i];
+            if (p < 0 || p >= cache->n_pages)
+                return bad(MLORA_ERR_INDEX, p);
+        }
+    }
+    if (cu_q[n_seqs] != T)
+        return bad(MLORA_ERR_SHAPE, cu_q[n_seqs]);
+    return MLORA_OK;
 }
 
 }  // namespace
@@ -301,53 +496,18 @@ mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int
                              int64_t max_q, int32_t causal, int32_t window, float scale, void *out,
                              int64_t out_stride, float *lse, hipStream_t stream)
 {
-    if (T_q < 0 || T_k < 0 || n_seqs < 0 || max_q < 0 || window < 0 || !(scale >= 0.f) ||
-        std::isinf(scale))
-        return MLORA_ERR_ARG;
-    const mlora_status st = check_heads(n_q_heads, n_kv_heads, head_dim);
-    if (st != MLORA_OK)
-        return st;
-    const int64_t qw = (int64_t)n_q_heads * head_dim, kw = (int64_t)n_kv_heads * head_dim;
-    if (!rows_ok(q_stride, qw) || !rows_ok(out_stride, qw) || !rows_ok(k_stride, kw) || !rows_ok(v_stride, kw) ||
-        (cu_k == nullptr && T_k != T_q))
-        return MLORA_ERR_SHAPE;
-    if (T_q >= MAX_KEYS || T_k >= MAX_KEYS || T_q * n_q_heads >= MAX_ROWS || k_stride >= MAX_STRIDE ||
-        v_stride >= MAX_STRIDE)
-        return MLORA_ERR_UNSUPPORTED;
-    if (T_q == 0 || n_seqs == 0 || max_q == 0)
-        return MLORA_OK;
-    if (q == nullptr || out == nullptr || cu_q == nullptr || !aligned16(q) || !aligned16(k) || !aligned16(v) ||
-        !aligned16(out) || (T_k > 0 && (k == nullptr || v == nullptr)))
-        return MLORA_ERR_ARG;
-    AttnArgs a{};
-    a.q = (const uint16_t *)q;
-    a.k = (const uint16_t *)k;
-    a.v = (const uint16_t *)v;
-    a.q_stride = q_stride;
-    a.k_stride = k_stride;
-    a.v_stride = v_stride;
-    a.out_stride = out_stride;
-    a.T = T_q;
-    a.Tk = T_k;
-    a.n_seqs = n_seqs;
-    a.hq = n_q_heads;
-    a.hkv = n_kv_heads;
-    a.group = n_q_heads / n_kv_heads;
-    a.cu_q = cu_q;
-    a.cu_k = cu_k;
-    a.max_q = std::min(max_q, T_q);
-    a.causal = causal;
-    a.window = seen_window(window, T_k);
-    a.scale = scale == 0.f ? (float)(1.0 / std::sqrt((double)head_dim)) : scale;
-    a.out = (uint16_t *)out;
-    a.lse = lse;
-    a.chunk = 1 << 30;
-    a.n_chunks = 1;
-    a.max_rows = 0x7fffffff;
-    trace_mark(stream, true);
-    const hipError_t e = launch_attn_wide(a, head_dim, false, stream);
-    trace_mark(stream, false);
-    return hip_status(e);
+    return attention(q, q_stride, k, k_stride, v, v_stride, T_q, T_k, n_seqs, cu_q, cu_k, n_q_heads, n_kv_heads,
+                     head_dim, max_q, causal, window, 0, scale, out, out_stride, lse, stream);
+}
+
+mlora_status mlora_attention_sinks(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                   int64_t v_stride, int64_t T_q, int64_t T_k, int32_t n_seqs, const int32_t *cu_q,
+                                   const int32_t *cu_k, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                   int64_t max_q, int32_t causal, int32_t window, int32_t sinks, float scale,
+                                   void *out, int64_t out_stride, float *lse, hipStream_t stream)
+{
+    return attention(q, q_stride, k, k_stride, v, v_stride, T_q, T_k, n_seqs, cu_q, cu_k, n_q_heads, n_kv_heads,
+                     head_dim, max_q, causal, window, sinks, scale, out, out_stride, lse, stream);
 }
 
 size_t mlora_paged_workspace_size(int64_t T, int32_t n_seqs, int32_t n_q_heads, int32_t n_kv_heads,
@@ -366,117 +526,34 @@ mlora_status mlora_paged_attention(const void *q, int64_t q_stride, int64_t T, i
                                    int64_t max_kv, int32_t causal, int32_t window, float scale, void *out,
                                    int64_t out_stride, float *lse, void *ws, size_t ws_bytes, hipStream_t stream)
 {
-    if (T < 0 || n_seqs < 0 || max_q < 0 || max_kv < 0 || table_stride < 0 || window < 0 || !(scale >= 0.f) ||
-        std::isinf(scale))
-        return MLORA_ERR_ARG;
-    AttnArgs a{};
-    mlora_status st = check_cache(cache, &a.cache);
-    if (st != MLORA_OK)
-        return st;
-    const int32_t d = cache->head_dim;
-    st = check_heads(n_q_heads, cache->n_kv_heads, d);
-    if (st != MLORA_OK)
-        return st;
-    if (!rows_ok(q_stride, (int64_t)n_q_heads * d) || !rows_ok(out_stride, (int64_t)n_q_heads * d))
-        return MLORA_ERR_SHAPE;
-    if (!paged_sizes_ok(T, n_seqs, n_q_heads, cache->n_kv_heads, max_kv) || table_stride >= MAX_ROWS)
-        return MLORA_ERR_UNSUPPORTED;
-    if (T == 0 || n_seqs == 0 || max_q == 0)
-        return MLORA_OK;
-    if (q == nullptr || out == nullptr || cu_q == nullptr || kv_len == nullptr || !aligned16(q) || !aligned16(out) ||
-        (max_kv > 0 && table_stride > 0 && page_table == nullptr))
-        return MLORA_ERR_ARG;
-    max_q = std::min(max_q, T);
-    const PagedPlan p = paged_plan(T, n_seqs, n_q_heads, cache->n_kv_heads, d, max_q, max_kv);
-    if (p.wide_chunks > 65535)
-        return MLORA_ERR_UNSUPPORTED;
-    uint8_t *base = (uint8_t *)(((uintptr_t)ws + 255) & ~(uintptr_t)255);
-    if (p.total() > 0 && (ws == nullptr || ws_bytes < p.total() + (size_t)(base - (uint8_t *)ws)))
-        return MLORA_ERR_WORKSPACE;
-    a.q = (const uint16_t *)q;
-    a.q_stride = q_stride;
-    a.out_stride = out_stride;
-    a.T = T;
-    a.n_seqs = n_seqs;
-    a.hq = n_q_heads;
-    a.hkv = cache->n_kv_heads;
-    a.group = n_q_heads / cache->n_kv_heads;
-    a.cu_q = cu_q;
-    a.kv_len = kv_len;
-    a.table = page_table;
-    a.table_stride = table_stride;
-    a.max_q = max_q;
-    a.max_kv = max_kv;
-    a.causal = causal;
-    a.window = seen_window(window, max_kv);
-    a.scale = scale == 0.f ? (float)(1.0 / std::sqrt((double)d)) : scale;
-    a.out = (uint16_t *)out;
-    a.lse = lse;
-    AttnArgs w = a;                     // the wide part
-    w.min_rows = (int32_t)p.dec_rows + 1;
-    w.max_rows = 0x7fffffff;
-    w.chunk = (int32_t)p.wide_chunk;
-    w.n_chunks = (int32_t)p.wide_chunks;
-    w.part_o = (float *)(base + p.dec_o + p.dec_ml);
-    w.part_ml = (float *)(base + p.dec_o + p.dec_ml + p.wide_o);
-    a.max_rows = (int32_t)p.dec_rows;   // and the decode rows
-    a.part_o = p.split ? (float *)base : nullptr;
-    a.part_ml = p.split ? (float *)(base + p.dec_o) : nullptr;
-    trace_mark(stream, true);
-    hipError_t e;
-    if (p.wide && p.dec_rows > 0)
-        e = launch_attn_mixed(w, a, d, p.shares, stream);
-    else if (p.wide)
-        e = launch_attn_wide(w, d, true, stream);
-    else
-        e = launch_attn_decode(a, d, p.nq, p.shares, stream);
-    if (e == hipSuccess && p.wide_chunks > 1)
-        e = launch_attn_wide_combine(w, d, stream);
-    if (e == hipSuccess && p.split)
-        e = launch_attn_combine(a, d, p.shares, stream);
-    trace_mark(stream, false);
-    return hip_status(e);
+    return paged_attention(q, q_stride, T, n_q_heads, cache, page_table, table_stride, n_seqs, cu_q, kv_len, max_q, max_kv,
+                           causal, window, 0, scale, out, out_stride, lse, ws, ws_bytes, stream);
+}
+
+mlora_status mlora_paged_attention_sinks(const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads,
+                                         const mlora_cache *cache, const int32_t *page_table, int64_t table_stride,
+                                         int32_t n_seqs, const int32_t *cu_q, const int32_t *kv_len, int64_t max_q,
+                                         int64_t max_kv, int32_t causal, int32_t window, int32_t sinks, float scale,
+                                         void *out, int64_t out_stride, float *lse, void *ws, size_t ws_bytes,
+                                         hipStream_t stream)
+{
+    return paged_attention(q, q_stride, T, n_q_heads, cache, page_table, table_stride, n_seqs, cu_q, kv_len, max_q, max_kv,
+                           causal, window, sinks, scale, out, out_stride, lse, ws, ws_bytes, stream);
 }
 
 mlora_status mlora_validate_pages(const mlora_cache *cache, const int32_t *page_table, int64_t table_stride,
                                   int32_t n_seqs, const int32_t *cu_q, const int32_t *kv_len, int64_t T,
                                   int64_t max_q, int64_t max_kv, int64_t *bad_value)
 {
-    if (cache == nullptr || n_seqs < 0 || T < 0 || table_stride < 0 || max_q < 0 || max_kv < 0)
-        return MLORA_ERR_ARG;
-    const mlora_status st =
-        check_cache_sizes(cache->n_pages, cache->n_kv_heads, cache->page_size, cache->head_dim, cache->dtype);
-    if (st != MLORA_OK)
-        return st;
-    if (table_stride >= MAX_ROWS)
-        return MLORA_ERR_UNSUPPORTED;
-    if (cu_q == nullptr || (n_seqs > 0 && kv_len == nullptr))
-        return MLORA_ERR_ARG;
-    const auto bad = [bad_value](mlora_status s, int64_t v) {
-        if (bad_value)
-            *bad_value = v;
-        return s;
-    };
-    if (cu_q[0] != 0)
-        return bad(MLORA_ERR_SHAPE, cu_q[0]);
-    for (int32_t b = 0; b < n_seqs; ++b) {
-        const int64_t n = (int64_t)cu_q[b + 1] - cu_q[b];
-        if (n < 0 || n > max_q)
-            return bad(MLORA_ERR_SHAPE, n);
-        if (kv_len[b] < 0 || kv_len[b] > max_kv || kv_len[b] > table_stride * cache->page_size)
-            return bad(MLORA_ERR_SHAPE, kv_len[b]);
-        if (kv_len[b] > 0 && page_table == nullptr)
-            return MLORA_ERR_ARG;
-        const int64_t pages = ((int64_t)kv_len[b] + cache->page_size - 1) / cache->page_size;
-        for (int64_t i = 0; i < pages; ++i) {
-            const int32_t p = page_table[b * table_stride + i];
-            if (p < 0 || p >= cache->n_pages)
-                return bad(MLORA_ERR_INDEX, p);
-        }
-    }
-    if (cu_q[n_seqs] != T)
-        return bad(MLORA_ERR_SHAPE, cu_q[n_seqs]);
-    return MLORA_OK;
+    return validate_pages(cache, page_table, table_stride, n_seqs, cu_q, kv_len, T, max_q, max_kv, 0, 0, bad_value);
+}
+
+mlora_status mlora_validate_pages_sinks(const mlora_cache *cache, const int32_t *page_table, int64_t table_stride,
+                                        int32_t n_seqs, const int32_t *cu_q, const int32_t *kv_len, int64_t T,
+                                        int64_t max_q, int64_t max_kv, int32_t window, int32_t sinks,
+                                        int64_t *bad_value)
+{
+    return validate_pages(cache, page_table, table_stride, n_seqs, cu_q, kv_len, T, max_q, max_kv, window, sinks, bad_value);
 }
 
 }  // extern "C"

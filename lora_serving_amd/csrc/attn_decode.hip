@@ -4,26 +4,26 @@
 
 namespace mlora {
 
-template <int D, int NQ, bool FP8>
+template <int D, int NQ, bool FP8, int KEYS>
 __global__ __launch_bounds__(256, decode_slots(D, NQ)) void attn_decode_kernel(AttnArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint8_t smem[decode_lds<D, NQ>];
-    attn_decode_body<D, NQ, FP8>(a, blockIdx.x, gridDim.x, smem);
+    attn_decode_body<D, NQ, FP8, KEYS>(a, blockIdx.x, gridDim.x, smem);
 }
 
 // The join, a workgroup a cut between shares: the first cut within a sequence and head joins its parts, one wave a
 // row.  A few MB that the shares just wrote: bound by the latency of a launch and its chain of loads (one context of
 // 1003 keys 3.8 us; 511 cuts 6 to 8 us).
-template <int D>
+template <int D, int KEYS>
 __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs a, int shares)
 {
     const int lane = threadIdx.x & 63, w1 = blockIdx.x + 1;
-    const LaneUnits u = lane_units(a, lane);
+    const LaneUnits u = lane_units<KEYS>(a, lane);
     const Shares cut((uint32_t)u.total * a.hkv, (uint32_t)shares);
     if ((uint32_t)w1 >= cut.n)
         return;
     const uint32_t u1 = cut.start(w1);
-    const UnitPlace at = find_unit(a, u, u1);
+    const UnitPlace at = find_unit<KEYS>(a, u, u1);
     const int w0 = w1 - 1;
     if (at.f == 0 || cut.start(w0) > u1 - at.f)     // nothing is cut here, or an earlier cut joins it
         return;
@@ -34,10 +34,13 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs a, int share
     }
 }
 
-hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream)
+namespace {
+
+template <int KEYS>
+hipError_t launch_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream)
 {
     const dim3 grid((unsigned)shares);
-#define DEC(D, NQ, F) attn_decode_kernel<D, NQ, F><<<grid, dim3(256), 0, stream>>>(a)
+#define DEC(D, NQ, F) attn_decode_kernel<D, NQ, F, KEYS><<<grid, dim3(256), 0, stream>>>(a)
 #define DEC_F(D, NQ) (a.cache.fp8 ? DEC(D, NQ, true) : DEC(D, NQ, false))
 #define DEC_Q(D) (nq == 1 ? DEC_F(D, 1) : DEC_F(D, 2))
     head_dim == 64 ? DEC_Q(64) : DEC_Q(128);
@@ -47,16 +50,31 @@ hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int share
     return hipGetLastError();
 }
 
-hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream)
+template <int KEYS>
+hipError_t launch_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream)
 {
     if (shares < 2)
         return hipSuccess;
     const dim3 grid((unsigned)(shares - 1));
     if (head_dim == 64)
-        attn_combine_kernel<64><<<grid, dim3(256), 0, stream>>>(a, shares);
+        attn_combine_kernel<64, KEYS><<<grid, dim3(256), 0, stream>>>(a, shares);
     else
-        attn_combine_kernel<128><<<grid, dim3(256), 0, stream>>>(a, shares);
+        attn_combine_kernel<128, KEYS><<<grid, dim3(256), 0, stream>>>(a, shares);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream)
+{
+    return a.sinks > 0 ? launch_decode<KEYS_SINKS>(a, head_dim, nq, shares, stream)
+                       : launch_decode<KEYS_PLAIN>(a, head_dim, nq, shares, stream);
+}
+
+hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream)
+{
+    return a.sinks > 0 ? launch_combine<KEYS_SINKS>(a, head_dim, shares, stream)
+                       : launch_combine<KEYS_PLAIN>(a, head_dim, shares, stream);
 }
 
 }  // namespace mlora

@@ -24,11 +24,14 @@
 namespace mlora {
 
 // A sequence: its queries and the units [first, first + units) of the keys [lo, L) that they see (at least one
-// unit; none if this launch does not answer the sequence).
+// unit; none if this launch does not answer the sequence).  KEYS_SINKS: `sink` units of the first keys come before
+// those from `first` on, and are counted in `units`; where no block of 32 lies between the first keys and lo, all
+// units are taken.
 struct SeqUnits {
-    int q0, n, L, lo, first, units;
+    int q0, n, L, lo, first, units, sink;
 };
 
+template <int KEYS>
 __device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b)
 {
     SeqUnits s;
@@ -36,10 +39,11 @@ __device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b)
     s.n = (int)min((int64_t)max(a.cu_q[b + 1], 0), a.T) - s.q0;
     s.L = (int)min((int64_t)max(a.kv_len[b], 0), min(a.max_kv, a.table_stride << a.cache.ps));
     s.lo = a.window > 0 ? max(0, s.L - s.n - a.window + 1) : 0;
-    s.first = s.lo / DECODE_UNIT;
+    s.first = KEYS == KEYS_SINKS && a.sinks >= (s.lo & ~31) ? 0 : s.lo / DECODE_UNIT;
+    s.sink = KEYS == KEYS_SINKS ? min((a.sinks + DECODE_UNIT - 1) / DECODE_UNIT, s.first) : 0;
     const int64_t rows = (int64_t)s.n * a.group;
     const bool mine = s.n > 0 && s.n <= a.max_q && rows >= a.min_rows && rows <= a.max_rows;
-    s.units = mine ? max(1, (s.L + DECODE_UNIT - 1) / DECODE_UNIT - s.first) : 0;
+    s.units = mine ? max(1, (s.L + DECODE_UNIT - 1) / DECODE_UNIT - s.first + s.sink) : 0;
     return s;
 }
 
@@ -50,6 +54,7 @@ struct LaneUnits {
     SeqUnits own;
 };
 
+template <int KEYS>
 __device__ __forceinline__ LaneUnits lane_units(const AttnArgs &a, int lane)
 {
     LaneUnits u{};
@@ -57,7 +62,7 @@ __device__ __forceinline__ LaneUnits lane_units(const AttnArgs &a, int lane)
     for (int i = 0; i < u.per; ++i) {
         const int s = lane * u.per + i;
         if (s < a.n_seqs) {
-            u.own = seq_units(a, s);
+            u.own = seq_units<KEYS>(a, s);
             u.mine += u.own.units;
         }
     }
@@ -100,6 +105,7 @@ struct UnitPlace {
     SeqUnits sq;
 };
 
+template <int KEYS>
 __device__ __forceinline__ UnitPlace find_unit(const AttnArgs &a, const LaneUnits &u, uint32_t at)
 {
     UnitPlace p;
@@ -115,10 +121,11 @@ __device__ __forceinline__ UnitPlace find_unit(const AttnArgs &a, const LaneUnit
         p.sq.lo = __builtin_amdgcn_readlane(u.own.lo, src);
         p.sq.first = __builtin_amdgcn_readlane(u.own.first, src);
         p.sq.units = __builtin_amdgcn_readlane(u.own.units, src);
+        p.sq.sink = KEYS == KEYS_SINKS ? __builtin_amdgcn_readlane(u.own.sink, src) : 0;
     } else {
-        p.sq = seq_units(a, p.b);
+        p.sq = seq_units<KEYS>(a, p.b);
     }
-    for (; rest >= (uint32_t)p.sq.units * a.hkv; p.sq = seq_units(a, ++p.b))
+    for (; rest >= (uint32_t)p.sq.units * a.hkv; p.sq = seq_units<KEYS>(a, ++p.b))
         rest -= (uint32_t)p.sq.units * a.hkv;
     p.h = (int)(rest / (uint32_t)p.sq.units);
     p.f = (int)rest - p.h * p.sq.units;
@@ -145,7 +152,7 @@ constexpr int decode_lds = 4 * 2 * (32 * D > 32 * (D + 4) ? 32 * D : 32 * (D + 4
                            (NQ > 1 ? 16 * NQ * D * 2 : 0);
 
 // Share `share` of `shares` (or sequence and head `share`, see launch_attn_decode); smem: decode_lds bytes.
-template <int D, int NQ, bool FP8>
+template <int D, int NQ, bool FP8, int KEYS = KEYS_PLAIN>
 __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t share, uint32_t shares, uint8_t *smem)
 {
     constexpr int ESZ = FP8 ? 1 : 2;
@@ -174,16 +181,16 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         at.b = (int)(share / a.hkv);
         at.h = (int)(share - (unsigned)at.b * a.hkv);
         at.f = 0;
-        at.sq = seq_units(a, at.b);
+        at.sq = seq_units<KEYS>(a, at.b);
         left = at.sq.units;
     } else {
-        const LaneUnits u = lane_units(a, lane);
+        const LaneUnits u = lane_units<KEYS>(a, lane);
         const Shares cut((uint32_t)u.total * a.hkv, shares);
         if (share >= cut.n)
             return;
         const uint32_t u0 = cut.start(share);
         left = (int)(cut.start(share + 1) - u0);
-        at = find_unit(a, u, u0);
+        at = find_unit<KEYS>(a, u, u0);
     }
     int b = at.b, h = at.h, f = at.f;
     SeqUnits sq = at.sq;
@@ -193,7 +200,20 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
     while (left > 0) {
         const int end = min(sq.units, f + left);
         const int rows = sq.n * a.group, L = sq.L, head = turned_head(a, b, h);
-        const int k0 = max((sq.first + f) * DECODE_UNIT, sq.lo & ~31), k1 = min(L, (sq.first + end) * DECODE_UNIT);
+        int k0, k1, s1 = 0;         // keys [k0, k1); KEYS_SINKS: and those from unit f to s1 before them
+        if (KEYS == KEYS_SINKS) {
+            // (first keys that reach into the unit `first`: from its start on)
+            const int unit = max(sq.first, sq.first + f - sq.sink) * DECODE_UNIT;
+            k0 = max(unit, a.sinks > sq.first * DECODE_UNIT ? 0 : sq.lo & ~31);
+            k1 = min(L, (sq.first + end - sq.sink) * DECODE_UNIT);
+            if (f < sq.sink)
+                s1 = min(min(end, sq.sink) * DECODE_UNIT, a.sinks);
+            if (end <= sq.sink)
+                k0 = k1 = s1;
+        } else {
+            k0 = max((sq.first + f) * DECODE_UNIT, sq.lo & ~31);
+            k1 = min(L, (sq.first + end) * DECODE_UNIT);
+        }
         const int32_t *__restrict__ table = a.table + (int64_t)b * a.table_stride;
 
         u32x4 kr[2][LD], vr[2][LD];
@@ -225,12 +245,16 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                 }
             }
         };
+        // this wave's next step
+        auto after = [&](int kb) { return KEYS == KEYS_SINKS && kb < s1 && kb + STEP >= s1 ? k0 + 32 * wave : kb + STEP; };
         int kb = k0 + 32 * wave;
+        if (KEYS == KEYS_SINKS && f * DECODE_UNIT + 32 * wave < s1)
+            kb = f * DECODE_UNIT + 32 * wave;
         if (kb < k1) {
             lookup(kb);
             load(kb);
-            if (kb + STEP < k1)
-                lookup(kb + STEP);
+            if (after(kb) < k1)
+                lookup(after(kb));
         }
 
         // Q as B operand: column = row of the sequence, 8 values a k-step (e4m3 K comes 16 values a lane: two
@@ -278,6 +302,10 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         const uint32_t wlane = col * D * 2 + 16 * ((FP8 ? 2 * g : g) ^ ad_swz<D>(col));
         const int vk = 4 * g + (col >> 2);
         const uint32_t rlane = vk * D * 2 + 16 * (((col & 3) >> 1) ^ ad_swz<D>(vk)) + 8 * (col & 1);
+        auto sees = [&](int key, int pos) {
+            return key < L && (!a.causal || key <= pos) &&
+                   (a.window <= 0 || key > pos - a.window || (KEYS == KEYS_SINKS && key < a.sinks));
+        };
         auto step = [&](auto edge) {
             uint32_t qa = qlane;
             asm volatile("" : "+v"(qa));        // (keeps the compiler from holding Q and every address in registers)
@@ -311,7 +339,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int key = 16 * u + col;
-                const bool in = kb + key < L && kb + key >= sq.lo;
+                const bool in = kb + key < L && (kb + key >= sq.lo || (KEYS == KEYS_SINKS && kb + key < a.sinks));
 #pragma unroll
                 for (int s = 0; s < LD; ++s) {
                     u32x4 w[2];
@@ -342,10 +370,11 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                     vss[u] = vs[u];
             }
             // the next step's loads
-            if (kb + STEP < k1) {
-                load(kb + STEP);
-                if (kb + 2 * STEP < k1)
-                    lookup(kb + 2 * STEP);
+            const int next = after(kb);
+            if (next < k1) {
+                load(next);
+                if (after(next) < k1)
+                    lookup(after(next));
             }
             u32x4 pf[PARTS][NQ];
 #pragma unroll
@@ -356,9 +385,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int key = kb + 16 * u + 4 * g + i;
-                            const bool see = key < L && (!a.causal || key <= pos[j]) &&
-                                             (a.window <= 0 || key > pos[j] - a.window);
-                            st[j][u][i] = see ? st[j][u][i] : -INFINITY;
+                            st[j][u][i] = sees(key, pos[j]) ? st[j][u][i] : -INFINITY;
                         }
                 float mx = -INFINITY;
 #pragma unroll
@@ -448,8 +475,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
 #pragma unroll
                             for (int w = 0; w < PARTS; ++w)
                                 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(as_bf16x8(f), as_bf16x8(pf[w][j]), t, 0, 0, 0);
-                            const bool see = ka < L && (!a.causal || ka <= pos[j]) &&
-                                             (a.window <= 0 || ka > pos[j] - a.window);
+                            const bool see = sees(ka, pos[j]);
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
                                 o[j][d][i] = see ? t[i] : o[j][d][i];
@@ -473,7 +499,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         };
         // steps that hold a key which some query of the sequence does not see: below `free` and from `full` on
         const int full = L - sq.n + 1 - 32, free = a.window > 0 ? L - a.window : 0;
-        for (; kb < k1 && kb < free; kb += STEP)
+        for (; kb < k1 && kb < free; kb = after(kb))
             step(std::true_type());
         for (; kb < k1 && kb <= full; kb += STEP)
             step(std::false_type());
@@ -555,7 +581,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         if (++h == a.hkv) {
             h = 0;
             do
-                sq = seq_units(a, ++b);
+                sq = seq_units<KEYS>(a, ++b);
             while (sq.units == 0);
         }
         __syncthreads();

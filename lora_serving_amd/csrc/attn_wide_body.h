@@ -137,7 +137,9 @@ constexpr int wide_lds = KG * 4 * AW_BN * D * 2 + (SRC == AW_PAGES_E4M3 ? 4 * 2 
 
 // Item and kv head bx, and chunk of keys by; smem: wide_lds bytes.  Returns how many items there are.  (MORE: called
 // for several items.)
-template <int D, int SRC, int KG, bool MORE = false>
+// KEYS_SINKS: the tiles that hold the first keys and those of the window are numbered through, without the tiles that
+// no row of the workgroup sees between them; chunks are equal pieces of these numbers.
+template <int D, int SRC, int KG, bool MORE = false, int KEYS = KEYS_PLAIN>
 __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by, uint8_t *smem)
 {
     constexpr bool FP8 = SRC == AW_PAGES_E4M3;
@@ -175,19 +177,29 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     const int pos = L - n + ri;
     auto first_key = [&](int r) { return a.window > 0 ? max(0, L - n + min(r, rows - 1) / a.group - a.window + 1) : 0; };
     auto end_key = [&](int r) { return a.causal ? min(L, L - n + min(r, rows - 1) / a.group + 1) : L; };
-    const int c0 = by * a.chunk;
+    const int c0 = KEYS == KEYS_SINKS ? 0 : by * a.chunk;
     const int kmin = max(first_key(rb * BM), c0);
-    const int kmax = (int)min((int64_t)end_key(rb * BM + BM - 1), (int64_t)c0 + a.chunk);
-    if (by > 0 && kmin >= kmax)
+    const int kmax = KEYS == KEYS_SINKS ? end_key(rb * BM + BM - 1)
+                                        : (int)min((int64_t)end_key(rb * BM + BM - 1), (int64_t)c0 + a.chunk);
+    if (KEYS != KEYS_SINKS && by > 0 && kmin >= kmax)
         return it.total;
     const int wrow = rb * BM + wave * 32;
     const int wmin = first_key(wrow), wmax = wrow < rows ? end_key(wrow + 31) : 0;
     // the tiles, or this half's of them
-    const int ta = kmin / BN, tb = kmax > kmin ? (kmax + BN - 1) / BN : ta, tm = KG > 1 ? ta + (tb - ta + 1) / 2 : tb;
+    int ta = kmin / BN, tb = kmax > kmin ? (kmax + BN - 1) / BN : ta;
+    // KEYS_SINKS: tiles from number ts on lie `skip` tiles further
+    const int ts = KEYS == KEYS_SINKS ? min((a.sinks + BN - 1) / BN, ta) : 0, skip = KEYS == KEYS_SINKS ? ta - ts : 0;
+    auto place = [&](int t) { return KEYS == KEYS_SINKS && t >= ts ? t + skip : t; };
+    if (KEYS == KEYS_SINKS) {
+        const int all = tb - skip;
+        ta = (int)((int64_t)all * by / a.n_chunks);
+        tb = (int)((int64_t)all * (by + 1) / a.n_chunks);
+    }
+    const int tm = KG > 1 ? ta + (tb - ta + 1) / 2 : tb;
     const int t0 = kg ? tm : ta, t1 = kg ? tb : tm;
     // tiles [f0, f1): every row of the workgroup sees every key
-    const int f0 = max(t0, (first_key(rb * BM + BM - 1) + BN - 1) / BN);
-    const int f1 = max(min(t1, min(kmax, end_key(rb * BM)) / BN), f0);
+    const int f0 = max(t0, (first_key(rb * BM + BM - 1) + BN - 1) / BN - skip);
+    const int f1 = max(min(t1, min(kmax, end_key(rb * BM)) / BN - skip), f0);
 
     u32x4 qf[KS];
     {
@@ -220,8 +232,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
                                               : (uint32_t)r * D * (FP8 ? 1 : 2));
         off_v[i] = SRC == AW_ROWS ? piece[i] + (uint32_t)(w16 + r) * (uint32_t)(2 * a.v_stride) : off_k[i];
     }
-    const uint16_t *kp = a.k + ((int64_t)key0 + (int64_t)t0 * BN) * a.k_stride + (int64_t)h * D;   // rows: the next tile
-    const uint16_t *vp = a.v + ((int64_t)key0 + (int64_t)t0 * BN) * a.v_stride + (int64_t)h * D;
+    const uint16_t *kp = a.k + ((int64_t)key0 + (int64_t)place(t0) * BN) * a.k_stride + (int64_t)h * D;   // rows: the next tile
+    const uint16_t *vp = a.v + ((int64_t)key0 + (int64_t)place(t0) * BN) * a.v_stride + (int64_t)h * D;
     int pgs = 0, pgk = 0, pgv = 0;
     u32x4 kr[IPW], vr[IPW];
     float scr = 0.f;
@@ -230,25 +242,28 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     // chunk split into pieces of a few tiles waits longer for its first: 100 tokens over 8192 39.4 us, so 40.1)
     auto lookup = [&](int t) {
         if (SRC != AW_ROWS)
-            pgs = table[min(((t & ~63) + lane) * BN + w16, L - 1) >> ps];
+            pgs = table[min(place((t & ~63) + lane) * BN + w16, L - 1) >> ps];
     };
     // (to: where the tile goes, bytes of LDS, this wave's rows)
     auto copy = [&](int t, const uint16_t *&rows, int64_t stride, const uint8_t *pages, int pg, const uint32_t (&off)[IPW],
                     uint32_t to, u32x4 (&regs)[IPW]) __attribute__((always_inline)) {
+        const int p = place(t);
         if (SRC == AW_ROWS) {
-            if (t * BN + BN <= L) {
+            if (p * BN + BN <= L) {
 #pragma unroll
                 for (int i = 0; i < IPW; ++i)
                     aw_dma(rows, off[i], to, RPI * i * D * 2);
             } else {
 #pragma unroll
                 for (int i = 0; i < IPW; ++i)
-                    aw_dma(rows, (uint32_t)min(w16 + RPI * i + crow, L - 1 - t * BN) * (uint32_t)(2 * stride) + piece[i],
+                    aw_dma(rows, (uint32_t)min(w16 + RPI * i + crow, L - 1 - p * BN) * (uint32_t)(2 * stride) + piece[i],
                            to, RPI * i * D * 2);
             }
             rows += BN * stride;
+            if (KEYS == KEYS_SINKS && t + 1 == ts)
+                rows += (int64_t)skip * BN * stride;
         } else {
-            const int64_t at = (((int64_t)uniform(pg) * a.cache.hkv + h) << ps) + ((t * BN + w16) & pm);
+            const int64_t at = (((int64_t)uniform(pg) * a.cache.hkv + h) << ps) + ((p * BN + w16) & pm);
             const uint8_t *base = pages + at * D * (FP8 ? 1 : 2);
 #pragma unroll
             for (int i = 0; i < IPW; ++i)
@@ -268,7 +283,7 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             copy(t + 1, kp, a.k_stride, a.cache.k, pgk, off_k, to_k + ((t + 1) & 1) * (2 * TILE), kr);
             if (FP8 && lane < 32)       // scales of K and of V, both of tile t + 1 (this wave's rows)
                 scr = (lane < 16 ? a.cache.k_scale : a.cache.v_scale)[(((int64_t)pgk * a.cache.hkv + h) << ps) +
-                                                                      (((t + 1) * BN + w16 + (lane & 15)) & pm)];
+                                                                      ((place(t + 1) * BN + w16 + (lane & 15)) & pm)];
         }
     };
     auto issue_v = [&](int t) __attribute__((always_inline)) {
@@ -353,14 +368,17 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
         for (int i = 0; i < 8; ++i)
             scaled(t, i >> 2, i & 3, st);
     };
+    auto sees = [&](int key) {
+        return key < L && (!a.causal || key <= pos) &&
+               (a.window <= 0 || key > pos - a.window || (KEYS == KEYS_SINKS && key < a.sinks));
+    };
     auto hide = [&](int t, f32x16 (&st)[2]) {
+        const int key0 = place(t) * BN;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const int key = t * BN + 32 * u + 8 * (i / 4) + 4 * hh + i % 4;
-                const bool see = key < L && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
-                st[u][i] = see ? st[u][i] : -INFINITY;
+                st[u][i] = sees(key0 + 32 * u + 8 * (i / 4) + 4 * hh + i % 4) ? st[u][i] : -INFINITY;
             }
     };
     auto largest = [&](const f32x16 &s, int i0, int i1, float mx) {
@@ -517,8 +535,7 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
         const uint64_t some = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)bad, 32) << 32) | (uint32_t)uniform((int)bad);
         for (uint64_t rest = some; rest; rest &= rest - 1) {
             const int bit = __ffsll((unsigned long long)rest) - 1, s = (bit & 31) >> 3, e = bit & 7;
-            const int key = t * BN + 16 * s + 8 * (e >> 2) + 4 * (bit >> 5) + (e & 3);
-            const bool see = key < L && (!a.causal || key <= pos) && (a.window <= 0 || key > pos - a.window);
+            const bool see = sees(place(t) * BN + 16 * s + 8 * (e >> 2) + 4 * (bit >> 5) + (e & 3));
             const uint32_t half = hh != (bit >> 5) ? 0u : (e & 1) ? 0xffff0000u : 0xffffu;
             u32x4 p;
 #pragma unroll
@@ -554,7 +571,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     };
     // a tile on its own (K of it in place before; afterwards K of the next)
     auto single = [&](int t) {
-        const bool work = t * BN < wmax && t * BN + BN > wmin;
+        const int key0 = place(t) * BN;
+        const bool work = key0 < wmax && (key0 + BN > wmin || (KEYS == KEYS_SINKS && key0 < a.sinks));
         if (t > t0)
             issue(t);
         if (work) {
@@ -692,11 +710,11 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
 }
 
 // Over pages: item and kv head bx, and every wide_x-th after it (wide_x: a multiple of the kv heads).
-template <int D, int SRC>
+template <int D, int SRC, int KEYS = KEYS_PLAIN>
 __device__ __forceinline__ void attn_wide_pages(const AttnArgs &a, int bx, int by, int wide_x, uint8_t *smem)
 {
     for (int64_t x = bx;; x += wide_x) {
-        const int total = attn_wide_body<D, SRC, 1, true>(a, (int)x, by, smem);
+        const int total = attn_wide_body<D, SRC, 1, true, KEYS>(a, (int)x, by, smem);
         if (x + wide_x >= (int64_t)total * a.hkv)
             return;
         __syncthreads();

@@ -198,7 +198,7 @@ mlora_status cache_read(PyObject *const *a)
     return unlocked([&] { return mlora_cache_read(c, slot, T, out[0], out[1], s); });
 }
 
-// (q, k, v, cu_q, out, cu_k, max_q, causal, window, scale, lse, stream)
+// (q, k, v, cu_q, out, cu_k, max_q, causal, window, scale, lse, stream, sinks)
 mlora_status attention(PyObject *const *a)
 {
     const Rows q = rows(a[0], "q"), k = rows(a[1], "k"), v = rows(a[2], "v", &k), out = rows(a[4], "out", &q);
@@ -207,17 +207,18 @@ mlora_status attention(PyObject *const *a)
     const int64_t n = tensor(a[3], "cu_q").numel() - 1;
     const int32_t *const cu_q = ints(a[3], "cu_q", n + 1), *const cu_k = a[5] == Py_None ? nullptr : ints(a[5], "cu_k", n + 1);
     const int64_t max_q = a[6] == Py_None ? q.n : integer(a[6]);
-    const int32_t causal = truth(a[7]), window = int32(a[8], "window");
+    const int32_t causal = truth(a[7]), window = int32(a[8], "window"), sinks = int32(a[12], "sinks");
     const float scale = (float)real(a[9]);
     float *const lse = lse_of(a[10], q.n, q.heads);
     const hipStream_t s = stream(a[11]);
     return unlocked([&] {
-        return mlora_attention(q.p, q.stride, k.p, k.stride, v.p, v.stride, q.n, k.n, (int32_t)n, cu_q, cu_k, (int32_t)q.heads,
-                               (int32_t)k.heads, (int32_t)q.d, max_q, causal, window, scale, out.p, out.stride, lse, s);
+        return mlora_attention_sinks(q.p, q.stride, k.p, k.stride, v.p, v.stride, q.n, k.n, (int32_t)n, cu_q, cu_k,
+                                     (int32_t)q.heads, (int32_t)k.heads, (int32_t)q.d, max_q, causal, window, sinks, scale,
+                                     out.p, out.stride, lse, s);
     });
 }
 
-// (q, cache, page_table, cu_q, kv_len, out, max_q, max_kv, causal, window, scale, lse, ws, stream)
+// (q, cache, page_table, cu_q, kv_len, out, max_q, max_kv, causal, window, scale, lse, ws, stream, sinks)
 mlora_status paged_attention(PyObject *const *a)
 {
     const Rows q = rows(a[0], "q"), out = rows(a[5], "out", &q);
@@ -240,13 +241,13 @@ mlora_status paged_attention(PyObject *const *a)
     const int32_t *const pages = ints(a[2], "page_table", table.numel()), *const cu_q = ints(a[3], "cu_q", n + 1),
                   *const kv_len = ints(a[4], "kv_len", n);
     const int64_t width = table.size(1), max_q = integer(a[6]), max_kv = integer(a[7]);
-    const int32_t causal = truth(a[8]), window = int32(a[9], "window");
+    const int32_t causal = truth(a[8]), window = int32(a[9], "window"), sinks = int32(a[14], "sinks");
     const float scale = (float)real(a[10]);
     float *const lse = lse_of(a[11], q.n, q.heads);
     const hipStream_t s = stream(a[13]);
     return unlocked([&] {
-        return mlora_paged_attention(q.p, q.stride, q.n, (int32_t)q.heads, c, pages, width, (int32_t)n, cu_q, kv_len, max_q, max_kv,
-                                     causal, window, scale, out.p, out.stride, lse, ws, ws_bytes, s);
+        return mlora_paged_attention_sinks(q.p, q.stride, q.n, (int32_t)q.heads, c, pages, width, (int32_t)n, cu_q, kv_len,
+                                           max_q, max_kv, causal, window, sinks, scale, out.p, out.stride, lse, ws, ws_bytes, s);
     });
 }
 
@@ -268,8 +269,8 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 }
 
 #define METHOD(name, f, n) {name, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {METHOD("qk_rope", qk_rope, 14), METHOD("cache_read", cache_read, 5), METHOD("attention", attention, 12),
-                         METHOD("paged_attention", paged_attention, 14), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {METHOD("qk_rope", qk_rope, 14), METHOD("cache_read", cache_read, 5), METHOD("attention", attention, 13),
+                         METHOD("paged_attention", paged_attention, 15), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

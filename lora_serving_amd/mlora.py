@@ -48,7 +48,8 @@ EXPORTS = ("mlora_status_string", "mlora_last_error", "mlora_factor", "mlora_slo
            "mlora_validate", "mlora_plan", "mlora_shrink", "mlora_expand", "mlora_linear",
            "mlora_linear_path", "mlora_linear_noalloc", "mlora_rope_turns", "mlora_cache_bytes",
            "mlora_qk_rope", "mlora_cache_read", "mlora_attention", "mlora_paged_workspace_size",
-           "mlora_paged_attention", "mlora_validate_pages", "mlora_trace_start",
+           "mlora_paged_attention", "mlora_validate_pages", "mlora_attention_sinks",
+           "mlora_paged_attention_sinks", "mlora_validate_pages_sinks", "mlora_trace_start",
            "mlora_trace_stop")
 
 _P = ctypes.c_void_p
@@ -133,6 +134,16 @@ _lib.mlora_paged_attention.argtypes = [_P, _i64, _i64, _i32, _CACHE_P, _P, _i64,
 _lib.mlora_validate_pages.restype = ctypes.c_int
 _lib.mlora_validate_pages.argtypes = [_CACHE_P, _P, _i64, _i32, _P, _P, _i64, _i64, _i64,
                                       ctypes.POINTER(_i64)]
+_lib.mlora_attention_sinks.restype = ctypes.c_int
+_lib.mlora_attention_sinks.argtypes = [_P, _i64, _P, _i64, _P, _i64, _i64, _i64, _i32, _P, _P, _i32,
+                                       _i32, _i32, _i64, _i32, _i32, _i32, _f32, _P, _i64, _P, _P]
+_lib.mlora_paged_attention_sinks.restype = ctypes.c_int
+_lib.mlora_paged_attention_sinks.argtypes = [_P, _i64, _i64, _i32, _CACHE_P, _P, _i64, _i32, _P, _P,
+                                             _i64, _i64, _i32, _i32, _i32, _f32, _P, _i64, _P, _P,
+                                             ctypes.c_size_t, _P]
+_lib.mlora_validate_pages_sinks.restype = ctypes.c_int
+_lib.mlora_validate_pages_sinks.argtypes = [_CACHE_P, _P, _i64, _i32, _P, _P, _i64, _i64, _i64, _i32,
+                                            _i32, ctypes.POINTER(_i64)]
 _lib.mlora_trace_start.restype = ctypes.c_int
 _lib.mlora_trace_start.argtypes = [_i32]
 _lib.mlora_trace_stop.restype = _i32
@@ -485,12 +496,13 @@ def mlora_cache_read(cache: Cache, slot, k, v, stream=None):
 
 
 def mlora_attention(q, k, v, cu_q, out, cu_k=None, max_q: int | None = None, causal: bool = True,
-                    window: int = 0, scale: float = 0.0, lse=None, stream=None):
+                    window: int = 0, scale: float = 0.0, lse=None, stream=None, sinks: int = 0):
     """q, out bf16 [T_q][n_q_heads][head_dim], k, v bf16 [T_k][n_kv_heads][head_dim], rows of any
     stride (views of a merged row); cu_q, cu_k int32 [n_seqs + 1] device.  max_q: the longest
-    sequence's queries (None: T_q)."""
+    sequence's queries (None: T_q).  sinks: first keys that stay visible behind the window
+    (mlora_attention_sinks)."""
     code = _calls.attention(q, k, v, cu_q, out, cu_k, max_q, causal, window, scale, lse,
-                            _stream(stream))
+                            _stream(stream), sinks)
     if code:
         _check(code, "mlora_attention")
 
@@ -513,19 +525,21 @@ def paged_workspace(T: int, n_seqs: int, n_q_heads: int, n_kv_heads: int, head_d
 
 def mlora_paged_attention(q, cache: Cache, page_table, cu_q, kv_len, out, max_q: int,
                           max_kv: int, causal: bool = True, window: int = 0, scale: float = 0.0,
-                          lse=None, ws=None, stream=None):
+                          lse=None, ws=None, stream=None, sinks: int = 0):
     """q, out bf16 [T][n_q_heads][head_dim] (rows of any stride); page_table int32
-    [n_seqs][pages], cu_q int32 [n_seqs + 1], kv_len int32 [n_seqs], device."""
+    [n_seqs][pages], cu_q int32 [n_seqs + 1], kv_len int32 [n_seqs], device.  sinks: first tokens
+    that stay visible behind the window (mlora_paged_attention_sinks)."""
     code = _calls.paged_attention(q, cache.address, page_table, cu_q, kv_len, out, max_q, max_kv,
-                                  causal, window, scale, lse, ws, _stream(stream))
+                                  causal, window, scale, lse, ws, _stream(stream), sinks)
     if code:
         _check(code, "mlora_paged_attention")
 
 
 def mlora_validate_pages(cache: Cache, page_table, cu_q, kv_len, T: int, max_q: int,
-                         max_kv: int):
+                         max_kv: int, window: int = 0, sinks: int = 0):
     """Host check of a paged batch (host int32 tensors or arrays); returns (status, offending
-    value)."""
+    value).  With a window, pages that it and the first `sinks` tokens leave out are not looked at
+    (mlora_validate_pages_sinks)."""
     import numpy as np
     table = np.ascontiguousarray(page_table, dtype=np.int32)
     cu = np.ascontiguousarray(cu_q, dtype=np.int32)
@@ -534,9 +548,10 @@ def mlora_validate_pages(cache: Cache, page_table, cu_q, kv_len, T: int, max_q: 
         raise ValueError("page_table [n_seqs][pages], cu_q [n_seqs + 1] and kv_len [n_seqs] "
                          "do not agree")
     bad = _i64(0)
-    code = _lib.mlora_validate_pages(cache.ref, table.ctypes.data_as(_P), table.shape[1],
-                                     lens.size, cu.ctypes.data_as(_P), lens.ctypes.data_as(_P),
-                                     T, max_q, max_kv, ctypes.byref(bad))
+    code = _lib.mlora_validate_pages_sinks(cache.ref, table.ctypes.data_as(_P), table.shape[1],
+                                           lens.size, cu.ctypes.data_as(_P),
+                                           lens.ctypes.data_as(_P), T, max_q, max_kv, window,
+                                           sinks, ctypes.byref(bad))
     return code, int(bad.value)
 
 
