@@ -480,6 +480,38 @@ mlora_status mlora_validate_pages_sinks(const mlora_cache *cache, const int32_t 
                                         int64_t *bad_value);
 
 /*
+ * mlora_paged_attention (without a window) of a batch whose sequences share first tokens: sequences
+ * [group_start[g], group_start[g + 1]) hold the same first prefix_len[g] tokens in the cache, and these are read once for
+ * the group, from the pages of its first sequence, instead of once a sequence.
+ *   group_start int32 [n_groups + 1] device, ascending from 0 (read as at most n_seqs; sequences from the last entry on
+ *       are in no group);  prefix_len int32 [n_groups] device, read as at most max_prefix and table_stride * page_size.
+ *       A group may be empty, of one sequence, or share nothing.
+ *   max_prefix  host upper bound of prefix_len
+ * page_table and kv_len are mlora_paged_attention's, with all tokens of every sequence; a sequence whose queries do not
+ * all see the whole prefix (kv_len less its queries, if causal, is below prefix_len) is answered from its own pages.  A group's first
+ * sequence must hold the whole prefix.  Probabilities of shared keys are rounded to bf16 for the product with V.
+ *   ws  mlora_prefix_workspace_size() bytes for the same sizes, or for larger ones of the same heads; the size
+ *       never falls as any of them rises (0 where the call would refuse them)
+ * mlora_validate_prefixes checks the groups on the host (all pointers host): group_start, 0 <= prefix_len <= max_prefix,
+ * and that the table and each first sequence's kv_len reach that far; MLORA_ERR_SHAPE and the value where not.
+ */
+size_t mlora_prefix_workspace_size(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t n_q_heads,
+                                   int32_t n_kv_heads, int32_t head_dim, int64_t max_q,
+                                   int64_t max_kv, int64_t max_prefix);
+mlora_status mlora_prefix_attention(const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads,
+                                    const mlora_cache *cache, const int32_t *page_table,
+                                    int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
+                                    const int32_t *kv_len, int32_t n_groups,
+                                    const int32_t *group_start, const int32_t *prefix_len,
+                                    int64_t max_q, int64_t max_kv, int64_t max_prefix, int32_t causal,
+                                    float scale, void *out, int64_t out_stride, float *lse, void *ws,
+                                    size_t ws_bytes, hipStream_t stream);
+mlora_status mlora_validate_prefixes(const mlora_cache *cache, int64_t table_stride, int32_t n_seqs,
+                                     const int32_t *kv_len, int32_t n_groups,
+                                     const int32_t *group_start, const int32_t *prefix_len,
+                                     int64_t max_prefix, int64_t *bad_value);
+
+/*
  * Profiling hook (not part of the computation).  mlora_trace_start creates 2*capacity HIP
  * events (no device memory); from then on every mlora_linear call records one event on its
  * stream right before and one right after each launch of its main product kernel (the decode

@@ -55,9 +55,17 @@ struct AttnArgs {
     float *part_o, *part_ml;       // [..][head_dim], [..][2]
     int32_t min_rows, max_rows;    // sequences this launch answers: rows = queries * group
     int32_t sinks;                 // first keys that stay visible behind the window (0, or a window is set)
+    // Sequences that share first keys: group g is the sequences [group_start[g], group_start[g + 1]), of which
+    // prefix_len[g] keys are shared.  Parts of a row in row_parts slots of its own from slot row_slot on ([token][head]
+    // [row_parts]), this launch's from number row_first on; cuts: where the decode kernel left a sequence and head.
+    const int32_t *group_start, *prefix_len;
+    int32_t n_groups, row_first, row_parts;
+    int64_t max_prefix, row_slot;
+    int32_t *cuts;                 // [n_seqs][hkv][2]: -1 (a slot of the row), or the first and last share
 };
-// Which keys a kernel's queries see, besides the causal limit: all or a window of them; a window and the first ones.
-enum { KEYS_PLAIN = 0, KEYS_SINKS = 1 };
+// Which keys a kernel's queries see, besides the causal limit: all or a window of them; a window and the first ones;
+// those that a group's sequences share (the group's rows are one sequence's); a sequence's others.
+enum { KEYS_PLAIN = 0, KEYS_SINKS = 1, KEYS_SHARED = 2, KEYS_OWN = 3 };
 // Whole prompts (cache unused) or, with pages, chunks of new tokens.
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream);
 constexpr int64_t CUS = 256;      // of an MI355X
@@ -88,5 +96,12 @@ hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int share
 hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream);
 // Both kinds of sequences over pages in one launch: w as for launch_attn_wide, d as for launch_attn_decode (nq 1).
 hipError_t launch_attn_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int shares, hipStream_t stream);
+
+// Sequences that share first keys: s (wide: the shared keys, n_chunks chunks), w and d (their own ones; as for
+// launch_attn_mixed, but `wide` = false: no sequence has more rows than 16 nq) in one launch, and the join of all parts.
+hipError_t launch_attn_prefix(const AttnArgs &s, const AttnArgs &w, const AttnArgs &d, int head_dim, bool wide, int nq,
+                              int shares, hipStream_t stream);
+hipError_t launch_attn_prefix_join(const AttnArgs &s, const AttnArgs &w, const AttnArgs &d, int head_dim,
+                                   hipStream_t stream);
 
 }  // namespace mlora

@@ -192,6 +192,58 @@ size_t paged_room(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d,
     return dec + wide;
 }
 
+// How a call over shared prefixes is cut: the decode and wide parts as in paged_plan (always with parts, for the join
+// takes a row's own keys as one of them), and the shared keys in chunks that give the groups' row blocks
+// SHARED_WANT workgroups, of SHARED_LEAST keys or more.
+constexpr int64_t SHARED_WANT = 512, SHARED_LEAST = 256;
+int64_t shared_cuts(int64_t items, int64_t max_prefix)
+{
+    return std::max<int64_t>(1, std::min((SHARED_WANT + items - 1) / items, (max_prefix + SHARED_LEAST - 1) / SHARED_LEAST));
+}
+
+struct PrefixPlan {
+    PagedPlan own;
+    int64_t chunk = 0, chunks = 0;
+    int64_t share_slots = 0, row_parts = 0;     // parts of the decode kernel's shares, and of each row
+    size_t o = 0, ml = 0, cuts = 0;             // bytes
+    size_t total() const { return o + ml + cuts; }
+};
+
+size_t cut_bytes(int64_t n_seqs, int32_t hkv) { return align_up((size_t)n_seqs * hkv * 8); }
+
+PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv,
+                       int64_t max_prefix)
+{
+    PrefixPlan p;
+    p.own = paged_plan(T, n_seqs, hq, hkv, d, max_q, max_kv, 0, 0);
+    const int64_t units = (std::max<int64_t>(max_kv, 1) + DECODE_UNIT - 1) / DECODE_UNIT;
+    p.own.shares = p.own.dec_rows > 0 ? (int)std::min((int64_t)n_seqs * hkv * units, 2 * CUS) : 0;
+    p.share_slots = 2 * (int64_t)p.own.shares * p.own.dec_rows;
+    const int64_t n = shared_cuts((T * (hq / hkv) + WIDE_ROWS - 1) / WIDE_ROWS * hkv, max_prefix);
+    p.chunk = ((max_prefix + n - 1) / n + 63) & ~INT64_C(63);
+    p.chunks = (max_prefix + p.chunk - 1) / p.chunk;
+    p.row_parts = p.chunks + std::max<int64_t>(p.own.wide_chunks, 1);
+    const size_t slots = (size_t)p.share_slots + (size_t)T * hq * p.row_parts;
+    p.o = align_up(slots * d * 4);
+    p.ml = align_up(slots * 8);
+    p.cuts = cut_bytes(n_seqs, hkv);
+    return p;
+}
+
+// The most that prefix_plan asks for over all sizes up to these (see paged_room).
+size_t prefix_room(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv,
+                   int64_t max_prefix)
+{
+    const int64_t group = hq / hkv, most = max_q * group, units = (std::max<int64_t>(max_kv, 1) + DECODE_UNIT - 1) / DECODE_UNIT;
+    const size_t shares = 2 * (size_t)std::min((int64_t)n_seqs * hkv * units, 2 * CUS) * std::min<int64_t>(most, 32);
+    size_t rows = (size_t)T * hq * 2;
+    for (int64_t r = 1; r * hkv < SHARED_WANT && (r - 1) * WIDE_ROWS < T * group; ++r) {
+        const int64_t wide = most > 32 && r * hkv < WIDE_WHOLE ? wide_cuts(r * hkv, std::max<int64_t>(max_kv, 1)) : 1;
+        rows = std::max(rows, (size_t)std::min(T, r * WIDE_ROWS / group) * hq * (shared_cuts(r * hkv, max_prefix) + wide));
+    }
+    return align_up((shares + rows) * d * 4) + align_up((shares + rows) * 8) + cut_bytes(n_seqs, hkv);
+}
+
 mlora_status attention(const void *q, int64_t q_stride, const void *k, int64_t k_stride, const void *v,
                        int64_t v_stride, int64_t T_q, int64_t T_k, int32_t n_seqs, const int32_t *cu_q,
                        const int32_t *cu_k, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim, int64_t max_q,
@@ -248,20 +300,26 @@ mlora_status attention(const void *q, int64_t q_stride, const void *k, int64_t k
     return hip_status(e);
 }
 
-mlora_status paged_attention(const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads, const mlora_cache *cache,
-                             const int32_t *page_table, int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
-                             const int32_t *kv_len, int64_t max_q, int64_t max_kv, int32_t causal, int32_t window,
-                             int32_t sinks, float scale, void *out, int64_t out_stride, float *lse, void *ws,
-                             size_t ws_bytes, hipStream_t stream)
+// A paged call that has passed its checks (nothing: there is nothing to do).
+struct PagedCall {
+    AttnArgs a{};
+    int32_t d = 0;
+    bool nothing = false;
+};
+
+mlora_status paged_call(PagedCall *c, const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads, const mlora_cache *cache,
+                        const int32_t *page_table, int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
+                        const int32_t *kv_len, int64_t max_q, int64_t max_kv, int32_t causal, int32_t window,
+                        int32_t sinks, float scale, void *out, int64_t out_stride, float *lse)
 {
     if (T < 0 || n_seqs < 0 || max_q < 0 || max_kv < 0 || table_stride < 0 || window < 0 || sinks < 0 || !(scale >= 0.f) ||
         std::isinf(scale))
         return MLORA_ERR_ARG;
-    AttnArgs a{};
+    AttnArgs &a = c->a;
     mlora_status st = check_cache(cache, &a.cache);
     if (st != MLORA_OK)
         return st;
-    const int32_t d = cache->head_dim;
+    const int32_t d = c->d = cache->head_dim;
     st = check_heads(n_q_heads, cache->n_kv_heads, d);
     if (st != MLORA_OK)
         return st;
@@ -269,20 +327,12 @@ mlora_status paged_attention(const void *q, int64_t q_stride, int64_t T, int32_t
         return MLORA_ERR_SHAPE;
     if (!paged_sizes_ok(T, n_seqs, n_q_heads, cache->n_kv_heads, max_kv) || table_stride >= MAX_ROWS)
         return MLORA_ERR_UNSUPPORTED;
-    if (T == 0 || n_seqs == 0 || max_q == 0)
+    c->nothing = T == 0 || n_seqs == 0 || max_q == 0;
+    if (c->nothing)
         return MLORA_OK;
     if (q == nullptr || out == nullptr || cu_q == nullptr || kv_len == nullptr || !aligned16(q) || !aligned16(out) ||
         (max_kv > 0 && table_stride > 0 && page_table == nullptr))
         return MLORA_ERR_ARG;
-    max_q = std::min(max_q, T);
-    a.window = seen_window(window, max_kv);
-    a.sinks = seen_sinks(sinks, a.window, max_kv);
-    const PagedPlan p = paged_plan(T, n_seqs, n_q_heads, cache->n_kv_heads, d, max_q, max_kv, a.window, a.sinks);
-    if (p.wide_chunks > 65535)
-        return MLORA_ERR_UNSUPPORTED;
-    uint8_t *base = (uint8_t *)(((uintptr_t)ws + 255) & ~(uintptr_t)255);
-    if (p.total() > 0 && (ws == nullptr || ws_bytes < p.total() + (size_t)(base - (uint8_t *)ws)))
-        return MLORA_ERR_WORKSPACE;
     a.q = (const uint16_t *)q;
     a.q_stride = q_stride;
     a.out_stride = out_stride;
@@ -295,12 +345,34 @@ mlora_status paged_attention(const void *q, int64_t q_stride, int64_t T, int32_t
     a.kv_len = kv_len;
     a.table = page_table;
     a.table_stride = table_stride;
-    a.max_q = max_q;
+    a.max_q = std::min(max_q, T);
     a.max_kv = max_kv;
     a.causal = causal;
+    a.window = seen_window(window, max_kv);
+    a.sinks = seen_sinks(sinks, a.window, max_kv);
     a.scale = scale == 0.f ? (float)(1.0 / std::sqrt((double)d)) : scale;
     a.out = (uint16_t *)out;
     a.lse = lse;
+    return MLORA_OK;
+}
+
+// The aligned start of a workspace, or NULL where it has not `need` bytes from there.
+uint8_t *workspace(void *ws, size_t ws_bytes, size_t need)
+{
+    uint8_t *const base = (uint8_t *)(((uintptr_t)ws + 255) & ~(uintptr_t)255);
+    return ws != nullptr && ws_bytes >= need + (size_t)(base - (uint8_t *)ws) ? base : nullptr;
+}
+
+mlora_status run_paged(const PagedCall &c, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    AttnArgs a = c.a;
+    const int32_t d = c.d;
+    const PagedPlan p = paged_plan(a.T, a.n_seqs, a.hq, a.hkv, d, a.max_q, a.max_kv, a.window, a.sinks);
+    if (p.wide_chunks > 65535)
+        return MLORA_ERR_UNSUPPORTED;
+    uint8_t *const base = workspace(ws, ws_bytes, p.total());
+    if (p.total() > 0 && base == nullptr)
+        return MLORA_ERR_WORKSPACE;
     AttnArgs w = a;                     // the wide part
     w.min_rows = (int32_t)p.dec_rows + 1;
     w.max_rows = 0x7fffffff;
@@ -325,6 +397,18 @@ mlora_status paged_attention(const void *q, int64_t q_stride, int64_t T, int32_t
         e = launch_attn_combine(a, d, p.shares, stream);
     trace_mark(stream, false);
     return hip_status(e);
+}
+
+mlora_status paged_attention(const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads, const mlora_cache *cache,
+                             const int32_t *page_table, int64_t table_stride, int32_t n_seqs, const int32_t *cu_q,
+                             const int32_t *kv_len, int64_t max_q, int64_t max_kv, int32_t causal, int32_t window,
+                             int32_t sinks, float scale, void *out, int64_t out_stride, float *lse, void *ws,
+                             size_t ws_bytes, hipStream_t stream)
+{
+    PagedCall c;
+    const mlora_status st = paged_call(&c, q, q_stride, T, n_q_heads, cache, page_table, table_stride, n_seqs, cu_q, kv_len,
+                                       max_q, max_kv, causal, window, sinks, scale, out, out_stride, lse);
+    return st != MLORA_OK || c.nothing ? st : run_paged(c, ws, ws_bytes, stream);
 }
 
 mlora_status validate_pages(const mlora_cache *cache, const int32_t *page_table, int64_t table_stride, int32_t n_seqs,
@@ -539,6 +623,109 @@ mlora_status mlora_paged_attention_sinks(const void *q, int64_t q_stride, int64_
 {
     return paged_attention(q, q_stride, T, n_q_heads, cache, page_table, table_stride, n_seqs, cu_q, kv_len, max_q, max_kv,
                            causal, window, sinks, scale, out, out_stride, lse, ws, ws_bytes, stream);
+}
+
+size_t mlora_prefix_workspace_size(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t n_q_heads, int32_t n_kv_heads,
+                                   int32_t head_dim, int64_t max_q, int64_t max_kv, int64_t max_prefix)
+{
+    if (n_groups < 0 || max_prefix < 0 || max_prefix >= MAX_KEYS)
+        return 0;
+    const size_t paged = mlora_paged_workspace_size(T, n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_kv);
+    if (paged == 0 || n_groups == 0 || max_prefix == 0)
+        return paged;
+    return std::max(paged, prefix_room(T, n_seqs, n_q_heads, n_kv_heads, head_dim, std::min(max_q, T), max_kv, max_prefix) + 256);
+}
+
+mlora_status mlora_prefix_attention(const void *q, int64_t q_stride, int64_t T, int32_t n_q_heads,
+                                    const mlora_cache *cache, const int32_t *page_table, int64_t table_stride,
+                                    int32_t n_seqs, const int32_t *cu_q, const int32_t *kv_len, int32_t n_groups,
+                                    const int32_t *group_start, const int32_t *prefix_len, int64_t max_q,
+                                    int64_t max_kv, int64_t max_prefix, int32_t causal, float scale, void *out,
+                                    int64_t out_stride, float *lse, void *ws, size_t ws_bytes, hipStream_t stream)
+{
+    if (n_groups < 0 || max_prefix < 0)
+        return MLORA_ERR_ARG;
+    if (max_prefix >= MAX_KEYS)
+        return MLORA_ERR_UNSUPPORTED;
+    PagedCall c;
+    const mlora_status st = paged_call(&c, q, q_stride, T, n_q_heads, cache, page_table, table_stride, n_seqs, cu_q, kv_len,
+                                       max_q, max_kv, causal, 0, 0, scale, out, out_stride, lse);
+    if (st != MLORA_OK || c.nothing)
+        return st;
+    if (n_groups > 0 && (group_start == nullptr || prefix_len == nullptr))
+        return MLORA_ERR_ARG;
+    max_prefix = std::min(max_prefix, max_kv);
+    if (n_groups == 0 || max_prefix == 0)
+        return run_paged(c, ws, ws_bytes, stream);
+    const AttnArgs &a = c.a;
+    const PrefixPlan p = prefix_plan(a.T, a.n_seqs, a.hq, a.hkv, c.d, a.max_q, a.max_kv, max_prefix);
+    if (p.own.wide_chunks > 65535)
+        return MLORA_ERR_UNSUPPORTED;
+    uint8_t *const base = workspace(ws, ws_bytes, p.total());
+    if (base == nullptr)
+        return MLORA_ERR_WORKSPACE;
+    AttnArgs d = a;                     // the decode rows' own keys
+    d.max_rows = (int32_t)p.own.dec_rows;
+    d.part_o = (float *)base;
+    d.part_ml = (float *)(base + p.o);
+    d.group_start = group_start;
+    d.prefix_len = prefix_len;
+    d.n_groups = n_groups;
+    d.max_prefix = max_prefix;
+    d.row_slot = p.share_slots;
+    d.row_parts = (int32_t)p.row_parts;
+    d.row_first = (int32_t)p.chunks;
+    d.cuts = (int32_t *)(base + p.o + p.ml);
+    AttnArgs w = d;                     // the wide ones'
+    w.min_rows = d.max_rows + 1;
+    w.max_rows = 0x7fffffff;
+    w.chunk = (int32_t)p.own.wide_chunk;
+    w.n_chunks = (int32_t)std::max<int64_t>(p.own.wide_chunks, 1);
+    AttnArgs s = d;                     // and the shared ones
+    s.max_q = a.T;
+    s.chunk = (int32_t)p.chunk;
+    s.n_chunks = (int32_t)p.chunks;
+    s.row_first = 0;
+    trace_mark(stream, true);
+    hipError_t e = launch_attn_prefix(s, w, d, c.d, p.own.wide, p.own.nq, p.own.shares, stream);
+    if (e == hipSuccess)
+        e = launch_attn_prefix_join(s, w, d, c.d, stream);
+    trace_mark(stream, false);
+    return hip_status(e);
+}
+
+mlora_status mlora_validate_prefixes(const mlora_cache *cache, int64_t table_stride, int32_t n_seqs,
+                                     const int32_t *kv_len, int32_t n_groups, const int32_t *group_start,
+                                     const int32_t *prefix_len, int64_t max_prefix, int64_t *bad_value)
+{
+    if (cache == nullptr || table_stride < 0 || n_seqs < 0 || n_groups < 0 || max_prefix < 0)
+        return MLORA_ERR_ARG;
+    const mlora_status st =
+        check_cache_sizes(cache->n_pages, cache->n_kv_heads, cache->page_size, cache->head_dim, cache->dtype);
+    if (st != MLORA_OK)
+        return st;
+    if (table_stride >= MAX_ROWS)
+        return MLORA_ERR_UNSUPPORTED;
+    if (n_groups == 0)
+        return MLORA_OK;
+    if (group_start == nullptr || prefix_len == nullptr || (n_seqs > 0 && kv_len == nullptr))
+        return MLORA_ERR_ARG;
+    const auto bad = [bad_value](int64_t v) {
+        if (bad_value)
+            *bad_value = v;
+        return MLORA_ERR_SHAPE;
+    };
+    if (group_start[0] != 0)
+        return bad(group_start[0]);
+    for (int32_t g = 0; g < n_groups; ++g) {
+        const int32_t b0 = group_start[g], b1 = group_start[g + 1];
+        if (b1 < b0 || b1 > n_seqs)
+            return bad(b1);
+        const int64_t keys = prefix_len[g];
+        if (keys < 0 || keys > max_prefix || keys > table_stride * cache->page_size || (b1 > b0 && keys > kv_len[b0]))
+            return bad(keys);
+    }
+    return MLORA_OK;
 }
 
 mlora_status mlora_validate_pages(const mlora_cache *cache, const int32_t *page_table, int64_t table_stride,

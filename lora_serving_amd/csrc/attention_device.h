@@ -143,6 +143,44 @@ __device__ __forceinline__ void join_parts(const AttnArgs &a, int ca, int cb, Sl
         a.lse[t * a.hq + hd] = sum == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
 }
 
+// A group of sequences [b0, b1) that share their first `keys` keys, read from the first one's pages.  A sequence alone
+// shares nothing.
+struct Group {
+    int b0, b1, keys;
+};
+
+__device__ __forceinline__ Group group_at(const AttnArgs &a, int g)
+{
+    Group r;
+    r.b0 = min(max(a.group_start[g], 0), a.n_seqs);
+    r.b1 = min(max(a.group_start[g + 1], 0), a.n_seqs);
+    const int keys = (int)min((int64_t)max(a.prefix_len[g], 0), min(a.max_prefix, a.table_stride << a.cache.ps));
+    r.keys = r.b1 - r.b0 >= 2 ? keys : 0;
+    return r;
+}
+
+// How many of sequence b's L keys (n of them its queries') are its group's: all of those, or none if some query does
+// not see them.
+__device__ __forceinline__ int shared_keys(const AttnArgs &a, int b, int n, int L)
+{
+    int lo = 0, hi = a.n_groups;
+    while (hi - lo > 1) {           // the last group that starts at b or before
+        const int mid = (lo + hi) >> 1;
+        if (a.group_start[mid] <= b)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const Group g = group_at(a, lo);
+    return b >= g.b0 && b < g.b1 && (a.causal ? L - n : L) >= g.keys ? g.keys : 0;
+}
+
+// Slot of part c among a row's own (see AttnArgs).
+__device__ __forceinline__ int64_t row_slot(const AttnArgs &a, int64_t t, int hd, int c)
+{
+    return a.row_slot + (t * a.hq + hd) * a.row_parts + a.row_first + c;
+}
+
 __device__ __forceinline__ int clamp_page(int page, int n_pages)
 {
     return min(max(page, 0), n_pages - 1);

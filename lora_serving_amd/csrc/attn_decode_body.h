@@ -38,7 +38,7 @@ __device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b)
     s.q0 = (int)min((int64_t)max(a.cu_q[b], 0), a.T);
     s.n = (int)min((int64_t)max(a.cu_q[b + 1], 0), a.T) - s.q0;
     s.L = (int)min((int64_t)max(a.kv_len[b], 0), min(a.max_kv, a.table_stride << a.cache.ps));
-    s.lo = a.window > 0 ? max(0, s.L - s.n - a.window + 1) : 0;
+    s.lo = KEYS == KEYS_OWN ? shared_keys(a, b, s.n, s.L) : a.window > 0 ? max(0, s.L - s.n - a.window + 1) : 0;
     s.first = KEYS == KEYS_SINKS && a.sinks >= (s.lo & ~31) ? 0 : s.lo / DECODE_UNIT;
     s.sink = KEYS == KEYS_SINKS ? min((a.sinks + DECODE_UNIT - 1) / DECODE_UNIT, s.first) : 0;
     const int64_t rows = (int64_t)s.n * a.group;
@@ -177,7 +177,9 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
     // this workgroup's share: `left` units from unit f of (sequence b, head h) on
     UnitPlace at;
     int left;
-    if (a.part_o == nullptr) {          // one workgroup a sequence and head
+    Shares cut(0, 0);
+    uint32_t u0 = 0;            // the unit f's number among all
+    if (KEYS != KEYS_OWN && a.part_o == nullptr) {          // one workgroup a sequence and head
         at.b = (int)(share / a.hkv);
         at.h = (int)(share - (unsigned)at.b * a.hkv);
         at.f = 0;
@@ -185,10 +187,10 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         left = at.sq.units;
     } else {
         const LaneUnits u = lane_units<KEYS>(a, lane);
-        const Shares cut((uint32_t)u.total * a.hkv, shares);
+        cut = Shares((uint32_t)u.total * a.hkv, shares);
         if (share >= cut.n)
             return;
-        const uint32_t u0 = cut.start(share);
+        u0 = cut.start(share);
         left = (int)(cut.start(share + 1) - u0);
         at = find_unit<KEYS>(a, u, u0);
     }
@@ -303,6 +305,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         const int vk = 4 * g + (col >> 2);
         const uint32_t rlane = vk * D * 2 + 16 * (((col & 3) >> 1) ^ ad_swz<D>(vk)) + 8 * (col & 1);
         auto sees = [&](int key, int pos) {
+            if (KEYS == KEYS_OWN)
+                return key < L && (!a.causal || key <= pos) && key >= sq.lo;
             return key < L && (!a.causal || key <= pos) &&
                    (a.window <= 0 || key > pos - a.window || (KEYS == KEYS_SINKS && key < a.sinks));
         };
@@ -498,7 +502,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
             }
         };
         // steps that hold a key which some query of the sequence does not see: below `free` and from `full` on
-        const int full = L - sq.n + 1 - 32, free = a.window > 0 ? L - a.window : 0;
+        const int full = L - sq.n + 1 - 32, free = KEYS == KEYS_OWN ? sq.lo : a.window > 0 ? L - a.window : 0;
         for (; kb < k1 && kb < free; kb = after(kb))
             step(std::true_type());
         for (; kb < k1 && kb <= full; kb += STEP)
@@ -550,7 +554,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                     }
                 }
                 const int i = row / a.group, hd = head * a.group + row - i * a.group;
-                if (f == 0 && end == sq.units) {
+                const bool whole = f == 0 && end == sq.units;
+                if (whole && (KEYS != KEYS_OWN || sq.lo == 0)) {
                     const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
                     uint16_t *dst = a.out + (sq.q0 + i) * a.out_stride + (int64_t)hd * D + part * VPT;
 #pragma unroll
@@ -563,7 +568,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                         a.lse[(int64_t)(sq.q0 + i) * a.hq + hd] =
                             sum == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
                 } else {
-                    const int64_t slot = part_slot(a, share, f > 0, row);
+                    const int64_t slot = KEYS == KEYS_OWN && whole ? row_slot(a, sq.q0 + i, hd, 0)
+                                                                   : part_slot(a, share, f > 0, row);
                     float *dst = a.part_o + slot * D + part * VPT;
 #pragma unroll
                     for (int e = 0; e < VPT; e += 4)
@@ -573,7 +579,13 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                 }
             }
         }
+        if (KEYS == KEYS_OWN && f == 0 && threadIdx.x == 0) {
+            int32_t *const c = a.cuts + 2 * ((int64_t)b * a.hkv + head);
+            c[0] = end == sq.units ? -1 : (int)share;
+            c[1] = (int)cut.of(u0 + sq.units - 1);
+        }
         // the next head or sequence
+        u0 += end - f;
         left -= end - f;
         if (left <= 0)
             break;

@@ -4,6 +4,7 @@
 // 64 to 2048 and a chunk of 2048 tokens after 6000: 361 to 383 us, one kernel after the other 447; with contexts of 1000
 // and a chunk over 8192 356 to 377 us against 432).
 #include "attn_decode_body.h"
+#include "attn_mixed.h"
 #include "attn_wide_body.h"
 
 namespace mlora {
@@ -22,28 +23,8 @@ __global__ __launch_bounds__(256, 2) void attn_mixed_kernel(AttnArgs w, AttnArgs
     constexpr int SRC = FP8 ? AW_PAGES_E4M3 : AW_PAGES;
     constexpr int LDS = wide_lds<D, SRC, 1> > decode_lds<D, 1> ? wide_lds<D, SRC, 1> : decode_lds<D, 1>;
     __shared__ __attribute__((aligned(16))) uint8_t smem[LDS];
-    // the first 256 of the wide ones, the first 256 of the others, then groups of each in turn.  Workgroups go to the 8
-    // XCDs, and within one to its shader engines and their CUs, in turn: smaller groups would give each kind to some
-    // of them alone (groups of 8: a chunk of 2048 with empty shares between 319 us, groups of 256 232).
-    constexpr uint32_t GROUP = 256;
-    const uint32_t wide = wide_x * w.n_chunks, w0 = min(wide, (uint32_t)CUS), d0 = min(shares, (uint32_t)CUS);
     uint32_t i = blockIdx.x;
-    bool is_wide = i < w0;
-    if (!is_wide) {
-        i -= w0;
-        if (i >= d0) {
-            i -= d0;
-            const uint32_t both = min(wide - w0, shares - d0) & ~(GROUP - 1);
-            if (i < 2 * both) {
-                is_wide = (i / GROUP & 1) == 0;
-                i = i / (2 * GROUP) * GROUP + (i & (GROUP - 1)) + (is_wide ? w0 : d0);
-            } else {
-                i -= 2 * both;
-                is_wide = i < wide - w0 - both;
-                i = is_wide ? i + w0 + both : i - (wide - w0 - both) + d0 + both;
-            }
-        }
-    }
+    const bool is_wide = mixed_place(wide_x * w.n_chunks, shares, &i);
     if (is_wide && MORE)
         attn_wide_pages<D, SRC, KEYS>(w, (int)(i % wide_x), (int)(i / wide_x), (int)wide_x, smem);
     else if (is_wide)

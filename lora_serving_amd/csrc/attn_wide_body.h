@@ -60,13 +60,26 @@ struct WideItem {
 // The sequence and row block of an item: the longest row blocks (the last ones of a causal prompt) first, of
 // all sequences up to 64 of them (they start first, so that the launch ends on short ones: 8 prompts of 2048
 // tokens), in each sequence where there are more (short prompts, or one chunk among many single tokens).
-template <bool ROWS>
+template <bool ROWS, int KEYS>
 __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, WideItem *w)
 {
-    int q0 = 0, q1 = 0, k0 = 0, k1 = 0;
+    int q0 = 0, q1 = 0, k0 = 0, k1 = 0, b0 = 0;
+    const int n_seqs = KEYS == KEYS_SHARED ? a.n_groups : a.n_seqs;
     auto load = [&](int s) {
         q0 = q1 = k0 = k1 = 0;
-        if (s < a.n_seqs) {
+        if (KEYS == KEYS_SHARED) {          // (a group)
+            if (s < n_seqs) {
+                const Group g = group_at(a, s);
+                b0 = g.b0;
+                k1 = g.keys;
+                if (k1 > 0) {
+                    q0 = (int)min((int64_t)max(a.cu_q[g.b0], 0), a.T);
+                    q1 = (int)min((int64_t)max(a.cu_q[g.b1], 0), a.T);
+                }
+            }
+            return q1 > q0 ? (int)(((int64_t)(q1 - q0) * a.group + WIDE_ROWS - 1) / WIDE_ROWS) : 0;
+        }
+        if (s < n_seqs) {
             const int32_t *cu = ROWS && a.cu_k ? a.cu_k : a.cu_q;
             const int32_t qa = a.cu_q[s], qb = a.cu_q[s + 1], ka = ROWS ? cu[s] : 0, kb = ROWS ? cu[s + 1] : a.kv_len[s];
             q0 = (int)min((int64_t)max(qa, 0), a.T);
@@ -79,14 +92,14 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, W
         return mine ? (int)((rows + WIDE_ROWS - 1) / WIDE_ROWS) : 0;
     };
     auto take = [&](int s0, int src, int block) {
-        w->seq = s0 + src;
+        w->seq = KEYS == KEYS_SHARED ? __builtin_amdgcn_readlane(b0, src) : s0 + src;
         w->block = block;
         w->q0 = __builtin_amdgcn_readlane(q0, src);
         w->n = __builtin_amdgcn_readlane(q1, src) - w->q0;
         w->key0 = __builtin_amdgcn_readlane(k0, src);
         w->L = max(__builtin_amdgcn_readlane(k1, src) - w->key0, 0);
     };
-    if (a.n_seqs <= 64) {
+    if (n_seqs <= 64) {
         const int nb = load(lane);
         // items of block numbers >= r
         auto count = [&](int r) { return wave_total(max(nb - r, 0)); };
@@ -109,7 +122,7 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, W
         return true;
     }
     // a lane counts `per` consecutive sequences; then those of the lane that has the item, a lane each
-    const int per = (a.n_seqs + 63) / 64;
+    const int per = (n_seqs + 63) / 64;
     int mine = 0;
 #pragma unroll 4
     for (int i = 0; i < per; ++i)
@@ -166,18 +179,19 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     const int item = (int)((unsigned)bx / a.hkv), h = (int)((unsigned)bx - (unsigned)item * a.hkv);
 
     WideItem it;
-    if (!aw_item<SRC == AW_ROWS>(a, item, lane, &it))
+    if (!aw_item<SRC == AW_ROWS, KEYS>(a, item, lane, &it))
         return it.total;
     const int b = it.seq, rb = it.block, q0 = it.q0, n = it.n, L = it.L, key0 = it.key0;
     const int rows = n * a.group;
+    const int own = KEYS == KEYS_OWN ? shared_keys(a, b, n, L) : 0;     // the first key that is the sequence's own
 
     // this lane's row, and the keys that the workgroup's and the wave's rows see
     const int row = rb * BM + wave * 32 + col;
     const int ri = min(row, rows - 1) / a.group, hd = h * a.group + min(row, rows - 1) - ri * a.group;
     const int pos = L - n + ri;
-    auto first_key = [&](int r) { return a.window > 0 ? max(0, L - n + min(r, rows - 1) / a.group - a.window + 1) : 0; };
-    auto end_key = [&](int r) { return a.causal ? min(L, L - n + min(r, rows - 1) / a.group + 1) : L; };
-    const int c0 = KEYS == KEYS_SINKS ? 0 : by * a.chunk;
+    auto first_key = [&](int r) { return KEYS == KEYS_OWN ? own : a.window > 0 ? max(0, L - n + min(r, rows - 1) / a.group - a.window + 1) : 0; };
+    auto end_key = [&](int r) { return KEYS != KEYS_SHARED && a.causal ? min(L, L - n + min(r, rows - 1) / a.group + 1) : L; };
+    const int c0 = KEYS == KEYS_SINKS ? 0 : (own & ~(BN - 1)) + by * a.chunk;
     const int kmin = max(first_key(rb * BM), c0);
     const int kmax = KEYS == KEYS_SINKS ? end_key(rb * BM + BM - 1)
                                         : (int)min((int64_t)end_key(rb * BM + BM - 1), (int64_t)c0 + a.chunk);
@@ -369,6 +383,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             scaled(t, i >> 2, i & 3, st);
     };
     auto sees = [&](int key) {
+        if (KEYS == KEYS_SHARED || KEYS == KEYS_OWN)
+            return key < L && key >= own && (KEYS == KEYS_SHARED || !a.causal || key <= pos);
         return key < L && (!a.causal || key <= pos) &&
                (a.window <= 0 || key > pos - a.window || (KEYS == KEYS_SINKS && key < a.sinks));
     };
@@ -669,7 +685,7 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
                     o[d][4 * i + e] = o[d][4 * i + e] * s0 + x[e] * s1;
             }
     }
-    if (a.n_chunks == 1) {
+    if (KEYS != KEYS_SHARED && a.n_chunks == 1 && (KEYS != KEYS_OWN || own == 0)) {
         // through the wave's own part of LDS (the tiles are done with), so that whole rows are stored
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
         if (KG == 1)
@@ -696,7 +712,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             a.lse[(int64_t)(q0 + ri) * a.hq + hd] =
                 l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * (1.f / ATTN_LOG2E);
     } else if (row < rows) {
-        const int64_t slot = ((int64_t)(q0 + ri) * a.hq + hd) * a.n_chunks + by;
+        const int64_t slot = KEYS == KEYS_SHARED || KEYS == KEYS_OWN ? row_slot(a, q0 + ri, hd, by)
+                                                                     : ((int64_t)(q0 + ri) * a.hq + hd) * a.n_chunks + by;
 #pragma unroll
         for (int d = 0; d < DB; ++d)
 #pragma unroll

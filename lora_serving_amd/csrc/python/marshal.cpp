@@ -218,36 +218,79 @@ mlora_status attention(PyObject *const *a)
     });
 }
 
+// a paged batch: the cache, its sequences' pages, queries and lengths
+struct Paged {
+    const mlora_cache *cache;
+    const int32_t *pages, *cu_q, *kv_len;
+    int64_t n, width;
+};
+
+Paged paged(PyObject *cache, PyObject *page_table, PyObject *cu_q, PyObject *kv_len, const Rows &q)
+{
+    Paged p{address<mlora_cache>(cache), nullptr, nullptr, nullptr, 0, 0};
+    if (q.d != p.cache->head_dim)
+        fail("q", "must have the head_dim of the cache");
+    p.n = tensor(kv_len, "kv_len").numel();
+    const at::Tensor &table = tensor(page_table, "page_table");
+    if (table.dim() != 2 || table.size(0) != p.n)
+        fail("page_table", "must be [n_seqs][pages]");
+    p.pages = ints(page_table, "page_table", table.numel());
+    p.cu_q = ints(cu_q, "cu_q", p.n + 1);
+    p.kv_len = ints(kv_len, "kv_len", p.n);
+    p.width = table.size(1);
+    return p;
+}
+
+struct Space {
+    void *p;
+    size_t bytes;
+};
+
+Space space(PyObject *o)
+{
+    if (o == Py_None)
+        return {nullptr, 0};
+    const at::Tensor &w = tensor(o, "ws");
+    if (!w.is_contiguous())
+        fail("ws", "must be contiguous");
+    return {w.data_ptr(), w.nbytes()};
+}
+
 // (q, cache, page_table, cu_q, kv_len, out, max_q, max_kv, causal, window, scale, lse, ws, stream, sinks)
 mlora_status paged_attention(PyObject *const *a)
 {
     const Rows q = rows(a[0], "q"), out = rows(a[5], "out", &q);
-    const mlora_cache *c = address<mlora_cache>(a[1]);
-    if (q.d != c->head_dim)
-        fail("q", "must have the head_dim of the cache");
-    const int64_t n = tensor(a[4], "kv_len").numel();
-    const at::Tensor &table = tensor(a[2], "page_table");
-    if (table.dim() != 2 || table.size(0) != n)
-        fail("page_table", "must be [n_seqs][pages]");
-    void *ws = nullptr;
-    size_t ws_bytes = 0;
-    if (a[12] != Py_None) {
-        const at::Tensor &w = tensor(a[12], "ws");
-        if (!w.is_contiguous())
-            fail("ws", "must be contiguous");
-        ws = w.data_ptr();
-        ws_bytes = w.nbytes();
-    }
-    const int32_t *const pages = ints(a[2], "page_table", table.numel()), *const cu_q = ints(a[3], "cu_q", n + 1),
-                  *const kv_len = ints(a[4], "kv_len", n);
-    const int64_t width = table.size(1), max_q = integer(a[6]), max_kv = integer(a[7]);
+    const Paged p = paged(a[1], a[2], a[3], a[4], q);
+    const Space ws = space(a[12]);
+    const int64_t max_q = integer(a[6]), max_kv = integer(a[7]);
     const int32_t causal = truth(a[8]), window = int32(a[9], "window"), sinks = int32(a[14], "sinks");
     const float scale = (float)real(a[10]);
     float *const lse = lse_of(a[11], q.n, q.heads);
     const hipStream_t s = stream(a[13]);
     return unlocked([&] {
-        return mlora_paged_attention_sinks(q.p, q.stride, q.n, (int32_t)q.heads, c, pages, width, (int32_t)n, cu_q, kv_len,
-                                           max_q, max_kv, causal, window, sinks, scale, out.p, out.stride, lse, ws, ws_bytes, s);
+        return mlora_paged_attention_sinks(q.p, q.stride, q.n, (int32_t)q.heads, p.cache, p.pages, p.width, (int32_t)p.n, p.cu_q,
+                                           p.kv_len, max_q, max_kv, causal, window, sinks, scale, out.p, out.stride, lse, ws.p,
+                                           ws.bytes, s);
+    });
+}
+
+// (q, cache, page_table, cu_q, kv_len, group_start, prefix_len, out, max_q, max_kv, max_prefix, causal, scale, lse, ws, stream)
+mlora_status prefix_attention(PyObject *const *a)
+{
+    const Rows q = rows(a[0], "q"), out = rows(a[7], "out", &q);
+    const Paged p = paged(a[1], a[2], a[3], a[4], q);
+    const int64_t groups = tensor(a[6], "prefix_len").numel();
+    const int32_t *const start = ints(a[5], "group_start", groups + 1), *const prefix = ints(a[6], "prefix_len", groups);
+    const int64_t max_q = integer(a[8]), max_kv = integer(a[9]), max_prefix = integer(a[10]);
+    const int32_t causal = truth(a[11]);
+    const float scale = (float)real(a[12]);
+    float *const lse = lse_of(a[13], q.n, q.heads);
+    const Space ws = space(a[14]);
+    const hipStream_t s = stream(a[15]);
+    return unlocked([&] {
+        return mlora_prefix_attention(q.p, q.stride, q.n, (int32_t)q.heads, p.cache, p.pages, p.width, (int32_t)p.n, p.cu_q, p.kv_len,
+                                      (int32_t)groups, start, prefix, max_q, max_kv, max_prefix, causal, scale, out.p, out.stride,
+                                      lse, ws.p, ws.bytes, s);
     });
 }
 
@@ -270,7 +313,7 @@ PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 
 #define METHOD(name, f, n) {name, (PyCFunction)(void (*)(void))entry<f, n>, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {METHOD("qk_rope", qk_rope, 14), METHOD("cache_read", cache_read, 5), METHOD("attention", attention, 13),
-                         METHOD("paged_attention", paged_attention, 15), {nullptr, nullptr, 0, nullptr}};
+                         METHOD("paged_attention", paged_attention, 15), METHOD("prefix_attention", prefix_attention, 16), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

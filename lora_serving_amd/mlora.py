@@ -49,7 +49,9 @@ EXPORTS = ("mlora_status_string", "mlora_last_error", "mlora_factor", "mlora_slo
            "mlora_linear_path", "mlora_linear_noalloc", "mlora_rope_turns", "mlora_cache_bytes",
            "mlora_qk_rope", "mlora_cache_read", "mlora_attention", "mlora_paged_workspace_size",
            "mlora_paged_attention", "mlora_validate_pages", "mlora_attention_sinks",
-           "mlora_paged_attention_sinks", "mlora_validate_pages_sinks", "mlora_trace_start",
+           "mlora_paged_attention_sinks", "mlora_validate_pages_sinks",
+           "mlora_prefix_workspace_size", "mlora_prefix_attention", "mlora_validate_prefixes",
+           "mlora_trace_start",
            "mlora_trace_stop")
 
 _P = ctypes.c_void_p
@@ -144,6 +146,15 @@ _lib.mlora_paged_attention_sinks.argtypes = [_P, _i64, _i64, _i32, _CACHE_P, _P,
 _lib.mlora_validate_pages_sinks.restype = ctypes.c_int
 _lib.mlora_validate_pages_sinks.argtypes = [_CACHE_P, _P, _i64, _i32, _P, _P, _i64, _i64, _i64, _i32,
                                             _i32, ctypes.POINTER(_i64)]
+_lib.mlora_prefix_workspace_size.restype = ctypes.c_size_t
+_lib.mlora_prefix_workspace_size.argtypes = [_i64, _i32, _i32, _i32, _i32, _i32, _i64, _i64, _i64]
+_lib.mlora_prefix_attention.restype = ctypes.c_int
+_lib.mlora_prefix_attention.argtypes = [_P, _i64, _i64, _i32, _CACHE_P, _P, _i64, _i32, _P, _P, _i32,
+                                        _P, _P, _i64, _i64, _i64, _i32, _f32, _P, _i64, _P, _P,
+                                        ctypes.c_size_t, _P]
+_lib.mlora_validate_prefixes.restype = ctypes.c_int
+_lib.mlora_validate_prefixes.argtypes = [_CACHE_P, _i64, _i32, _P, _i32, _P, _P, _i64,
+                                         ctypes.POINTER(_i64)]
 _lib.mlora_trace_start.restype = ctypes.c_int
 _lib.mlora_trace_start.argtypes = [_i32]
 _lib.mlora_trace_stop.restype = _i32
@@ -552,6 +563,58 @@ def mlora_validate_pages(cache: Cache, page_table, cu_q, kv_len, T: int, max_q: 
                                            lens.size, cu.ctypes.data_as(_P),
                                            lens.ctypes.data_as(_P), T, max_q, max_kv, window,
                                            sinks, ctypes.byref(bad))
+    return code, int(bad.value)
+
+
+def mlora_prefix_workspace_size(T: int, n_seqs: int, n_groups: int, n_q_heads: int,
+                                n_kv_heads: int, head_dim: int, max_q: int, max_kv: int,
+                                max_prefix: int) -> int:
+    return int(_lib.mlora_prefix_workspace_size(T, n_seqs, n_groups, n_q_heads, n_kv_heads,
+                                                head_dim, max_q, max_kv, max_prefix))
+
+
+def prefix_workspace(T: int, n_seqs: int, n_groups: int, n_q_heads: int, n_kv_heads: int,
+                     head_dim: int, max_q: int, max_kv: int, max_prefix: int, device="cuda"):
+    """A workspace of mlora_prefix_workspace_size() bytes, for calls of these sizes and of smaller
+    ones."""
+    import torch
+    n = mlora_prefix_workspace_size(T, n_seqs, n_groups, n_q_heads, n_kv_heads, head_dim, max_q,
+                                    max_kv, max_prefix)
+    if n == 0:
+        raise MloraError(MLORA_ERR_ARG, "mlora_prefix_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def mlora_prefix_attention(q, cache: Cache, page_table, cu_q, kv_len, group_start, prefix_len, out,
+                           max_q: int, max_kv: int, max_prefix: int, causal: bool = True,
+                           scale: float = 0.0, lse=None, ws=None, stream=None):
+    """mlora_paged_attention of sequences that share first tokens: those of a group, sequences
+    [group_start[g], group_start[g + 1]), their first prefix_len[g].  group_start int32
+    [n_groups + 1], prefix_len int32 [n_groups], device; the rest as mlora_paged_attention."""
+    code = _calls.prefix_attention(q, cache.address, page_table, cu_q, kv_len, group_start,
+                                   prefix_len, out, max_q, max_kv, max_prefix, causal, scale, lse,
+                                   ws, _stream(stream))
+    if code:
+        _check(code, "mlora_prefix_attention")
+
+
+def mlora_validate_prefixes(cache: Cache, page_table, kv_len, group_start, prefix_len,
+                            max_prefix: int):
+    """Host check of a batch's groups (host int32 tensors or arrays); returns (status, offending
+    value)."""
+    import numpy as np
+    table = np.asarray(page_table)
+    lens = np.ascontiguousarray(kv_len, dtype=np.int32)
+    start = np.ascontiguousarray(group_start, dtype=np.int32)
+    prefix = np.ascontiguousarray(prefix_len, dtype=np.int32)
+    if table.ndim != 2 or table.shape[0] != lens.size or start.size != prefix.size + 1:
+        raise ValueError("page_table [n_seqs][pages] and kv_len [n_seqs], or group_start "
+                         "[n_groups + 1] and prefix_len [n_groups], do not agree")
+    bad = _i64(0)
+    code = _lib.mlora_validate_prefixes(cache.ref, table.shape[1], lens.size,
+                                        lens.ctypes.data_as(_P), prefix.size,
+                                        start.ctypes.data_as(_P), prefix.ctypes.data_as(_P),
+                                        max_prefix, ctypes.byref(bad))
     return code, int(bad.value)
 
 
