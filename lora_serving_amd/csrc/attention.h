@@ -60,8 +60,9 @@ struct AttnArgs {
     // [row_parts]), this launch's from number row_first on; cuts: where the decode kernel left a sequence and head.
     const int32_t *group_start, *prefix_len;
     int32_t n_groups, row_first, row_parts;
+    int32_t alone_rows;            // sequences of more rows share nothing
     int64_t max_prefix, row_slot;
-    int32_t *cuts;                 // [n_seqs][hkv][2]: -1 (a slot of the row), or the first and last share
+    int32_t *cuts;                 // [n_seqs][hkv][4]: first share (-1: a slot of the row), last share, shared keys
 };
 // Which keys a kernel's queries see, besides the causal limit: all or a window of them; a window and the first ones;
 // those that a group's sequences share (the group's rows are one sequence's); a sequence's others.
@@ -90,6 +91,7 @@ hipError_t launch_attn_wide_combine(const AttnArgs &a, int head_dim, hipStream_t
 // Sequences of up to 16 * nq rows (nq 1 or 2) over pages, their keys cut into `shares` equal shares, or (part_o ==
 // nullptr) one workgroup a sequence and kv head, then shares = n_seqs * hkv.
 constexpr int DECODE_UNIT = 128;  // keys: the unit that shares are made of
+constexpr int OWN_UNIT = 32;      // of KEYS_OWN, whose shares are a wave's
 // Workgroups that a CU holds at a time.
 constexpr int decode_slots(int head_dim, int nq) { return head_dim == 64 && nq == 1 ? 3 : 2; }
 hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream);

@@ -71,6 +71,12 @@ bool paged_sizes_ok(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int64_t 
            (int64_t)n_seqs * hkv * (max_kv / DECODE_UNIT + 1) < MAX_ROWS;
 }
 
+// And of a call over shared prefixes, whose shares are made of smaller units.
+bool prefix_sizes_ok(int32_t n_seqs, int32_t hkv, int64_t max_kv, int64_t max_prefix)
+{
+    return max_prefix < MAX_KEYS && (int64_t)n_seqs * hkv * (max_kv / OWN_UNIT + 1) < MAX_ROWS;
+}
+
 bool rows_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
 
 // A window that no sequence is longer than hides nothing (and is left out, so that positions minus the window
@@ -192,13 +198,33 @@ size_t paged_room(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d,
     return dec + wide;
 }
 
-// How a call over shared prefixes is cut: the decode and wide parts as in paged_plan (always with parts, for the join
-// takes a row's own keys as one of them), and the shared keys in chunks that give the groups' row blocks
-// SHARED_WANT workgroups, of SHARED_LEAST keys or more.
-constexpr int64_t SHARED_WANT = 512, SHARED_LEAST = 256;
-int64_t shared_cuts(int64_t items, int64_t max_prefix)
+// How a call over shared prefixes is cut: the kernels as in paged_plan, but always with parts, for the join takes a row's own
+// keys as one of them; a sequence of more than ALONE_ROWS rows shares nothing (it reads the prefix for rows enough, and
+// answers them without parts).
+constexpr int32_t ALONE_ROWS = 256;
+
+// Chunks of keys for `items` row blocks of `keys` keys at the most, up to `limit`, in us: a tile takes 1.2 in a workgroup alone
+// on its CU and 1.95 in two, in rounds of 512, and a part of 128 rows 0.04 to write and to read again.
+int64_t prefix_cuts(int64_t items, int64_t keys, int64_t limit)
 {
-    return std::max<int64_t>(1, std::min((SHARED_WANT + items - 1) / items, (max_prefix + SHARED_LEAST - 1) / SHARED_LEAST));
+    const int64_t tiles = (keys + 63) / 64;
+    int64_t best = 1;
+    double least = 0.;
+    for (int64_t n = 1; n <= limit && (n == 1 || n * items <= 8 * CUS); ++n) {
+        const int64_t groups = items * n, each = (tiles + n - 1) / n;
+        const double us = (groups <= CUS ? 1.2 * each : 1.95 * each * ((groups + 2 * CUS - 1) / (2 * CUS))) + 0.04 * groups;
+        if (n == 1 || us < least) {
+            best = n;
+            least = us;
+        }
+    }
+    return best;
+}
+
+// The limit of the cuts of a batch of these row blocks: every row has room for a part of each.
+int64_t most_prefix_cuts(int64_t items, int64_t keys)
+{
+    return std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(64, 8 * CUS / items), (keys + 63) / 64 / 2));
 }
 
 struct PrefixPlan {
@@ -209,19 +235,38 @@ struct PrefixPlan {
     size_t total() const { return o + ml + cuts; }
 };
 
-size_t cut_bytes(int64_t n_seqs, int32_t hkv) { return align_up((size_t)n_seqs * hkv * 8); }
+size_t cut_bytes(int64_t n_seqs, int32_t hkv) { return align_up((size_t)n_seqs * hkv * 16); }
+
+// Workgroups of the decode kernel, of four shares each.
+int64_t own_workgroups(int32_t n_seqs, int32_t hkv, int64_t max_kv)
+{
+    const int64_t units = (std::max<int64_t>(max_kv, 1) + OWN_UNIT - 1) / OWN_UNIT;
+    return std::min(((int64_t)n_seqs * hkv * units + 3) / 4, 2 * CUS);
+}
 
 PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv,
                        int64_t max_prefix)
 {
     PrefixPlan p;
     p.own = paged_plan(T, n_seqs, hq, hkv, d, max_q, max_kv, 0, 0);
-    const int64_t units = (std::max<int64_t>(max_kv, 1) + DECODE_UNIT - 1) / DECODE_UNIT;
-    p.own.shares = p.own.dec_rows > 0 ? (int)std::min((int64_t)n_seqs * hkv * units, 2 * CUS) : 0;
-    p.share_slots = 2 * (int64_t)p.own.shares * p.own.dec_rows;
-    const int64_t n = shared_cuts((T * (hq / hkv) + WIDE_ROWS - 1) / WIDE_ROWS * hkv, max_prefix);
+    // The rows of sequences that share nothing, if those of more than one token are alike, and the others'.
+    const int64_t group = hq / hkv, all = T * group, items = (all + WIDE_ROWS - 1) / WIDE_ROWS * hkv;
+    const int64_t alone = max_q * group > ALONE_ROWS ? std::min(T, std::max<int64_t>(T - n_seqs, 0) / std::max<int64_t>(max_q - 1, 1) * max_q) * group : 0;
+    const auto blocks = [&](int64_t rows) { return std::max<int64_t>(1, (rows + WIDE_ROWS - 1) / WIDE_ROWS) * hkv; };
+    const int64_t shared = blocks(all - alone);
+    int64_t n = prefix_cuts(shared, max_prefix, most_prefix_cuts(items, max_prefix));
     p.chunk = ((max_prefix + n - 1) / n + 63) & ~INT64_C(63);
     p.chunks = (max_prefix + p.chunk - 1) / p.chunk;
+    // the card holds 512 workgroups: those of the shares start beside the others' (one of each on a CU at the most)
+    const int64_t beside = std::min(shared * p.chunks, CUS);
+    p.own.shares = p.own.dec_rows > 0 ? (int)std::min(own_workgroups(n_seqs, hkv, max_kv), 2 * CUS - beside) : 0;
+    p.share_slots = 2 * 4 * (int64_t)p.own.shares * p.own.dec_rows;
+    if (p.own.wide) {
+        const int64_t keys = std::max<int64_t>(max_kv, 1);
+        n = prefix_cuts(blocks(alone > 0 ? alone : all), keys, most_prefix_cuts(items, keys));
+        p.own.wide_chunk = ((keys + n - 1) / n + 127) & ~INT64_C(127);
+        p.own.wide_chunks = (keys + p.own.wide_chunk - 1) / p.own.wide_chunk;
+    }
     p.row_parts = p.chunks + std::max<int64_t>(p.own.wide_chunks, 1);
     const size_t slots = (size_t)p.share_slots + (size_t)T * hq * p.row_parts;
     p.o = align_up(slots * d * 4);
@@ -234,12 +279,12 @@ PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32
 size_t prefix_room(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv,
                    int64_t max_prefix)
 {
-    const int64_t group = hq / hkv, most = max_q * group, units = (std::max<int64_t>(max_kv, 1) + DECODE_UNIT - 1) / DECODE_UNIT;
-    const size_t shares = 2 * (size_t)std::min((int64_t)n_seqs * hkv * units, 2 * CUS) * std::min<int64_t>(most, 32);
+    const int64_t group = hq / hkv, most = max_q * group;
+    const size_t shares = 8 * (size_t)own_workgroups(n_seqs, hkv, max_kv) * std::min<int64_t>(most, 32);
     size_t rows = (size_t)T * hq * 2;
-    for (int64_t r = 1; r * hkv < SHARED_WANT && (r - 1) * WIDE_ROWS < T * group; ++r) {
-        const int64_t wide = most > 32 && r * hkv < WIDE_WHOLE ? wide_cuts(r * hkv, std::max<int64_t>(max_kv, 1)) : 1;
-        rows = std::max(rows, (size_t)std::min(T, r * WIDE_ROWS / group) * hq * (shared_cuts(r * hkv, max_prefix) + wide));
+    for (int64_t r = 1; r * hkv <= 8 * CUS && (r - 1) * WIDE_ROWS < T * group; ++r) {
+        const int64_t wide = most > 32 ? most_prefix_cuts(r * hkv, std::max<int64_t>(max_kv, 1)) : 1;
+        rows = std::max(rows, (size_t)std::min(T, r * WIDE_ROWS / group) * hq * (most_prefix_cuts(r * hkv, max_prefix) + wide));
     }
     return align_up((shares + rows) * d * 4) + align_up((shares + rows) * 8) + cut_bytes(n_seqs, hkv);
 }
@@ -628,9 +673,11 @@ mlora_status mlora_paged_attention_sinks(const void *q, int64_t q_stride, int64_
 size_t mlora_prefix_workspace_size(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t n_q_heads, int32_t n_kv_heads,
                                    int32_t head_dim, int64_t max_q, int64_t max_kv, int64_t max_prefix)
 {
-    if (n_groups < 0 || max_prefix < 0 || max_prefix >= MAX_KEYS)
+    if (n_groups < 0 || max_prefix < 0)
         return 0;
     const size_t paged = mlora_paged_workspace_size(T, n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_kv);
+    if (paged > 0 && !prefix_sizes_ok(n_seqs, n_kv_heads, max_kv, max_prefix))
+        return 0;
     if (paged == 0 || n_groups == 0 || max_prefix == 0)
         return paged;
     return std::max(paged, prefix_room(T, n_seqs, n_q_heads, n_kv_heads, head_dim, std::min(max_q, T), max_kv, max_prefix) + 256);
@@ -645,13 +692,15 @@ mlora_status mlora_prefix_attention(const void *q, int64_t q_stride, int64_t T, 
 {
     if (n_groups < 0 || max_prefix < 0)
         return MLORA_ERR_ARG;
-    if (max_prefix >= MAX_KEYS)
-        return MLORA_ERR_UNSUPPORTED;
     PagedCall c;
     const mlora_status st = paged_call(&c, q, q_stride, T, n_q_heads, cache, page_table, table_stride, n_seqs, cu_q, kv_len,
                                        max_q, max_kv, causal, 0, 0, scale, out, out_stride, lse);
-    if (st != MLORA_OK || c.nothing)
+    if (st != MLORA_OK)
         return st;
+    if (!prefix_sizes_ok(n_seqs, c.a.hkv, max_kv, max_prefix))
+        return MLORA_ERR_UNSUPPORTED;
+    if (c.nothing)
+        return MLORA_OK;
     if (n_groups > 0 && (group_start == nullptr || prefix_len == nullptr))
         return MLORA_ERR_ARG;
     max_prefix = std::min(max_prefix, max_kv);
@@ -676,6 +725,7 @@ mlora_status mlora_prefix_attention(const void *q, int64_t q_stride, int64_t T, 
     d.row_parts = (int32_t)p.row_parts;
     d.row_first = (int32_t)p.chunks;
     d.cuts = (int32_t *)(base + p.o + p.ml);
+    d.alone_rows = ALONE_ROWS;
     AttnArgs w = d;                     // the wide ones'
     w.min_rows = d.max_rows + 1;
     w.max_rows = 0x7fffffff;
@@ -686,6 +736,7 @@ mlora_status mlora_prefix_attention(const void *q, int64_t q_stride, int64_t T, 
     s.chunk = (int32_t)p.chunk;
     s.n_chunks = (int32_t)p.chunks;
     s.row_first = 0;
+    s.max_rows = (int32_t)std::min<int64_t>(a.max_q * a.group, 0x7fffffff);
     trace_mark(stream, true);
     hipError_t e = launch_attn_prefix(s, w, d, c.d, p.own.wide, p.own.nq, p.own.shares, stream);
     if (e == hipSuccess)

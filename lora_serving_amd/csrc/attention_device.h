@@ -172,7 +172,7 @@ __device__ __forceinline__ int shared_keys(const AttnArgs &a, int b, int n, int 
             hi = mid;
     }
     const Group g = group_at(a, lo);
-    return b >= g.b0 && b < g.b1 && (a.causal ? L - n : L) >= g.keys ? g.keys : 0;
+    return b >= g.b0 && b < g.b1 && (a.causal ? L - n : L) >= g.keys && (int64_t)n * a.group <= a.alone_rows ? g.keys : 0;
 }
 
 // Slot of part c among a row's own (see AttnArgs).

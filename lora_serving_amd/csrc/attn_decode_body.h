@@ -31,19 +31,22 @@ struct SeqUnits {
     int q0, n, L, lo, first, units, sink;
 };
 
+template <int KEYS> constexpr int unit_keys = KEYS == KEYS_OWN ? OWN_UNIT : DECODE_UNIT;
+
 template <int KEYS>
 __device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b)
 {
+    constexpr int UNIT = unit_keys<KEYS>;
     SeqUnits s;
     s.q0 = (int)min((int64_t)max(a.cu_q[b], 0), a.T);
     s.n = (int)min((int64_t)max(a.cu_q[b + 1], 0), a.T) - s.q0;
     s.L = (int)min((int64_t)max(a.kv_len[b], 0), min(a.max_kv, a.table_stride << a.cache.ps));
     s.lo = KEYS == KEYS_OWN ? shared_keys(a, b, s.n, s.L) : a.window > 0 ? max(0, s.L - s.n - a.window + 1) : 0;
-    s.first = KEYS == KEYS_SINKS && a.sinks >= (s.lo & ~31) ? 0 : s.lo / DECODE_UNIT;
-    s.sink = KEYS == KEYS_SINKS ? min((a.sinks + DECODE_UNIT - 1) / DECODE_UNIT, s.first) : 0;
+    s.first = KEYS == KEYS_SINKS && a.sinks >= (s.lo & ~31) ? 0 : s.lo / UNIT;
+    s.sink = KEYS == KEYS_SINKS ? min((a.sinks + UNIT - 1) / UNIT, s.first) : 0;
     const int64_t rows = (int64_t)s.n * a.group;
     const bool mine = s.n > 0 && s.n <= a.max_q && rows >= a.min_rows && rows <= a.max_rows;
-    s.units = mine ? max(1, (s.L + DECODE_UNIT - 1) / DECODE_UNIT - s.first + s.sink) : 0;
+    s.units = mine ? max(1, (s.L + UNIT - 1) / UNIT - s.first + s.sink) : 0;
     return s;
 }
 
@@ -147,11 +150,17 @@ __device__ __forceinline__ int ad_swz(int key)
     return D == 128 ? (key & 7) << 1 | ((key >> 3) & 1) : ((key >> 1) & 3) << 1 | ((key >> 3) & 1);
 }
 
-template <int D, int NQ>
-constexpr int decode_lds = 4 * 2 * (32 * D > 32 * (D + 4) ? 32 * D : 32 * (D + 4)) + 4 * 16 * 2 * 4 +
-                           (NQ > 1 ? 16 * NQ * D * 2 : 0);
+// (KEYS_OWN: V and Q of each wave; else V, the waves' parts and Q)
+template <int D, int NQ, int KEYS = KEYS_PLAIN>
+constexpr int decode_lds = KEYS == KEYS_OWN ? 4 * 2 * 32 * D + (NQ > 1 ? 4 * 16 * NQ * D * 2 : 0)
+                                            : 4 * 2 * (32 * D > 32 * (D + 4) ? 32 * D : 32 * (D + 4)) + 4 * 16 * 2 * 4 +
+                                                  (NQ > 1 ? 16 * NQ * D * 2 : 0);
 
 // Share `share` of `shares` (or sequence and head `share`, see launch_attn_decode); smem: decode_lds bytes.
+// KEYS_OWN: shares are not a workgroup's but a wave's (of `share` this one has number 4 share + wave, of 4 shares), and a
+// wave leaves its parts to the join by itself: no barrier, so that the start of one wave's sequence, a chain of loads,
+// hides behind the others' keys.  What comes after a shared prefix is short, and a workgroup's waves, starting each together,
+// waited for it together (256 of an e4m3 cache behind four prefixes, 1 to 700 keys each: @OWN@).
 template <int D, int NQ, bool FP8, int KEYS = KEYS_PLAIN>
 __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t share, uint32_t shares, uint8_t *smem)
 {
@@ -162,14 +171,19 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
     constexpr int PARTS = NQ == 1 ? 2 : 1;      // bf16 parts of a probability
     constexpr int OS = D + 4;           // row stride of the joined accumulators in LDS
     constexpr int VW = 32 * D;          // a wave's V rows in LDS
-    constexpr int NW = 4, STEP = 32 * NW;       // waves; keys they take at a time
-    static_assert(STEP == DECODE_UNIT, "units are whole steps");
-    constexpr int PW = VW > 32 * OS ? VW : 32 * OS;     // a wave's V rows or, for the join, accumulators
+    constexpr bool OWN = KEYS == KEYS_OWN;
+    constexpr int NW = 4, STEP = OWN ? 32 : 32 * NW;    // waves; keys they take at a time
+    constexpr int UNIT = unit_keys<KEYS>;
+    static_assert(STEP == UNIT, "units are whole steps");
+    constexpr int PW = OWN || VW > 32 * OS ? VW : 32 * OS;      // a wave's V rows or, for the join, accumulators
     uint16_t *const lds = (uint16_t *)smem;
     float (*const ml)[16][2] = (float (*)[16][2])(smem + NW * PW * 2);
-    uint16_t *const ql = (uint16_t *)(smem + NW * PW * 2 + NW * 16 * 2 * 4);        // two column tiles: Q
+    const int wave = uniform(threadIdx.x >> 6), w32 = OWN ? 0 : 32 * wave;
+    // two column tiles: Q
+    uint16_t *const ql = (uint16_t *)(smem + NW * PW * 2 + (OWN ? wave * 16 * NQ * D * 2 : NW * 16 * 2 * 4));
+    if (OWN)
+        share = 4 * share + wave;
 
-    const int wave = uniform(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int ps = a.cache.ps, pm = (1 << ps) - 1;
     uint16_t *vl = lds + wave * VW;
@@ -179,7 +193,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
     int left;
     Shares cut(0, 0);
     uint32_t u0 = 0;            // the unit f's number among all
-    if (KEYS != KEYS_OWN && a.part_o == nullptr) {          // one workgroup a sequence and head
+    if (!OWN && a.part_o == nullptr) {          // one workgroup a sequence and head
         at.b = (int)(share / a.hkv);
         at.h = (int)(share - (unsigned)at.b * a.hkv);
         at.f = 0;
@@ -187,7 +201,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         left = at.sq.units;
     } else {
         const LaneUnits u = lane_units<KEYS>(a, lane);
-        cut = Shares((uint32_t)u.total * a.hkv, shares);
+        cut = Shares((uint32_t)u.total * a.hkv, OWN ? 4 * shares : shares);
         if (share >= cut.n)
             return;
         u0 = cut.start(share);
@@ -205,16 +219,16 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         int k0, k1, s1 = 0;         // keys [k0, k1); KEYS_SINKS: and those from unit f to s1 before them
         if (KEYS == KEYS_SINKS) {
             // (first keys that reach into the unit `first`: from its start on)
-            const int unit = max(sq.first, sq.first + f - sq.sink) * DECODE_UNIT;
-            k0 = max(unit, a.sinks > sq.first * DECODE_UNIT ? 0 : sq.lo & ~31);
-            k1 = min(L, (sq.first + end - sq.sink) * DECODE_UNIT);
+            const int unit = max(sq.first, sq.first + f - sq.sink) * UNIT;
+            k0 = max(unit, a.sinks > sq.first * UNIT ? 0 : sq.lo & ~31);
+            k1 = min(L, (sq.first + end - sq.sink) * UNIT);
             if (f < sq.sink)
-                s1 = min(min(end, sq.sink) * DECODE_UNIT, a.sinks);
+                s1 = min(min(end, sq.sink) * UNIT, a.sinks);
             if (end <= sq.sink)
                 k0 = k1 = s1;
         } else {
-            k0 = max((sq.first + f) * DECODE_UNIT, sq.lo & ~31);
-            k1 = min(L, (sq.first + end) * DECODE_UNIT);
+            k0 = max((sq.first + f) * UNIT, sq.lo & ~31);
+            k1 = min(L, (sq.first + end) * UNIT);
         }
         const int32_t *__restrict__ table = a.table + (int64_t)b * a.table_stride;
 
@@ -248,10 +262,10 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
             }
         };
         // this wave's next step
-        auto after = [&](int kb) { return KEYS == KEYS_SINKS && kb < s1 && kb + STEP >= s1 ? k0 + 32 * wave : kb + STEP; };
-        int kb = k0 + 32 * wave;
-        if (KEYS == KEYS_SINKS && f * DECODE_UNIT + 32 * wave < s1)
-            kb = f * DECODE_UNIT + 32 * wave;
+        auto after = [&](int kb) { return KEYS == KEYS_SINKS && kb < s1 && kb + STEP >= s1 ? k0 + w32 : kb + STEP; };
+        int kb = k0 + w32;
+        if (KEYS == KEYS_SINKS && f * UNIT + w32 < s1)
+            kb = f * UNIT + w32;
         if (kb < k1) {
             lookup(kb);
             load(kb);
@@ -274,14 +288,14 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
                     qf[NQ == 1 ? s : 0] = *(const u32x4 *)(qr + 8 * qpiece(s));
-            } else if (wave == j) {
+            } else if (OWN || wave == j) {
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
                     *(u32x4 *)(ql + (16 * j + col) * D + 8 * (qpiece(s) ^ (col & (D / 8 - 1)))) =
                         *(const u32x4 *)(qr + 8 * qpiece(s));
             }
         }
-        if (NQ > 1)
+        if (NQ > 1 && !OWN)
             __syncthreads();
         const uint32_t qlane = col * D * 2 + 16 * (qpiece(0) ^ (col & (D / 8 - 1)));
         auto qfrag = [&](uint32_t at, int j, int s) {       // (piece s is piece 0 with bits of s changed)
@@ -305,7 +319,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         const int vk = 4 * g + (col >> 2);
         const uint32_t rlane = vk * D * 2 + 16 * (((col & 3) >> 1) ^ ad_swz<D>(vk)) + 8 * (col & 1);
         auto sees = [&](int key, int pos) {
-            if (KEYS == KEYS_OWN)
+            if (OWN)
                 return key < L && (!a.causal || key <= pos) && key >= sq.lo;
             return key < L && (!a.causal || key <= pos) &&
                    (a.window <= 0 || key > pos - a.window || (KEYS == KEYS_SINKS && key < a.sinks));
@@ -502,7 +516,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
             }
         };
         // steps that hold a key which some query of the sequence does not see: below `free` and from `full` on
-        const int full = L - sq.n + 1 - 32, free = KEYS == KEYS_OWN ? sq.lo : a.window > 0 ? L - a.window : 0;
+        const int full = L - sq.n + 1 - 32, free = OWN ? sq.lo : a.window > 0 ? L - a.window : 0;
         for (; kb < k1 && kb < free; kb = after(kb))
             step(std::true_type());
         for (; kb < k1 && kb <= full; kb += STEP)
@@ -510,10 +524,44 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         for (; kb < k1; kb += STEP)
             step(std::true_type());
 
+        const bool whole = f == 0 && end == sq.units;
+        if (OWN) {
+#pragma unroll
+            for (int j = 0; j < NQ; ++j) {
+                float sum = l[j] + __shfl_xor(l[j], 16, 64);
+                sum += __shfl_xor(sum, 32, 64);
+                const int row = 16 * j + col;
+                if (row >= rows)
+                    continue;
+                const int i = row / a.group, hd = head * a.group + row - i * a.group;
+                if (whole && sq.lo == 0) {
+                    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+                    uint16_t *dst = a.out + (sq.q0 + i) * a.out_stride + (int64_t)hd * D + 4 * g;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+                        *(u32x2 *)(dst + 16 * d) = u32x2{cvt_bf16x2(o[j][d][0] * inv, o[j][d][1] * inv),
+                                                         cvt_bf16x2(o[j][d][2] * inv, o[j][d][3] * inv)};
+                    if (a.lse && g == 0)
+                        a.lse[(int64_t)(sq.q0 + i) * a.hq + hd] =
+                            sum == 0.f ? -INFINITY : (m[j] + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
+                } else {
+                    const int64_t slot = whole ? row_slot(a, sq.q0 + i, hd, 0) : part_slot(a, share, f > 0, row);
+                    float *dst = a.part_o + slot * D + 4 * g;
+#pragma unroll
+                    for (int d = 0; d < DB; ++d)
+                        *(f32x4 *)(dst + 16 * d) = o[j][d];
+                    if (g == 0)
+                        *(f32x2 *)(a.part_ml + 2 * slot) = f32x2{m[j], sum};
+                }
+            }
+            if (f == 0 && lane == 0)
+                *(u32x4 *)(a.cuts + 4 * ((int64_t)b * a.hkv + head)) =
+                    u32x4{whole ? ~0u : share, (uint32_t)cut.of(u0 + sq.units - 1), (uint32_t)sq.lo, 0};
+        }
         // join the waves, 16 rows at a time
         float *of = (float *)lds;
 #pragma unroll
-        for (int j = 0; j < NQ; ++j) {
+        for (int j = 0; j < (OWN ? 0 : NQ); ++j) {
             if (j > 0 && 16 * j >= rows)
                 break;
             float lj = l[j] + __shfl_xor(l[j], 16, 64);
@@ -554,8 +602,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                     }
                 }
                 const int i = row / a.group, hd = head * a.group + row - i * a.group;
-                const bool whole = f == 0 && end == sq.units;
-                if (whole && (KEYS != KEYS_OWN || sq.lo == 0)) {
+                if (whole) {
                     const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
                     uint16_t *dst = a.out + (sq.q0 + i) * a.out_stride + (int64_t)hd * D + part * VPT;
 #pragma unroll
@@ -568,8 +615,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                         a.lse[(int64_t)(sq.q0 + i) * a.hq + hd] =
                             sum == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
                 } else {
-                    const int64_t slot = KEYS == KEYS_OWN && whole ? row_slot(a, sq.q0 + i, hd, 0)
-                                                                   : part_slot(a, share, f > 0, row);
+                    const int64_t slot = part_slot(a, share, f > 0, row);
                     float *dst = a.part_o + slot * D + part * VPT;
 #pragma unroll
                     for (int e = 0; e < VPT; e += 4)
@@ -578,11 +624,6 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                         *(f32x2 *)(a.part_ml + 2 * slot) = f32x2{mx, sum};
                 }
             }
-        }
-        if (KEYS == KEYS_OWN && f == 0 && threadIdx.x == 0) {
-            int32_t *const c = a.cuts + 2 * ((int64_t)b * a.hkv + head);
-            c[0] = end == sq.units ? -1 : (int)share;
-            c[1] = (int)cut.of(u0 + sq.units - 1);
         }
         // the next head or sequence
         u0 += end - f;
@@ -596,7 +637,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                 sq = seq_units<KEYS>(a, ++b);
             while (sq.units == 0);
         }
-        __syncthreads();
+        if (!OWN)
+            __syncthreads();
     }
 }
 

@@ -16,65 +16,135 @@ __global__ __launch_bounds__(256, 2) void attn_prefix_kernel(AttnArgs s, AttnArg
                                                              uint32_t wide_x, uint32_t shares)
 {
     constexpr int SRC = FP8 ? AW_PAGES_E4M3 : AW_PAGES;
-    constexpr int LDS = wide_lds<D, SRC, 1> > decode_lds<D, NQ> ? wide_lds<D, SRC, 1> : decode_lds<D, NQ>;
+    constexpr int LDS_D = decode_lds<D, NQ, KEYS_OWN>, LDS = wide_lds<D, SRC, 1> > LDS_D ? wide_lds<D, SRC, 1> : LDS_D;
     __shared__ __attribute__((aligned(16))) uint8_t smem[LDS];
     uint32_t i = blockIdx.x;
     const uint32_t shared = shared_x * s.n_chunks;
     if (!mixed_place(shared + (WIDE ? wide_x * w.n_chunks : 0), shares, &i)) {
         attn_decode_body<D, NQ, FP8, KEYS_OWN>(d, i, shares, smem);
-    } else if (!WIDE || i < shared) {
-        attn_wide_body<D, SRC, 1, false, KEYS_SHARED>(s, (int)(i % shared_x), (int)(i / shared_x), smem);
-    } else {
-        i -= shared;
+    } else if (WIDE && i < wide_x * w.n_chunks) {       // (the longer ones)
         attn_wide_pages<D, SRC, KEYS_OWN>(w, (int)(i % wide_x), (int)(i / wide_x), (int)wide_x, smem);
+    } else {
+        if (WIDE)
+            i -= wide_x * w.n_chunks;
+        attn_wide_body<D, SRC, 1, false, KEYS_SHARED>(s, (int)(i % shared_x), (int)(i / shared_x), smem);
     }
 }
 
-// The join, one wave a (token, head): the chunks of the shared keys, and what its own keys left: a slot of the row, or
-// (decode) the parts of the shares that it was cut between, or (wide) its chunks.
-template <int D>
-__global__ __launch_bounds__(256) void attn_prefix_join_kernel(AttnArgs s, AttnArgs w, AttnArgs d)
+// The parts of a row, joined by D / 4 lanes (`lane` of them; a row's lanes are in step): parts [0, n) at slot(c).
+template <int D, class Slot>
+__device__ __forceinline__ void join_row(const AttnArgs &a, int n, Slot slot, int64_t t, int hd, int lane)
 {
-    const int64_t th = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-    const int lane = threadIdx.x & 63;
-    if (th >= d.T * d.hq)
-        return;
-    const int t = (int)(th / d.hq), hd = (int)(th - (int64_t)t * d.hq);
-    int b = -1;
-    for (int s0 = 0; s0 < d.n_seqs; s0 += 64) {
-        const int i = s0 + lane;
-        const uint64_t hit = ballot64(i < d.n_seqs && d.cu_q[i] <= t && t < d.cu_q[i + 1]);
-        if (hit) {
-            b = s0 + __ffsll((unsigned long long)hit) - 1;
-            break;
+    constexpr int LPR = D / 4, AHEAD = 8;
+    auto largest = [](float v) {
+#pragma unroll
+        for (int off = LPR / 2; off >= 1; off >>= 1)
+            v = fmaxf(v, __shfl_xor(v, off, 64));
+        return v;
+    };
+    auto load_ml = [&](int c) { return c < n ? *(const f32x2 *)(a.part_ml + 2 * slot(c)) : f32x2{ATTN_LOWEST, 0.f}; };
+    const f32x2 first = load_ml(lane);
+    float mx = first[0];
+    for (int c = lane + LPR; c < n; c += LPR)
+        mx = fmaxf(mx, load_ml(c)[0]);
+    mx = largest(fmaxf(mx, ATTN_LOWEST));
+    float sum = 0.f;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = 0; c0 < n; c0 += LPR) {
+        const f32x2 ml = c0 ? load_ml(c0 + lane) : first;
+        const float f = c0 + lane < n ? __builtin_amdgcn_exp2f(ml[0] - mx) : 0.f;       // this lane's part
+        sum += f * ml[1];
+        const int m = min(LPR, n - c0);
+        for (int i = 0; i < m; i += AHEAD) {
+            f32x4 x[AHEAD];
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j)
+                x[j] = *(const f32x4 *)(a.part_o + slot(c0 + min(i + j, m - 1)) * D + 4 * lane);
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const float w = __shfl(f, i + j, LPR);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    acc[e] += i + j < m ? w * x[j][e] : 0.f;
+            }
         }
     }
-    if (b < 0)
+#pragma unroll
+    for (int off = LPR / 2; off >= 1; off >>= 1)
+        sum += __shfl_xor(sum, off, 64);
+    const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;
+    *(u32x2 *)(a.out + t * a.out_stride + (int64_t)hd * D + 4 * lane) =
+        u32x2{cvt_bf16x2(acc[0] * inv, acc[1] * inv), cvt_bf16x2(acc[2] * inv, acc[3] * inv)};
+    if (a.lse && lane == 0)
+        a.lse[t * a.hq + hd] = sum == 0.f ? -INFINITY : (mx + __builtin_amdgcn_logf(sum)) * (1.f / ATTN_LOG2E);
+}
+
+// The join, D / 4 lanes a (token, head): the chunks of the shared keys, and what its own keys left: a slot of the row, or
+// (decode) the parts of the shares that it was cut between, or (wide) its chunks.  A wave takes `heads` heads of a token.
+template <int D>
+__global__ __launch_bounds__(256) void attn_prefix_join_kernel(AttnArgs s, AttnArgs w, AttnArgs d, int heads)
+{
+    const uint32_t item = blockIdx.x * 4 + (threadIdx.x >> 6), pieces = (uint32_t)(d.hq + heads - 1) / heads;
+    const int t = uniform((int)(item / pieces)), h0 = uniform((int)(item - t * pieces)) * heads;
+    const int lane = threadIdx.x & 63;
+    if (t >= d.T)
         return;
-    const int q0 = max(d.cu_q[b], 0), n = (int)min((int64_t)d.cu_q[b + 1], d.T) - q0;
+    // the token's sequence: as in a batch of single tokens, or searched for, 256 sequences a trip to memory
+    int b = min(t, d.n_seqs - 1), q0 = d.cu_q[b], q1 = d.cu_q[b + 1];
+    if (t < q0 || t >= q1) {
+        b = -1;
+        for (int s0 = 0; s0 < d.n_seqs && b < 0; s0 += 256) {
+            int from[4], to[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = min(s0 + 64 * j + lane, d.n_seqs - 1);
+                from[j] = d.cu_q[i];
+                to[j] = d.cu_q[i + 1];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t hit = ballot64(from[j] <= t && t < to[j]);
+                if (b < 0 && hit) {
+                    const int src = __ffsll((unsigned long long)hit) - 1;
+                    b = min(s0 + 64 * j + src, d.n_seqs - 1);
+                    q0 = __builtin_amdgcn_readlane(from[j], src);
+                    q1 = __builtin_amdgcn_readlane(to[j], src);
+                }
+            }
+        }
+        if (b < 0)
+            return;
+    }
+    q0 = max(q0, 0);
+    const int n = (int)min((int64_t)q1, d.T) - q0;
     if (n > d.max_q)
         return;
-    const int L = (int)min((int64_t)max(d.kv_len[b], 0), min(d.max_kv, d.table_stride << d.cache.ps));
-    const int keys = shared_keys(d, b, n, L), chunks = (keys + s.chunk - 1) / s.chunk;
+    constexpr int LPR = D / 4;
     const int64_t rows = (int64_t)n * d.group;
+    const int end = min(h0 + heads, d.hq), l = lane & (LPR - 1);
     if (rows <= d.max_rows) {
-        const int h = hd / d.group, row = (t - q0) * d.group + hd - h * d.group;
-        const int32_t *const c = d.cuts + 2 * ((int64_t)b * d.hkv + h);
-        const int w0 = c[0], w1 = c[1];
-        if (w0 < 0 && keys == 0)        // answered whole
-            return;
-        join_parts<D>(d, 0, chunks + (w0 < 0 ? 1 : w1 - w0 + 1), [&](int i) {
-            return i < chunks ? row_slot(s, t, hd, i)
-                   : w0 < 0   ? row_slot(d, t, hd, 0)
-                              : part_slot(d, w0 + i - chunks, i > chunks, row);
-        }, t, hd);
+        for (int hd = h0 + lane / LPR; hd < end; hd += 64 / LPR) {
+            const int h = hd / d.group, row = (t - q0) * d.group + hd - h * d.group;
+            const u32x4 c = *(const u32x4 *)(d.cuts + 4 * ((int64_t)b * d.hkv + h));
+            const int w0 = (int)c[0], w1 = (int)c[1], keys = (int)c[2], chunks = (keys + s.chunk - 1) / s.chunk;
+            if (w0 < 0 && keys == 0)        // answered whole
+                continue;
+            join_row<D>(d, chunks + (w0 < 0 ? 1 : w1 - w0 + 1), [&](int i) {
+                return i < chunks ? row_slot(s, t, hd, i)
+                       : w0 < 0   ? row_slot(d, t, hd, 0)
+                                  : part_slot(d, w0 + i - chunks, i > chunks, row);
+            }, t, hd, l);
+        }
     } else {
+        const int L = (int)min((int64_t)max(d.kv_len[b], 0), min(d.max_kv, d.table_stride << d.cache.ps));
+        const int keys = shared_keys(d, b, n, L), chunks = (keys + s.chunk - 1) / s.chunk;
         if (w.n_chunks == 1 && keys == 0)
             return;
         const int hi = w.causal ? min(L, L - n + t - q0 + 1) : L, from = keys & ~(AW_BN - 1);
         const int own = hi > keys ? (hi - 1 - from) / w.chunk + 1 : 1;
-        join_parts<D>(d, 0, chunks + own, [&](int i) { return i < chunks ? row_slot(s, t, hd, i) : row_slot(w, t, hd, i - chunks); },
-                      t, hd);
+        for (int hd = h0 + lane / LPR; hd < end; hd += 64 / LPR)
+            join_row<D>(d, chunks + own, [&](int i) { return i < chunks ? row_slot(s, t, hd, i) : row_slot(w, t, hd, i - chunks); },
+                        t, hd, l);
     }
 }
 
@@ -100,11 +170,19 @@ hipError_t launch_attn_prefix(const AttnArgs &s, const AttnArgs &w, const AttnAr
 
 hipError_t launch_attn_prefix_join(const AttnArgs &s, const AttnArgs &w, const AttnArgs &d, int head_dim, hipStream_t stream)
 {
-    const unsigned blocks = (unsigned)((d.T * d.hq + 3) / 4);
+    // a wave's lanes full, and more heads a wave where there are rows enough to fill the card with waves
+    const int least = 256 / head_dim;
+    int heads = least;
+    while (heads < 8 && d.T * d.hq >= 2 * heads * INT64_C(8192))
+        heads *= 2;
+    const int64_t waves = d.T * ((d.hq + heads - 1) / heads);
+    if (waves > INT64_C(0x7fffffff))
+        return hipErrorInvalidValue;
+    const unsigned blocks = (unsigned)((waves + 3) / 4);
     if (head_dim == 64)
-        attn_prefix_join_kernel<64><<<blocks, 256, 0, stream>>>(s, w, d);
+        attn_prefix_join_kernel<64><<<blocks, 256, 0, stream>>>(s, w, d, heads);
     else
-        attn_prefix_join_kernel<128><<<blocks, 256, 0, stream>>>(s, w, d);
+        attn_prefix_join_kernel<128><<<blocks, 256, 0, stream>>>(s, w, d, heads);
     return hipGetLastError();
 }
 

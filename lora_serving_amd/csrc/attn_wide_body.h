@@ -183,6 +183,16 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
         return it.total;
     const int b = it.seq, rb = it.block, q0 = it.q0, n = it.n, L = it.L, key0 = it.key0;
     const int rows = n * a.group;
+    if (KEYS == KEYS_SHARED && a.alone_rows < a.max_rows) {
+        // rows of one sequence that shares nothing
+        const int ta = q0 + rb * BM / a.group, tb = q0 + (min(rows, rb * BM + BM) - 1) / a.group;
+        bool skip = false;
+#pragma unroll 4
+        for (int s = b + lane; s < a.n_seqs; s += 64)
+            skip |= a.cu_q[s] <= ta && tb < a.cu_q[s + 1] && ((int64_t)a.cu_q[s + 1] - a.cu_q[s]) * a.group > a.alone_rows;
+        if (__any(skip))
+            return it.total;
+    }
     const int own = KEYS == KEYS_OWN ? shared_keys(a, b, n, L) : 0;     // the first key that is the sequence's own
 
     // this lane's row, and the keys that the workgroup's and the wave's rows see
