@@ -21,7 +21,7 @@ template <int D, bool FP8, bool MORE, int KEYS>
 __global__ __launch_bounds__(256, 2) void attn_mixed_kernel(AttnArgs w, AttnArgs d, uint32_t wide_x, uint32_t shares)
 {
     constexpr int SRC = FP8 ? AW_PAGES_E4M3 : AW_PAGES;
-    constexpr int LDS = wide_lds<D, SRC, 1> > decode_lds<D, 1> ? wide_lds<D, SRC, 1> : decode_lds<D, 1>;
+    constexpr int LDS_W = wide_lds<D, SRC, 1, KEYS>, LDS = LDS_W > decode_lds<D, 1> ? LDS_W : decode_lds<D, 1>;
     __shared__ __attribute__((aligned(16))) uint8_t smem[LDS];
     uint32_t i = blockIdx.x;
     const bool is_wide = mixed_place(wide_x * w.n_chunks, shares, &i);

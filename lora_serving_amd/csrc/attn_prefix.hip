@@ -16,7 +16,7 @@ __global__ __launch_bounds__(256, 2) void attn_prefix_kernel(AttnArgs s, AttnArg
                                                              uint32_t wide_x, uint32_t shares)
 {
     constexpr int SRC = FP8 ? AW_PAGES_E4M3 : AW_PAGES;
-    constexpr int LDS_D = decode_lds<D, NQ, KEYS_OWN>, LDS = wide_lds<D, SRC, 1> > LDS_D ? wide_lds<D, SRC, 1> : LDS_D;
+    constexpr int LDS_D = decode_lds<D, NQ, KEYS_OWN>, LDS_W = wide_lds<D, SRC, 1, KEYS_OWN>, LDS = LDS_W > LDS_D ? LDS_W : LDS_D;
     __shared__ __attribute__((aligned(16))) uint8_t smem[LDS];
     uint32_t i = blockIdx.x;
     const uint32_t shared = shared_x * s.n_chunks;

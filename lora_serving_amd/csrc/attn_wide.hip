@@ -9,7 +9,7 @@ namespace mlora {
 template <int D, int SRC, int KG, int KEYS>
 __global__ __launch_bounds__(KG * 256, 2) void attn_wide_kernel(AttnArgs a)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t smem[wide_lds<D, SRC, KG>];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[wide_lds<D, SRC, KG, KEYS>];
     attn_wide_body<D, SRC, KG, false, KEYS>(a, blockIdx.x, blockIdx.y, smem);
 }
 

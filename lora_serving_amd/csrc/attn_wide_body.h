@@ -145,13 +145,18 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, W
     }
 }
 
+// tiles, scales, the join of halves, and (but for KEYS_PLAIN) which keys of two tiles hold an infinity or NaN in V
 template <int D, int SRC, int KG>
-constexpr int wide_lds = KG * 4 * AW_BN * D * 2 + (SRC == AW_PAGES_E4M3 ? 4 * 2 * AW_BN * 4 : 0) + (KG > 1 ? 4 * 64 * 2 * 4 : 0);
+constexpr int wide_tiles = KG * 4 * AW_BN * D * 2 + (SRC == AW_PAGES_E4M3 ? 4 * 2 * AW_BN * 4 : 0) + (KG > 1 ? 4 * 64 * 2 * 4 : 0);
+template <int D, int SRC, int KG, int KEYS = KEYS_PLAIN>
+constexpr int wide_lds = wide_tiles<D, SRC, KG> + (KEYS == KEYS_PLAIN ? 0 : KG * 2 * 4 * 2);
 
 // Item and kv head bx, and chunk of keys by; smem: wide_lds bytes.  Returns how many items there are.  (MORE: called
 // for several items.)
-// KEYS_SINKS: the tiles that hold the first keys and those of the window are numbered through, without the tiles that
-// no row of the workgroup sees between them; chunks are equal pieces of these numbers.
+// KEYS_SINKS: tiles are made of blocks of 16 keys, as many as a wave copies; those of the first keys and of the window are
+// numbered through, without the blocks that no row of the workgroup sees between them, so that a few first keys cost a
+// quarter of a tile and the window's begins in the same one (8 prompts of 2048, window 512, 4 first keys: @SINK16@).  Chunks
+// are equal pieces of the tiles.
 template <int D, int SRC, int KG, bool MORE = false, int KEYS = KEYS_PLAIN>
 __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by, uint8_t *smem)
 {
@@ -211,19 +216,20 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     const int wmin = first_key(wrow), wmax = wrow < rows ? end_key(wrow + 31) : 0;
     // the tiles, or this half's of them
     int ta = kmin / BN, tb = kmax > kmin ? (kmax + BN - 1) / BN : ta;
-    // KEYS_SINKS: tiles from number ts on lie `skip` tiles further
-    const int ts = KEYS == KEYS_SINKS ? min((a.sinks + BN - 1) / BN, ta) : 0, skip = KEYS == KEYS_SINKS ? ta - ts : 0;
-    auto place = [&](int t) { return KEYS == KEYS_SINKS && t >= ts ? t + skip : t; };
+    // KEYS_SINKS: blocks from number gs on lie `skip` blocks further
+    const int gs = KEYS == KEYS_SINKS ? (min(a.sinks, L) + 15) / 16 : 0, skip = KEYS == KEYS_SINKS ? max(kmin / 16 - gs, 0) : 0;
+    auto block_key = [&](int g) { return 16 * (KEYS == KEYS_SINKS && g >= gs ? g + skip : g); };
     if (KEYS == KEYS_SINKS) {
-        const int all = tb - skip;
+        const int all = kmax > kmin ? ((kmax + 15) / 16 - skip + 3) / 4 : 0;
         ta = (int)((int64_t)all * by / a.n_chunks);
         tb = (int)((int64_t)all * (by + 1) / a.n_chunks);
     }
     const int tm = KG > 1 ? ta + (tb - ta + 1) / 2 : tb;
     const int t0 = kg ? tm : ta, t1 = kg ? tb : tm;
     // tiles [f0, f1): every row of the workgroup sees every key
-    const int f0 = max(t0, (first_key(rb * BM + BM - 1) + BN - 1) / BN - skip);
-    const int f1 = max(min(t1, min(kmax, end_key(rb * BM)) / BN - skip), f0);
+    const int seen0 = first_key(rb * BM + BM - 1), seen1 = min(kmax, end_key(rb * BM));
+    const int f0 = max(t0, KEYS == KEYS_SINKS ? ((seen0 + 15) / 16 - skip + 3) / 4 : (seen0 + BN - 1) / BN);
+    const int f1 = max(min(t1, KEYS == KEYS_SINKS ? (seen1 / 16 - skip) / 4 : seen1 / BN), f0);
 
     u32x4 qf[KS];
     {
@@ -247,47 +253,60 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     const int w16 = 16 * wave, crow = lane / LPR, cpiece = lane % LPR;
     const int32_t *__restrict__ table = SRC == AW_ROWS ? nullptr : a.table + (int64_t)b * a.table_stride;
     const int ps = a.cache.ps, pm = (1 << ps) - 1;
+    const int row0 = KEYS == KEYS_SINKS ? 0 : w16;          // (KEYS_SINKS: the base is the wave's)
     uint32_t off_k[IPW], off_v[IPW], piece[IPW];
 #pragma unroll
     for (int i = 0; i < IPW; ++i) {
         const int r = RPI * i + crow;
         piece[i] = 16 * (FP8 ? cpiece : cpiece ^ aw_swz<D>(r));
-        off_k[i] = piece[i] + (SRC == AW_ROWS ? (uint32_t)(w16 + r) * (uint32_t)(2 * a.k_stride)
+        off_k[i] = piece[i] + (SRC == AW_ROWS ? (uint32_t)(row0 + r) * (uint32_t)(2 * a.k_stride)
                                               : (uint32_t)r * D * (FP8 ? 1 : 2));
-        off_v[i] = SRC == AW_ROWS ? piece[i] + (uint32_t)(w16 + r) * (uint32_t)(2 * a.v_stride) : off_k[i];
+        off_v[i] = SRC == AW_ROWS ? piece[i] + (uint32_t)(row0 + r) * (uint32_t)(2 * a.v_stride) : off_k[i];
     }
-    const uint16_t *kp = a.k + ((int64_t)key0 + (int64_t)place(t0) * BN) * a.k_stride + (int64_t)h * D;   // rows: the next tile
-    const uint16_t *vp = a.v + ((int64_t)key0 + (int64_t)place(t0) * BN) * a.v_stride + (int64_t)h * D;
+    // rows: the next tile (KEYS_SINKS: the sequence)
+    const uint16_t *kp = a.k + ((int64_t)key0 + (KEYS == KEYS_SINKS ? 0 : (int64_t)t0 * BN)) * a.k_stride + (int64_t)h * D;
+    const uint16_t *vp = a.v + ((int64_t)key0 + (KEYS == KEYS_SINKS ? 0 : (int64_t)t0 * BN)) * a.v_stride + (int64_t)h * D;
     int pgs = 0, pgk = 0, pgv = 0;
     u32x4 kr[IPW], vr[IPW];
     float scr = 0.f;
+    // the first key of this wave's rows of a tile
+    auto wave_key = [&](int t) { return KEYS == KEYS_SINKS ? block_key(4 * t + wave) : t * BN + w16; };
     // pages of this wave's rows of the 64 tiles around t, one a lane: a scalar load a tile comes late when memory is
     // busy, and its wait drains the reads of LDS with it (256 single tokens and a chunk of 2048 392 us, so 367; a
     // chunk split into pieces of a few tiles waits longer for its first: 100 tokens over 8192 39.4 us, so 40.1)
     auto lookup = [&](int t) {
         if (SRC != AW_ROWS)
-            pgs = table[min(place((t & ~63) + lane) * BN + w16, L - 1) >> ps];
+            pgs = table[min(wave_key((t & ~63) + lane), L - 1) >> ps];
     };
     // (to: where the tile goes, bytes of LDS, this wave's rows)
     auto copy = [&](int t, const uint16_t *&rows, int64_t stride, const uint8_t *pages, int pg, const uint32_t (&off)[IPW],
                     uint32_t to, u32x4 (&regs)[IPW]) __attribute__((always_inline)) {
-        const int p = place(t);
-        if (SRC == AW_ROWS) {
-            if (p * BN + BN <= L) {
+        if (SRC == AW_ROWS && KEYS == KEYS_SINKS) {
+            const int key = wave_key(t), from = min(key, L - 1);
+            const uint16_t *const base = rows + from * stride;
+            if (key + 16 <= L) {
+#pragma unroll
+                for (int i = 0; i < IPW; ++i)
+                    aw_dma(base, off[i], to, RPI * i * D * 2);
+            } else {
+#pragma unroll
+                for (int i = 0; i < IPW; ++i)
+                    aw_dma(base, (uint32_t)min(RPI * i + crow, L - 1 - from) * (uint32_t)(2 * stride) + piece[i], to, RPI * i * D * 2);
+            }
+        } else if (SRC == AW_ROWS) {
+            if (t * BN + BN <= L) {
 #pragma unroll
                 for (int i = 0; i < IPW; ++i)
                     aw_dma(rows, off[i], to, RPI * i * D * 2);
             } else {
 #pragma unroll
                 for (int i = 0; i < IPW; ++i)
-                    aw_dma(rows, (uint32_t)min(w16 + RPI * i + crow, L - 1 - p * BN) * (uint32_t)(2 * stride) + piece[i],
+                    aw_dma(rows, (uint32_t)min(w16 + RPI * i + crow, L - 1 - t * BN) * (uint32_t)(2 * stride) + piece[i],
                            to, RPI * i * D * 2);
             }
             rows += BN * stride;
-            if (KEYS == KEYS_SINKS && t + 1 == ts)
-                rows += (int64_t)skip * BN * stride;
         } else {
-            const int64_t at = (((int64_t)uniform(pg) * a.cache.hkv + h) << ps) + ((p * BN + w16) & pm);
+            const int64_t at = (((int64_t)uniform(pg) * a.cache.hkv + h) << ps) + (wave_key(t) & pm);
             const uint8_t *base = pages + at * D * (FP8 ? 1 : 2);
 #pragma unroll
             for (int i = 0; i < IPW; ++i)
@@ -307,7 +326,7 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             copy(t + 1, kp, a.k_stride, a.cache.k, pgk, off_k, to_k + ((t + 1) & 1) * (2 * TILE), kr);
             if (FP8 && lane < 32)       // scales of K and of V, both of tile t + 1 (this wave's rows)
                 scr = (lane < 16 ? a.cache.k_scale : a.cache.v_scale)[(((int64_t)pgk * a.cache.hkv + h) << ps) +
-                                                                      ((place(t + 1) * BN + w16 + (lane & 15)) & pm)];
+                                                                      ((wave_key(t + 1) + (lane & 15)) & pm)];
         }
     };
     auto issue_v = [&](int t) __attribute__((always_inline)) {
@@ -399,12 +418,15 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
                (a.window <= 0 || key > pos - a.window || (KEYS == KEYS_SINKS && key < a.sinks));
     };
     auto hide = [&](int t, f32x16 (&st)[2]) {
-        const int key0 = place(t) * BN;
+        int from[4];            // (first keys of the tile's blocks)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            from[j] = block_key(4 * t + j);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                st[u][i] = sees(key0 + 32 * u + 8 * (i / 4) + 4 * hh + i % 4) ? st[u][i] : -INFINITY;
+                st[u][i] = sees(from[2 * u + i / 8] + 8 * (i / 4 % 2) + 4 * hh + i % 4) ? st[u][i] : -INFINITY;
             }
     };
     auto largest = [&](const f32x16 &s, int i0, int i1, float mx) {
@@ -534,12 +556,49 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     };
     // the same for a tile that some rows see in part: V may hold an infinity or NaN where a row must not see it
     // (0 x NaN is NaN); then one key at a time, kept only by the rows that see it
+    // (but for KEYS_PLAIN each wave has looked at its own rows before the barrier: a quarter of the reads.  8 prompts of 2048,
+    // window 512, 4 first keys: @SCAN@)
+    constexpr bool SCAN = KEYS != KEYS_PLAIN;
+    uint16_t *const flags = (uint16_t *)(smem + wide_tiles<D, SRC, KG>) + 8 * kg;
+    auto scan = [&](int t) {
+        const uint8_t *const v = (const uint8_t *)(vl + (t & 1) * TILE + w16 * D) + 16 * lane;
+        uint32_t rows = 0;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {          // 64 / CPR rows at a time
+            const u32x4 w = *(const u32x4 *)(v + 1024 * j);
+            uint32_t x = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x = not_finite(x, w[i]);
+            const uint64_t hit = ballot64((x & 0x80008000u) != 0);
+            if (hit)
+#pragma unroll
+                for (int r = 0; r < 64 / CPR; ++r)
+                    rows |= (uint32_t)((hit >> (CPR * r) & ((UINT64_C(1) << CPR) - 1)) != 0) << (64 / CPR * j + r);
+        }
+        if (lane == 0)
+            flags[4 * (t & 1) + wave] = (uint16_t)rows;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
     auto outputs_edge = [&](int t) {
+        uint64_t found = 0;
+        if (SCAN) {
+            const u32x2 f = *(const u32x2 *)(flags + 4 * (t & 1));
+            const uint64_t rows = (uint64_t)(uint32_t)uniform((int)f[1]) << 32 | (uint32_t)uniform((int)f[0]);
+            if (rows == 0) {
+                outputs(t);
+                return;
+            }
+            for (uint64_t rest = rows; rest; rest &= rest - 1) {        // row 16 s + 8 x + 4 y + z: bit 32 y + 8 s + 4 x + z
+                const int r = __ffsll((unsigned long long)rest) - 1;
+                found |= UINT64_C(1) << (32 * (r >> 2 & 1) + 8 * (r >> 4) + 4 * (r >> 3 & 1) + (r & 3));
+            }
+        }
         const uint32_t at = tile_at(vlane, t);
         // keys of this lane's fragments (k index (hh, e) of step s) that hold an infinity or NaN: bit 8 s + e
         uint32_t bad = 0;
 #pragma unroll 1
-        for (int s = 0; s < 4; ++s) {
+        for (int s = 0; s < (SCAN ? 0 : 4); ++s) {
             u32x4 w = {0, 0, 0, 0};
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
@@ -558,10 +617,11 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1)
                 bad |= __shfl_xor(bad, off, 64);
-        const uint64_t some = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)bad, 32) << 32) | (uint32_t)uniform((int)bad);
+        const uint64_t some = SCAN ? found
+                                   : ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)bad, 32) << 32) | (uint32_t)uniform((int)bad);
         for (uint64_t rest = some; rest; rest &= rest - 1) {
             const int bit = __ffsll((unsigned long long)rest) - 1, s = (bit & 31) >> 3, e = bit & 7;
-            const bool see = sees(place(t) * BN + 16 * s + 8 * (e >> 2) + 4 * (bit >> 5) + (e & 3));
+            const bool see = sees(block_key(4 * t + s) + 8 * (e >> 2) + 4 * (bit >> 5) + (e & 3));
             const uint32_t half = hh != (bit >> 5) ? 0u : (e & 1) ? 0xffff0000u : 0xffffu;
             u32x4 p;
 #pragma unroll
@@ -597,8 +657,7 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     };
     // a tile on its own (K of it in place before; afterwards K of the next)
     auto single = [&](int t) {
-        const int key0 = place(t) * BN;
-        const bool work = key0 < wmax && (key0 + BN > wmin || (KEYS == KEYS_SINKS && key0 < a.sinks));
+        const bool work = block_key(4 * t) < wmax && (block_key(4 * t + 3) + 16 > wmin || (KEYS == KEYS_SINKS && 4 * t < gs));
         if (t > t0)
             issue(t);
         if (work) {
@@ -609,6 +668,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             all_powers(t, sa, std::true_type());
         }
         land(t);
+        if (SCAN)
+            scan(t);
         phase_end();
         if (work)
             outputs_edge(t);
@@ -630,6 +691,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             if (t > t0)
                 issue(t);
             land(t);
+            if (SCAN)
+                scan(t);
             phase_end();
         }
     }
