@@ -204,15 +204,16 @@ size_t paged_room(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d,
 constexpr int32_t ALONE_ROWS = 256;
 
 // Chunks of keys for `items` row blocks of `keys` keys at the most, up to `limit`, in us: a tile takes 1.2 in a workgroup alone
-// on its CU and 1.95 in two, in rounds of 512, and a part of 128 rows 0.04 to write and to read again.
-int64_t prefix_cuts(int64_t items, int64_t keys, int64_t limit)
+// on its CU and 1.95 in two, in rounds of 512, and a part of 128 rows 0.08 to write and to read again (whole: one chunk leaves
+// none).
+int64_t prefix_cuts(int64_t items, int64_t keys, int64_t limit, bool whole)
 {
     const int64_t tiles = (keys + 63) / 64;
     int64_t best = 1;
     double least = 0.;
     for (int64_t n = 1; n <= limit && (n == 1 || n * items <= 8 * CUS); ++n) {
         const int64_t groups = items * n, each = (tiles + n - 1) / n;
-        const double us = (groups <= CUS ? 1.2 * each : 1.95 * each * ((groups + 2 * CUS - 1) / (2 * CUS))) + 0.04 * groups;
+        const double us = (groups <= CUS ? 1.2 * each : 1.95 * each * ((groups + 2 * CUS - 1) / (2 * CUS))) + (whole && n == 1 ? 0. : 0.08 * groups);
         if (n == 1 || us < least) {
             best = n;
             least = us;
@@ -244,7 +245,7 @@ int64_t own_workgroups(int32_t n_seqs, int32_t hkv, int64_t max_kv)
     return std::min(((int64_t)n_seqs * hkv * units + 3) / 4, 2 * CUS);
 }
 
-PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv,
+PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv,
                        int64_t max_prefix)
 {
     PrefixPlan p;
@@ -253,17 +254,21 @@ PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32
     const int64_t group = hq / hkv, all = T * group, items = (all + WIDE_ROWS - 1) / WIDE_ROWS * hkv;
     const int64_t alone = max_q * group > ALONE_ROWS ? std::min(T, std::max<int64_t>(T - n_seqs, 0) / std::max<int64_t>(max_q - 1, 1) * max_q) * group : 0;
     const auto blocks = [&](int64_t rows) { return std::max<int64_t>(1, (rows + WIDE_ROWS - 1) / WIDE_ROWS) * hkv; };
-    const int64_t shared = blocks(all - alone);
-    int64_t n = prefix_cuts(shared, max_prefix, most_prefix_cuts(items, max_prefix));
+    // (half of the groups' last row blocks are taken to be more)
+    const int64_t shared = blocks(all - alone) + std::min<int64_t>(n_groups / 2, T) * hkv;
+    int64_t n = prefix_cuts(shared, max_prefix, most_prefix_cuts(items, max_prefix), false);
+    if (getenv("PX_N")) n = std::min<int64_t>(atoi(getenv("PX_N")), most_prefix_cuts(items, max_prefix));
     p.chunk = ((max_prefix + n - 1) / n + 63) & ~INT64_C(63);
     p.chunks = (max_prefix + p.chunk - 1) / p.chunk;
     // the card holds 512 workgroups: those of the shares start beside the others' (one of each on a CU at the most)
     const int64_t beside = std::min(shared * p.chunks, CUS);
     p.own.shares = p.own.dec_rows > 0 ? (int)std::min(own_workgroups(n_seqs, hkv, max_kv), 2 * CUS - beside) : 0;
+    if (getenv("PX_W") && p.own.dec_rows) p.own.shares = std::min<int64_t>(own_workgroups(n_seqs, hkv, max_kv),atoi(getenv("PX_W")));
     p.share_slots = 2 * 4 * (int64_t)p.own.shares * p.own.dec_rows;
     if (p.own.wide) {
         const int64_t keys = std::max<int64_t>(max_kv, 1);
-        n = prefix_cuts(blocks(alone > 0 ? alone : all), keys, most_prefix_cuts(items, keys));
+        n = prefix_cuts(blocks(alone > 0 ? alone : all), keys, most_prefix_cuts(items, keys), true);
+        if (getenv("PX_WN")) n = std::min<int64_t>(atoi(getenv("PX_WN")), most_prefix_cuts(items, keys));
         p.own.wide_chunk = ((keys + n - 1) / n + 127) & ~INT64_C(127);
         p.own.wide_chunks = (keys + p.own.wide_chunk - 1) / p.own.wide_chunk;
     }
@@ -707,7 +712,7 @@ mlora_status mlora_prefix_attention(const void *q, int64_t q_stride, int64_t T, 
     if (n_groups == 0 || max_prefix == 0)
         return run_paged(c, ws, ws_bytes, stream);
     const AttnArgs &a = c.a;
-    const PrefixPlan p = prefix_plan(a.T, a.n_seqs, a.hq, a.hkv, c.d, a.max_q, a.max_kv, max_prefix);
+    const PrefixPlan p = prefix_plan(a.T, a.n_seqs, n_groups, a.hq, a.hkv, c.d, a.max_q, a.max_kv, max_prefix);
     if (p.own.wide_chunks > 65535)
         return MLORA_ERR_UNSUPPORTED;
     uint8_t *const base = workspace(ws, ws_bytes, p.total());

@@ -161,6 +161,11 @@ __device__ __forceinline__ Group group_at(const AttnArgs &a, int g)
 
 // How many of sequence b's L keys (n of them its queries') are its group's: all of those, or none if some query does
 // not see them.
+__device__ __forceinline__ int shared_keys(const AttnArgs &a, const Group &g, int b, int n, int L)
+{
+    return b >= g.b0 && b < g.b1 && (a.causal ? L - n : L) >= g.keys && (int64_t)n * a.group <= a.alone_rows ? g.keys : 0;
+}
+
 __device__ __forceinline__ int shared_keys(const AttnArgs &a, int b, int n, int L)
 {
     int lo = 0, hi = a.n_groups;
@@ -171,8 +176,7 @@ __device__ __forceinline__ int shared_keys(const AttnArgs &a, int b, int n, int 
         else
             hi = mid;
     }
-    const Group g = group_at(a, lo);
-    return b >= g.b0 && b < g.b1 && (a.causal ? L - n : L) >= g.keys && (int64_t)n * a.group <= a.alone_rows ? g.keys : 0;
+    return shared_keys(a, group_at(a, lo), b, n, L);
 }
 
 // Slot of part c among a row's own (see AttnArgs).

@@ -24,30 +24,37 @@
 namespace mlora {
 
 // A sequence: its queries and the units [first, first + units) of the keys [lo, L) that they see (at least one
-// unit; none if this launch does not answer the sequence).  KEYS_SINKS: `sink` units of the first keys come before
-// those from `first` on, and are counted in `units`; where no block of 32 lies between the first keys and lo, all
-// units are taken.
+// unit; none if this launch does not answer the sequence).  KEYS_SINKS: `sink` blocks of 32 first keys and those from lo
+// on are numbered through, without the `first` blocks between them, and four in a row are a unit.
 struct SeqUnits {
     int q0, n, L, lo, first, units, sink;
 };
 
 template <int KEYS> constexpr int unit_keys = KEYS == KEYS_OWN ? OWN_UNIT : DECODE_UNIT;
 
-template <int KEYS>
-__device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b)
+// (shared: KEYS_OWN, a function of b, n and L that gives the sequence's shared keys)
+template <int KEYS, class Shared>
+__device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b, Shared shared)
 {
     constexpr int UNIT = unit_keys<KEYS>;
     SeqUnits s;
     s.q0 = (int)min((int64_t)max(a.cu_q[b], 0), a.T);
     s.n = (int)min((int64_t)max(a.cu_q[b + 1], 0), a.T) - s.q0;
     s.L = (int)min((int64_t)max(a.kv_len[b], 0), min(a.max_kv, a.table_stride << a.cache.ps));
-    s.lo = KEYS == KEYS_OWN ? shared_keys(a, b, s.n, s.L) : a.window > 0 ? max(0, s.L - s.n - a.window + 1) : 0;
-    s.first = KEYS == KEYS_SINKS && a.sinks >= (s.lo & ~31) ? 0 : s.lo / UNIT;
-    s.sink = KEYS == KEYS_SINKS ? min((a.sinks + UNIT - 1) / UNIT, s.first) : 0;
+    s.lo = KEYS == KEYS_OWN ? shared(b, s.n, s.L) : a.window > 0 ? max(0, s.L - s.n - a.window + 1) : 0;
+    s.sink = KEYS == KEYS_SINKS ? min((a.sinks + 31) / 32, s.lo / 32) : 0;
+    s.first = KEYS == KEYS_SINKS ? s.lo / 32 - s.sink : s.lo / UNIT;
     const int64_t rows = (int64_t)s.n * a.group;
     const bool mine = s.n > 0 && s.n <= a.max_q && rows >= a.min_rows && rows <= a.max_rows;
-    s.units = mine ? max(1, (s.L + UNIT - 1) / UNIT - s.first + s.sink) : 0;
+    const int units = KEYS == KEYS_SINKS ? ((s.L + 31) / 32 - s.first + UNIT / 32 - 1) / (UNIT / 32) : (s.L + UNIT - 1) / UNIT - s.first;
+    s.units = mine ? max(1, units) : 0;
     return s;
+}
+
+template <int KEYS>
+__device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b)
+{
+    return seq_units<KEYS>(a, b, [&](int b, int n, int L) { return shared_keys(a, b, n, L); });
 }
 
 // Units of the sequences per lane (`per` consecutive ones each): this lane's, those before it, and all (one head's);
@@ -150,9 +157,10 @@ __device__ __forceinline__ int ad_swz(int key)
     return D == 128 ? (key & 7) << 1 | ((key >> 3) & 1) : ((key >> 1) & 3) << 1 | ((key >> 3) & 1);
 }
 
-// (KEYS_OWN: V and Q of each wave; else V, the waves' parts and Q)
+// (KEYS_OWN: V and Q of each wave, and the first OWN_SEQS sequences; else V, the waves' parts and Q)
+constexpr int OWN_SEQS = 256;
 template <int D, int NQ, int KEYS = KEYS_PLAIN>
-constexpr int decode_lds = KEYS == KEYS_OWN ? 4 * 2 * 32 * D + (NQ > 1 ? 4 * 16 * NQ * D * 2 : 0)
+constexpr int decode_lds = KEYS == KEYS_OWN ? 4 * 2 * 32 * D + (NQ > 1 ? 4 * 16 * NQ * D * 2 : 0) + OWN_SEQS * 5 * 4
                                             : 4 * 2 * (32 * D > 32 * (D + 4) ? 32 * D : 32 * (D + 4)) + 4 * 16 * 2 * 4 +
                                                   (NQ > 1 ? 16 * NQ * D * 2 : 0);
 
@@ -188,48 +196,97 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
     const int ps = a.cache.ps, pm = (1 << ps) - 1;
     uint16_t *vl = lds + wave * VW;
 
+    // KEYS_OWN: up to OWN_SEQS sequences are listed in LDS, 64 a wave, from loads that do not wait for each other: a chain
+    // of them for each of a lane's sequences, its group searched for, took @LIST@
+    const bool listed = OWN && a.n_seqs <= OWN_SEQS && a.n_groups <= 64;
+    u32x4 *const list = (u32x4 *)(smem + decode_lds<D, NQ, KEYS> - OWN_SEQS * 5 * 4);      // q0, n, L, lo
+    int *const list_of = (int *)(list + OWN_SEQS);                                          // units
+    if (listed) {
+        Group mine = {0, 0, 0};
+        if (lane < a.n_groups)
+            mine = group_at(a, lane);
+        const int s = 64 * wave + lane;
+        if (64 * wave < a.n_seqs) {
+            const SeqUnits q = seq_units<KEYS>(a, min(s, a.n_seqs - 1), [&](int b, int n, int L) {
+                Group g = {0, 0, 0};
+                for (int i = 0; i < a.n_groups; ++i) {
+                    const Group x = {__builtin_amdgcn_readlane(mine.b0, i), __builtin_amdgcn_readlane(mine.b1, i),
+                                     __builtin_amdgcn_readlane(mine.keys, i)};
+                    if (b >= x.b0 && b < x.b1)
+                        g = x;
+                }
+                return shared_keys(a, g, b, n, L);
+            });
+            list[s] = u32x4{(uint32_t)q.q0, (uint32_t)q.n, (uint32_t)q.L, (uint32_t)q.lo};
+            list_of[s] = s < a.n_seqs ? q.units : 0;
+        }
+        __syncthreads();
+    }
+    auto list_at = [&](int b) {
+        const u32x4 x = list[b];
+        const int lo = uniform((int)x[3]);
+        return SeqUnits{uniform((int)x[0]), uniform((int)x[1]), uniform((int)x[2]), lo, lo / UNIT, uniform(list_of[b]), 0};
+    };
+    auto list_units = [&] {         // (as lane_units)
+        LaneUnits u{};
+        u.per = (a.n_seqs + 63) / 64;
+        for (int i = 0; i < u.per; ++i)
+            u.mine += lane * u.per + i < a.n_seqs ? list_of[lane * u.per + i] : 0;
+        const int upto = wave_prefix(u.mine);
+        u.before = upto - u.mine;
+        u.total = __builtin_amdgcn_readlane(upto, 63);
+        return u;
+    };
+    auto list_find = [&](const LaneUnits &u, uint32_t at) {         // (as find_unit)
+        UnitPlace p;
+        const uint32_t first = (uint32_t)u.before * a.hkv;
+        const int src = __ffsll((unsigned long long)ballot64(first <= at && at - first < (uint32_t)u.mine * a.hkv)) - 1;
+        uint32_t rest = at - (uint32_t)__builtin_amdgcn_readlane(u.before, src) * a.hkv;
+        p.b = src * u.per;
+        p.sq = list_at(p.b);
+        for (; rest >= (uint32_t)p.sq.units * a.hkv; p.sq = list_at(++p.b))
+            rest -= (uint32_t)p.sq.units * a.hkv;
+        p.h = (int)(rest / (uint32_t)p.sq.units);
+        p.f = (int)rest - p.h * p.sq.units;
+        return p;
+    };
+
     // this workgroup's share: `left` units from unit f of (sequence b, head h) on
-    UnitPlace at;
+    UnitPlace from;
     int left;
     Shares cut(0, 0);
     uint32_t u0 = 0;            // the unit f's number among all
     if (!OWN && a.part_o == nullptr) {          // one workgroup a sequence and head
-        at.b = (int)(share / a.hkv);
-        at.h = (int)(share - (unsigned)at.b * a.hkv);
-        at.f = 0;
-        at.sq = seq_units<KEYS>(a, at.b);
-        left = at.sq.units;
+        from.b = (int)(share / a.hkv);
+        from.h = (int)(share - (unsigned)from.b * a.hkv);
+        from.f = 0;
+        from.sq = seq_units<KEYS>(a, from.b);
+        left = from.sq.units;
     } else {
-        const LaneUnits u = lane_units<KEYS>(a, lane);
-        cut = Shares((uint32_t)u.total * a.hkv, OWN ? 4 * shares : shares);
+        const LaneUnits u = listed ? list_units() : lane_units<KEYS>(a, lane);
+        // (OWN: half of what a sequence and head has in the mean, up to four units, at the least, for each part is one more
+        // for the join)
+        const uint32_t all = (uint32_t)u.total * a.hkv, least = OWN ? min(max(all / (2 * (uint32_t)(a.n_seqs * a.hkv)), 1u), 4u) : 1;
+        cut = Shares(all, OWN ? min(4 * shares, (all + least - 1) / least) : shares);
         if (share >= cut.n)
             return;
         u0 = cut.start(share);
         left = (int)(cut.start(share + 1) - u0);
-        at = find_unit<KEYS>(a, u, u0);
+        from = listed ? list_find(u, u0) : find_unit<KEYS>(a, u, u0);
     }
-    int b = at.b, h = at.h, f = at.f;
-    SeqUnits sq = at.sq;
+    int b = from.b, h = from.h, f = from.f;
+    SeqUnits sq = from.sq;
     const float cs = a.scale * ATTN_LOG2E;
     const int last = (int)a.table_stride - 1;
 
     while (left > 0) {
         const int end = min(sq.units, f + left);
         const int rows = sq.n * a.group, L = sq.L, head = turned_head(a, b, h);
-        int k0, k1, s1 = 0;         // keys [k0, k1); KEYS_SINKS: and those from unit f to s1 before them
-        if (KEYS == KEYS_SINKS) {
-            // (first keys that reach into the unit `first`: from its start on)
-            const int unit = max(sq.first, sq.first + f - sq.sink) * UNIT;
-            k0 = max(unit, a.sinks > sq.first * UNIT ? 0 : sq.lo & ~31);
-            k1 = min(L, (sq.first + end - sq.sink) * UNIT);
-            if (f < sq.sink)
-                s1 = min(min(end, sq.sink) * UNIT, a.sinks);
-            if (end <= sq.sink)
-                k0 = k1 = s1;
-        } else {
-            k0 = max((sq.first + f) * UNIT, sq.lo & ~31);
-            k1 = min(L, (sq.first + end) * UNIT);
-        }
+        // keys [k0, k1) (KEYS_SINKS: of the numbered ones)
+        const int skip = KEYS == KEYS_SINKS ? 32 * sq.first : 0, first = KEYS == KEYS_SINKS ? 0 : sq.first;
+        const int k0 = max((first + f) * UNIT, KEYS == KEYS_SINKS ? 0 : sq.lo & ~31), k1 = min(L - skip, (first + end) * UNIT);
+        // the step at k: its first key
+        auto key_at = [&](int k) { return KEYS == KEYS_SINKS && k >= 32 * sq.sink ? k + skip : k; };
         const int32_t *__restrict__ table = a.table + (int64_t)b * a.table_stride;
 
         u32x4 kr[2][LD], vr[2][LD];
@@ -247,8 +304,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int page = clamp_page(uniform(pg[u]), a.cache.n_pages);
-                const int64_t at = (((int64_t)page * a.cache.hkv + head) << ps) + ((kb + 16 * u) & pm);
-                const uint8_t *kp = a.cache.k + at * D * ESZ, *vp = a.cache.v + at * D * ESZ;
+                const int64_t row = (((int64_t)page * a.cache.hkv + head) << ps) + ((kb + 16 * u) & pm);
+                const uint8_t *kp = a.cache.k + row * D * ESZ, *vp = a.cache.v + row * D * ESZ;
 #pragma unroll
                 for (int s = 0; s < LD; ++s)
                     kr[u][s] = *(const u32x4 *)(kp + (off + 64 * s));
@@ -256,21 +313,17 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                 for (int s = 0; s < LD; ++s)
                     vr[u][s] = *(const u32x4 *)(vp + (off + 64 * s));
                 if (FP8) {
-                    ks[u] = *(const f32x4 *)(a.cache.k_scale + at + 4 * g);
-                    vs[u] = *(const f32x4 *)(a.cache.v_scale + at + 4 * g);
+                    ks[u] = *(const f32x4 *)(a.cache.k_scale + row + 4 * g);
+                    vs[u] = *(const f32x4 *)(a.cache.v_scale + row + 4 * g);
                 }
             }
         };
-        // this wave's next step
-        auto after = [&](int kb) { return KEYS == KEYS_SINKS && kb < s1 && kb + STEP >= s1 ? k0 + w32 : kb + STEP; };
-        int kb = k0 + w32;
-        if (KEYS == KEYS_SINKS && f * UNIT + w32 < s1)
-            kb = f * UNIT + w32;
-        if (kb < k1) {
+        int at = k0 + w32, kb = key_at(at);     // this wave's step, and its first key
+        if (at < k1) {
             lookup(kb);
             load(kb);
-            if (after(kb) < k1)
-                lookup(after(kb));
+            if (at + STEP < k1)
+                lookup(key_at(at + STEP));
         }
 
         // Q as B operand: column = row of the sequence, 8 values a k-step (e4m3 K comes 16 values a lane: two
@@ -388,11 +441,10 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                     vss[u] = vs[u];
             }
             // the next step's loads
-            const int next = after(kb);
-            if (next < k1) {
-                load(next);
-                if (after(next) < k1)
-                    lookup(after(next));
+            if (at + STEP < k1) {
+                load(key_at(at + STEP));
+                if (at + 2 * STEP < k1)
+                    lookup(key_at(at + 2 * STEP));
             }
             u32x4 pf[PARTS][NQ];
 #pragma unroll
@@ -517,11 +569,11 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         };
         // steps that hold a key which some query of the sequence does not see: below `free` and from `full` on
         const int full = L - sq.n + 1 - 32, free = OWN ? sq.lo : a.window > 0 ? L - a.window : 0;
-        for (; kb < k1 && kb < free; kb = after(kb))
+        for (; at < k1 && kb < free; at += STEP, kb = key_at(at))
             step(std::true_type());
-        for (; kb < k1 && kb <= full; kb += STEP)
+        for (; at < k1 && kb <= full; at += STEP, kb = key_at(at))
             step(std::false_type());
-        for (; kb < k1; kb += STEP)
+        for (; at < k1; at += STEP, kb = key_at(at))
             step(std::true_type());
 
         const bool whole = f == 0 && end == sq.units;
@@ -634,7 +686,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         if (++h == a.hkv) {
             h = 0;
             do
-                sq = seq_units<KEYS>(a, ++b);
+                sq = listed ? list_at(++b) : seq_units<KEYS>(a, ++b);
             while (sq.units == 0);
         }
         if (!OWN)

@@ -99,6 +99,16 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, W
         w->key0 = __builtin_amdgcn_readlane(k0, src);
         w->L = max(__builtin_amdgcn_readlane(k1, src) - w->key0, 0);
     };
+    if (n_seqs <= 64 && (KEYS == KEYS_SINKS || KEYS == KEYS_SHARED)) {
+        // (alike, but for the first ones of a window: no search for the longest)
+        const int nb = load(lane), up = wave_prefix(nb);
+        w->total = __builtin_amdgcn_readlane(up, 63);
+        if (item >= w->total)
+            return false;
+        const int src = uniform(__ffsll((unsigned long long)ballot64(item < up)) - 1);
+        take(0, src, __builtin_amdgcn_readlane(up, src) - 1 - item);
+        return true;
+    }
     if (n_seqs <= 64) {
         const int nb = load(lane);
         // items of block numbers >= r
@@ -418,6 +428,21 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
                (a.window <= 0 || key > pos - a.window || (KEYS == KEYS_SINKS && key < a.sinks));
     };
     auto hide = [&](int t, f32x16 (&st)[2]) {
+        if (KEYS == KEYS_SINKS) {
+            // a lane's keys are 4 hh + a constant from a block's first one: its bounds are compared with the constants
+            const int last = a.causal ? min(pos, L - 1) : L - 1, lo = pos - a.window + 1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int from = block_key(4 * t + j) + 4 * hh;
+                const int c0 = lo - from, c1 = last - from, cs = 4 * t + j <= gs ? min(a.sinks, L) - from : -1000;
+#pragma unroll
+                for (int i = 8 * (j & 1); i < 8 * (j & 1) + 8; ++i) {
+                    const int c = 8 * (i / 4 % 2) + i % 4;
+                    st[j >> 1][i] = c <= c1 && (c >= c0 || c < cs) ? st[j >> 1][i] : -INFINITY;
+                }
+            }
+            return;
+        }
         int from[4];            // (first keys of the tile's blocks)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
