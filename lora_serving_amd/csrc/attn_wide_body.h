@@ -519,12 +519,41 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             for (int d = 0; d < DB; ++d)
                 o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d)), as_bf16x8(pf[s]), o[d], 0, 0, 0);
     };
+    // Keys of a tile with an infinity or NaN in V: each wave looks at its own rows before the barrier, a quarter of the reads that each
+    // looking at all of them takes (KEYS_PLAIN).  8 prompts of 2048,
+    // window 512, 4 first keys: @SCAN@)
+    constexpr bool SCAN = KEYS != KEYS_PLAIN;
+    uint16_t *const flags = (uint16_t *)(smem + wide_tiles<D, SRC, KG>) + 8 * kg;
+    auto scan = [&](int t) {
+        const uint8_t *const v = (const uint8_t *)(vl + (t & 1) * TILE + w16 * D) + 16 * lane;
+        uint32_t rows = 0;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {          // 64 / CPR rows at a time
+            const u32x4 w = *(const u32x4 *)(v + 1024 * j);
+            uint32_t x = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x = not_finite(x, w[i]);
+            const uint64_t hit = ballot64((x & 0x80008000u) != 0);
+            if (hit)
+#pragma unroll
+                for (int r = 0; r < 64 / CPR; ++r)
+                    rows |= (uint32_t)((hit >> (CPR * r) & ((UINT64_C(1) << CPR) - 1)) != 0) << (64 / CPR * j + r);
+        }
+        if (lane == 0)
+            flags[4 * (t & 1) + wave] = (uint16_t)rows;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+    auto flagged = [&](int t) {         // (keys of the tile, a bit each)
+        const u32x2 f = *(const u32x2 *)(flags + 4 * (t & 1));
+        return (uint64_t)(uint32_t)uniform((int)f[1]) << 32 | (uint32_t)uniform((int)f[0]);
+    };
     // Scores of tile t + 1 (into nx), powers of tile t (from st) and its outputs, in steps of two products: the
     // fragments are read AHEAD steps before their use, the powers of a step's keys come before it, and the next
     // tile's largest score after its last; the fences keep the compiler to that order.  Copies of rows are issued
     // between the first products (10000 tokens of one head: 115 us against 123), those of pages, whose
     // addresses take longer, before them (2048 tokens over 8192: 232 us against 239).
-    auto body = [&](int t, const f32x16 (&st)[2], f32x16 (&nx)[2]) __attribute__((always_inline)) {
+    auto body = [&](int t, const f32x16 (&st)[2], f32x16 (&nx)[2], auto next_edge) __attribute__((always_inline)) {
         constexpr int N = KS + 2 * DB, AHEAD = FP8 ? 2 : 4;     // (e4m3: as the registers allow)
         if (SRC != AW_ROWS)
             issue(t + 1);
@@ -565,7 +594,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     scaled(t + 1, i - (N - 2), j, nx);
-                mx = largest(nx[i - (N - 2)], 0, 16, mx);
+                if (!next_edge)
+                    mx = largest(nx[i - (N - 2)], 0, 16, mx);
             }
             __builtin_amdgcn_sched_barrier(0);
             if (SRC == AW_ROWS && i == 0)
@@ -575,41 +605,22 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             if (SRC == AW_ROWS && (i == 0 || i == KS / 2))
                 __builtin_amdgcn_sched_barrier(0);
         }
+        if (next_edge) {
+            hide(t + 1, nx);
+            mx = largest(nx[1], 0, 16, largest(nx[0], 0, 16, mx));
+        }
         raise(mx);
         land(t + 1);
+        if (next_edge)
+            scan(t + 1);
         phase_end();
     };
     // the same for a tile that some rows see in part: V may hold an infinity or NaN where a row must not see it
     // (0 x NaN is NaN); then one key at a time, kept only by the rows that see it
-    // (but for KEYS_PLAIN each wave has looked at its own rows before the barrier: a quarter of the reads.  8 prompts of 2048,
-    // window 512, 4 first keys: @SCAN@)
-    constexpr bool SCAN = KEYS != KEYS_PLAIN;
-    uint16_t *const flags = (uint16_t *)(smem + wide_tiles<D, SRC, KG>) + 8 * kg;
-    auto scan = [&](int t) {
-        const uint8_t *const v = (const uint8_t *)(vl + (t & 1) * TILE + w16 * D) + 16 * lane;
-        uint32_t rows = 0;
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) {          // 64 / CPR rows at a time
-            const u32x4 w = *(const u32x4 *)(v + 1024 * j);
-            uint32_t x = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                x = not_finite(x, w[i]);
-            const uint64_t hit = ballot64((x & 0x80008000u) != 0);
-            if (hit)
-#pragma unroll
-                for (int r = 0; r < 64 / CPR; ++r)
-                    rows |= (uint32_t)((hit >> (CPR * r) & ((UINT64_C(1) << CPR) - 1)) != 0) << (64 / CPR * j + r);
-        }
-        if (lane == 0)
-            flags[4 * (t & 1) + wave] = (uint16_t)rows;
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    };
     auto outputs_edge = [&](int t) {
         uint64_t found = 0;
         if (SCAN) {
-            const u32x2 f = *(const u32x2 *)(flags + 4 * (t & 1));
-            const uint64_t rows = (uint64_t)(uint32_t)uniform((int)f[1]) << 32 | (uint32_t)uniform((int)f[0]);
+            const uint64_t rows = flagged(t);
             if (rows == 0) {
                 outputs(t);
                 return;
@@ -721,6 +732,9 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             phase_end();
         }
     }
+    // KEYS_SINKS: of a window's few tiles the one after those that all rows see is in the loop too (@EDGES@; e4m3 would
+    // spill 11 registers, and the tile before them 60)
+    constexpr bool LAST = KEYS == KEYS_SINKS && !FP8;
     const int lead = f0 < f1 ? f0 : t1;
     for (; t < lead; ++t)
         single(t);
@@ -734,17 +748,24 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
         land(t);
         phase_end();
         for (; t + 2 < f1; t += 2) {
-            body(t, sa, sb);
-            body(t + 1, sb, sa);
+            body(t, sa, sb, std::false_type());
+            body(t + 1, sb, sa, std::false_type());
         }
         if (t + 1 < f1) {
-            body(t, sa, sb);
+            body(t, sa, sb, std::false_type());
             sa[0] = sb[0];
             sa[1] = sb[1];
             ++t;
         }
-        all_powers(t, sa, std::false_type());
-        outputs(t);
+        if (LAST && t + 1 < t1) {
+            body(t, sa, sb, std::integral_constant<bool, LAST>());
+            ++t;
+            all_powers(t, sb, std::true_type());
+            outputs_edge(t);
+        } else {
+            all_powers(t, sa, std::false_type());
+            outputs(t);
+        }
         for (++t; t < t1; ++t)
             single(t);
     }
