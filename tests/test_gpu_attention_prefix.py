@@ -165,6 +165,21 @@ def test_groups(m, case):
     b.check(out, causal, lse)
 
 
+MANY = [
+    # more sequences and groups than a workgroup lists at a time
+    ([after(40 + i, (1, 1 + i % 7), (1, 2), (2, 5)) for i in range(120)], [(1, 30)], 4, 2, 64, 16, True, True),
+    ([after(90, *[(1, 1 + i % 9) for i in range(300)])], [], 4, 1, 128, 16, False, True),
+    ([after(90, *[(1, 1 + i % 9) for i in range(255)]), after(33, (1, 2), (1, 40))], [], 2, 2, 64, 32, False, True),
+    ([after(256, *[(1, 1 + i % 9) for i in range(100)] + [(70, 100)] + [(1, 1 + i % 9) for i in range(100)])], [], 8, 2, 64, 16,
+     True, True),                                                                     # rows of one that shares nothing between
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-40:])
+def test_many_sequences(m, case):
+    test_groups(m, case)
+
+
 @pytest.mark.parametrize("seed", range(40))
 def test_random_groups(m, seed):
     r = random.Random(seed)
@@ -250,6 +265,31 @@ def test_bad_values_reach_only_who_sees_them(m, d, fp8):
         assert seen.any()
         assert torch.equal(good[~seen], got[~seen])
         assert got[seen].isnan().any(-1).all()
+
+
+def test_pages_past_32_bits(m):
+    """Pages whose bytes lie past 4 GiB from the start of the cache, in both operators; a workspace that starts anywhere."""
+    hkv, page, d, pages = 8, 64, 128, 40000                       # 2.6 billion values, 5.2 GB each of K and V
+    b = Batch(m, gen(6), [after(150, (1, 4), (1, 90), (5, 20))], 16, hkv, d, page, False)
+    k, v = [torch.empty(pages, hkv, page, d, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    n = b.cache.n_pages
+    k[pages - n:], v[pages - n:] = b.cache.k, b.cache.v
+    table = torch.where(b.table < n, b.table + (pages - n), b.table).cuda()
+    cache = m.Cache(k, v)
+    ws = b.workspace()[8:]
+    out = torch.empty(b.T, 16, d, device="cuda", dtype=torch.bfloat16)
+    m.mlora_prefix_attention(**{**b.args(), "cache": cache, "page_table": table}, out=out, ws=ws)
+    torch.cuda.synchronize()
+    b.check(out)
+    a = b.args()
+    outs = []
+    for c, t in ((b.cache, b.table.cuda()), (cache, table)):
+        o = torch.empty_like(out)
+        m.mlora_paged_attention(a["q"], c, t, a["cu_q"], a["kv_len"], o, b.mq, b.mk, window=40, sinks=3,
+                                ws=m.paged_workspace(b.T, 3, 16, hkv, d, b.mq, b.mk))
+        outs.append(o)
+    torch.cuda.synchronize()
+    assert torch.equal(*outs)
 
 
 def test_strided_rows_and_scale(m):
