@@ -489,9 +489,13 @@ mlora_status mlora_validate_pages_sinks(const mlora_cache *cache, const int32_t 
  *   max_prefix  host upper bound of prefix_len
  * page_table and kv_len are mlora_paged_attention's, with all tokens of every sequence; a sequence whose queries do not
  * all see the whole prefix (kv_len less its queries, if causal, is below prefix_len) is answered from its own pages.  A group's first
- * sequence must hold the whole prefix.  Probabilities of shared keys are rounded to bf16 for the product with V.
+ * sequence must hold the whole prefix.  Probabilities of shared keys are rounded to bf16 for the product with V.  Sequences of more
+ * than 256 rows (queries x heads of a kv head's group) read the prefix for themselves, for they fill the matrix cores without others.
+ * Where less than about 32 MB of keys and values need not be read again (sequences x shared tokens), mlora_paged_attention is faster,
+ * by 5 us at the most.
  *   ws  mlora_prefix_workspace_size() bytes for the same sizes, or for larger ones of the same heads; the size
- *       never falls as any of them rises (0 where the call would refuse them)
+ *       never falls as any of them rises (0 where the call would refuse them).  It holds fp32 parts of every row, at least
+ *       2 T n_q_heads (4 head_dim + 8) bytes
  * mlora_validate_prefixes checks the groups on the host (all pointers host): group_start, 0 <= prefix_len <= max_prefix,
  * and that the table and each first sequence's kv_len reach that far; MLORA_ERR_SHAPE and the value where not.
  */

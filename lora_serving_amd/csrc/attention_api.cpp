@@ -263,10 +263,15 @@ PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t hq, 
     if (getenv("PX_N")) n = std::min<int64_t>(atoi(getenv("PX_N")), most_prefix_cuts(items, max_prefix));
     p.chunk = ((max_prefix + n - 1) / n + 63) & ~INT64_C(63);
     p.chunks = (max_prefix + p.chunk - 1) / p.chunk;
-    // the card holds 512 workgroups: those of the shares start beside the others' (one of each on a CU at the most)
+    // The card holds 512 workgroups: those of the shares start beside the others', one of which a CU has at the most.  Where a
+    // sequence may have more than 1536 keys of its own, they outlast the others, and as many on every CU are faster than a second
+    // one on some (128 tokens behind 4000 keys, 500 to 3000 of their own: 384 209 us, 256 182; 64 behind 4096, 1 to 1024: 384 39,
+    // 256 45).
     const int64_t beside = std::min(shared * p.chunks, CUS);
-    p.own.shares = p.own.dec_rows > 0 ? (int)std::min(own_workgroups(n_seqs, hkv, max_kv), 2 * CUS - beside) : 0;
-    if (getenv("PX_W") && p.own.dec_rows) p.own.shares = std::min<int64_t>(own_workgroups(n_seqs, hkv, max_kv),atoi(getenv("PX_W")));
+    int64_t groups = 2 * CUS - beside;
+    if (max_kv - max_prefix > 1536)
+        groups = beside < CUS / 2 ? 2 * CUS : CUS;
+    p.own.shares = p.own.dec_rows > 0 ? (int)std::min(own_workgroups(n_seqs, hkv, max_kv), groups) : 0;
     p.share_slots = 2 * 4 * (int64_t)p.own.shares * p.own.dec_rows;
     if (p.own.wide) {
         const int64_t keys = std::max<int64_t>(max_kv, 1);

@@ -12,6 +12,9 @@
 // one's softmax and second product run.  Bound by HBM (or, for a short batch, by latency).  Measured
 // (D = 128, 32 heads on 8, with the join): 64 contexts of 1 to 8192 225 to 232 us (5.6 to 5.7 TB/s), 64 of
 // 4096 184 to 187 us (5.8), 256 of an e4m3 cache 231 us (5.1), one of 1003 10.5 us (7 the shares, 4 the join).
+// With a window and first keys (KEYS_SINKS): 64 contexts of 1 to 16384, window 2048, 105 us (5.0), 256 of an e4m3 cache, window
+// 1024, 124 us (4.3: the 33 blocks of a sequence are 9 steps of four waves, the last for one of them); two steps' loads in flight
+// were slower (130), three workgroups a CU too (199, 43 registers spilled).
 // With two column tiles of D = 128 27 registers (e4m3: 15) are spilled, outside the loop over keys: 32 x 8 tokens
 // over 4096 keys 137 us (3.9 TB/s), of an e4m3 cache 69 to 71 us (3.9).
 #pragma once
@@ -165,10 +168,10 @@ constexpr int decode_lds = KEYS == KEYS_OWN ? 4 * 2 * 32 * D + (NQ > 1 ? 4 * 16 
                                                   (NQ > 1 ? 16 * NQ * D * 2 : 0);
 
 // Share `share` of `shares` (or sequence and head `share`, see launch_attn_decode); smem: decode_lds bytes.
-// KEYS_OWN: shares are not a workgroup's but a wave's (of `share` this one has number 4 share + wave, of 4 shares), and a
-// wave leaves its parts to the join by itself: no barrier, so that the start of one wave's sequence, a chain of loads,
-// hides behind the others' keys.  What comes after a shared prefix is short, and a workgroup's waves, starting each together,
-// waited for it together (256 of an e4m3 cache behind four prefixes, 1 to 700 keys each: @OWN@).
+// KEYS_OWN: shares are not a workgroup's but a wave's (4 share + wave of 4 shares), and a wave leaves its parts to the join by
+// itself: no barrier, so that the start of one wave's sequence, a chain of loads, hides behind the others' keys.  What comes after a
+// shared prefix is short, and the waves of a workgroup waited for each start together (256 of an e4m3 cache behind four
+// prefixes, 1 to 700 keys each: the kernel 97 us, with this and fewer chunks of the prefixes 77).
 template <int D, int NQ, bool FP8, int KEYS = KEYS_PLAIN>
 __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t share, uint32_t shares, uint8_t *smem)
 {
@@ -196,8 +199,9 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
     const int ps = a.cache.ps, pm = (1 << ps) - 1;
     uint16_t *vl = lds + wave * VW;
 
-    // KEYS_OWN: up to OWN_SEQS sequences are listed in LDS, 64 a wave, from loads that do not wait for each other: a chain
-    // of them for each of a lane's sequences, its group searched for, took @LIST@
+    // KEYS_OWN: up to OWN_SEQS sequences are listed in LDS, 64 a wave, from loads that do not wait for each other, instead of a
+    // chain of them for each of a lane's sequences, whose group is searched for (256 of an e4m3 cache, four groups: a call 84 us,
+    // listed 80)
     const bool listed = OWN && a.n_seqs <= OWN_SEQS && a.n_groups <= 64;
     u32x4 *const list = (u32x4 *)(smem + decode_lds<D, NQ, KEYS> - OWN_SEQS * 5 * 4);      // q0, n, L, lo
     int *const list_of = (int *)(list + OWN_SEQS);                                          // units

@@ -16,7 +16,9 @@
 // (D = 128, 32 heads on 8): 8 prompts of 2048 308 to 317 us (870 to 890 TFLOP/s), one of 16384 1.91 to 1.97 ms
 // (1120 to 1150), 2048 tokens over 8192 keys in bf16 pages 228 to 234 us (1030 to 1050), in e4m3 pages 273 to
 // 282 us (850 to 880: conversions and scales take the issue), D = 64 148 to 153 us (780 to 810: the same
-// exponentials for half the products).
+// exponentials for half the products).  With a window and first keys (KEYS_SINKS): one of 16384, window 4096, 888 us (1090),
+// 8 of 2048, window 512, 180 us (670: of a workgroup's 46 thousand cycles 10 go by until its first tile is there, 8 in the tile
+// before those that all rows see, 26 in those 8, 3 at the end).
 #pragma once
 
 #include <type_traits>
@@ -165,8 +167,8 @@ constexpr int wide_lds = wide_tiles<D, SRC, KG> + (KEYS == KEYS_PLAIN ? 0 : KG *
 // for several items.)
 // KEYS_SINKS: tiles are made of blocks of 16 keys, as many as a wave copies; those of the first keys and of the window are
 // numbered through, without the blocks that no row of the workgroup sees between them, so that a few first keys cost a
-// quarter of a tile and the window's begins in the same one (8 prompts of 2048, window 512, 4 first keys: @SINK16@).  Chunks
-// are equal pieces of the tiles.
+// quarter of a tile and the window's begins in the same one (8 prompts of 2048, window 512, 4 first keys: 230 us with whole tiles
+// of first keys, 193 with this and the look at V below).  Chunks are equal pieces of the tiles.
 template <int D, int SRC, int KG, bool MORE = false, int KEYS = KEYS_PLAIN>
 __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by, uint8_t *smem)
 {
@@ -519,9 +521,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             for (int d = 0; d < DB; ++d)
                 o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d)), as_bf16x8(pf[s]), o[d], 0, 0, 0);
     };
-    // Keys of a tile with an infinity or NaN in V: each wave looks at its own rows before the barrier, a quarter of the reads that each
-    // looking at all of them takes (KEYS_PLAIN).  8 prompts of 2048,
-    // window 512, 4 first keys: @SCAN@)
+    // Keys of a tile with an infinity or NaN in V: each wave looks at its own rows before the barrier, a quarter of the reads that it
+    // takes for each to look at all of them (KEYS_PLAIN)
     constexpr bool SCAN = KEYS != KEYS_PLAIN;
     uint16_t *const flags = (uint16_t *)(smem + wide_tiles<D, SRC, KG>) + 8 * kg;
     auto scan = [&](int t) {
@@ -732,8 +733,9 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             phase_end();
         }
     }
-    // KEYS_SINKS: of a window's few tiles the one after those that all rows see is in the loop too (@EDGES@; e4m3 would
-    // spill 11 registers, and the tile before them 60)
+    // KEYS_SINKS: of a window's few tiles the one after those that all rows see is in the loop too (8 prompts of 2048, window 512:
+    // 183 us, so 180; one of 16384, window 4096: 900, so 888; e4m3 would spill 11 registers; with the one before them as well,
+    // looked at ahead of the loop, 188 and 916)
     constexpr bool LAST = KEYS == KEYS_SINKS && !FP8;
     const int lead = f0 < f1 ? f0 : t1;
     for (; t < lead; ++t)
