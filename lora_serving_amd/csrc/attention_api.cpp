@@ -136,7 +136,8 @@ PagedPlan paged_plan(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t
     const int64_t group = hq / hkv, most = max_q * group;
     max_kv = std::max<int64_t>(max_kv, 1);
     const auto seen = [&](int64_t queries) {
-        return sinks > 0 ? std::min(max_kv, window + queries + (sinks + DECODE_UNIT) / DECODE_UNIT * DECODE_UNIT + DECODE_UNIT) : max_kv;
+        const int64_t first = (sinks + DECODE_UNIT) / DECODE_UNIT * DECODE_UNIT;
+        return sinks > 0 ? std::min(max_kv, window + queries + first + DECODE_UNIT) : max_kv;
     };
     if (most <= 32) {
         p.dec_rows = most;
@@ -216,7 +217,8 @@ int64_t prefix_cuts(int64_t items, int64_t keys, int64_t limit, bool whole)
     double least = 0.;
     for (int64_t n = 1; n <= limit && (n == 1 || n * items <= 8 * CUS); ++n) {
         const int64_t groups = items * n, each = (tiles + n - 1) / n;
-        const double us = (groups <= CUS ? 1.2 * each : 1.95 * each * ((groups + 2 * CUS - 1) / (2 * CUS))) + (whole && n == 1 ? 0. : 0.08 * groups);
+        const double tile_us = groups <= CUS ? 1.2 : 1.95 * ((groups + 2 * CUS - 1) / (2 * CUS));
+        const double us = tile_us * each + (whole && n == 1 ? 0. : 0.08 * groups);
         if (n == 1 || us < least) {
             best = n;
             least = us;
@@ -248,14 +250,15 @@ int64_t own_workgroups(int32_t n_seqs, int32_t hkv, int64_t max_kv)
     return std::min(((int64_t)n_seqs * hkv * units + 3) / 4, 2 * CUS);
 }
 
-PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t hq, int32_t hkv, int32_t d, int64_t max_q, int64_t max_kv,
-                       int64_t max_prefix)
+PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t hq, int32_t hkv, int32_t d, int64_t max_q,
+                       int64_t max_kv, int64_t max_prefix)
 {
     PrefixPlan p;
     p.own = paged_plan(T, n_seqs, hq, hkv, d, max_q, max_kv, 0, 0);
     // The rows of sequences that share nothing, if those of more than one token are alike, and the others'.
     const int64_t group = hq / hkv, all = T * group, items = (all + WIDE_ROWS - 1) / WIDE_ROWS * hkv;
-    const int64_t alone = max_q * group > ALONE_ROWS ? std::min(T, std::max<int64_t>(T - n_seqs, 0) / std::max<int64_t>(max_q - 1, 1) * max_q) * group : 0;
+    const int64_t chunks = std::max<int64_t>(T - n_seqs, 0) / std::max<int64_t>(max_q - 1, 1);
+    const int64_t alone = max_q * group > ALONE_ROWS ? std::min(T, chunks * max_q) * group : 0;
     const auto blocks = [&](int64_t rows) { return std::max<int64_t>(1, (rows + WIDE_ROWS - 1) / WIDE_ROWS) * hkv; };
     // (half of the groups' last row blocks are taken to be more)
     const int64_t shared = blocks(all - alone) + std::min<int64_t>(n_groups / 2, T) * hkv;

@@ -49,7 +49,8 @@ __device__ __forceinline__ SeqUnits seq_units(const AttnArgs &a, int b, Shared s
     s.first = KEYS == KEYS_SINKS ? s.lo / 32 - s.sink : s.lo / UNIT;
     const int64_t rows = (int64_t)s.n * a.group;
     const bool mine = s.n > 0 && s.n <= a.max_q && rows >= a.min_rows && rows <= a.max_rows;
-    const int units = KEYS == KEYS_SINKS ? ((s.L + 31) / 32 - s.first + UNIT / 32 - 1) / (UNIT / 32) : (s.L + UNIT - 1) / UNIT - s.first;
+    const int units = KEYS == KEYS_SINKS ? ((s.L + 31) / 32 - s.first + UNIT / 32 - 1) / (UNIT / 32)
+                                         : (s.L + UNIT - 1) / UNIT - s.first;
     s.units = mine ? max(1, units) : 0;
     return s;
 }
@@ -168,10 +169,10 @@ constexpr int decode_lds = KEYS == KEYS_OWN ? 4 * 2 * 32 * D + (NQ > 1 ? 4 * 16 
                                                   (NQ > 1 ? 16 * NQ * D * 2 : 0);
 
 // Share `share` of `shares` (or sequence and head `share`, see launch_attn_decode); smem: decode_lds bytes.
-// KEYS_OWN: shares are not a workgroup's but a wave's (4 share + wave of 4 shares), and a wave leaves its parts to the join by
-// itself: no barrier, so that the start of one wave's sequence, a chain of loads, hides behind the others' keys.  What comes after a
-// shared prefix is short, and the waves of a workgroup waited for each start together (256 of an e4m3 cache behind four
-// prefixes, 1 to 700 keys each: the kernel 97 us, with this and fewer chunks of the prefixes 77).
+// KEYS_OWN: shares are not a workgroup's but a wave's (4 share + wave of 4 shares), and a wave leaves its parts to the join
+// by itself: no barrier, so that the start of one wave's sequence, a chain of loads, hides behind the others' keys.  What
+// comes after a shared prefix is short, and the waves of a workgroup waited for each start together (256 of an e4m3 cache
+// behind four prefixes, 1 to 700 keys each: the kernel 97 us, with this and fewer chunks of the prefixes 77).
 template <int D, int NQ, bool FP8, int KEYS = KEYS_PLAIN>
 __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t share, uint32_t shares, uint8_t *smem)
 {
@@ -270,7 +271,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
         const LaneUnits u = listed ? list_units() : lane_units<KEYS>(a, lane);
         // (OWN: half of what a sequence and head has in the mean, up to four units, at the least, for each part is one more
         // for the join)
-        const uint32_t all = (uint32_t)u.total * a.hkv, least = OWN ? min(max(all / (2 * (uint32_t)(a.n_seqs * a.hkv)), 1u), 4u) : 1;
+        const uint32_t all = (uint32_t)u.total * a.hkv;
+        const uint32_t least = OWN ? min(max(all / (2 * (uint32_t)(a.n_seqs * a.hkv)), 1u), 4u) : 1;
         cut = Shares(all, OWN ? min(4 * shares, (all + least - 1) / least) : shares);
         if (share >= cut.n)
             return;
@@ -283,6 +285,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
     const float cs = a.scale * ATTN_LOG2E;
     const int last = (int)a.table_stride - 1;
 
+    // KEYS_OWN: the pages of a sequence's first step, for its next head starts there again
+    int pgf[2], seen = -1;
     while (left > 0) {
         const int end = min(sq.units, f + left);
         const int rows = sq.n * a.group, L = sq.L, head = turned_head(a, b, h);
@@ -323,8 +327,19 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
             }
         };
         int at = k0 + w32, kb = key_at(at);     // this wave's step, and its first key
+        if (OWN && b != seen) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+                pgf[u] = table[min(((sq.lo & ~31) + 16 * u) >> ps, last)];
+            seen = b;
+        }
         if (at < k1) {
-            lookup(kb);
+            if (OWN && f == 0) {
+                pg[0] = pgf[0];
+                pg[1] = pgf[1];
+            } else {
+                lookup(kb);
+            }
             load(kb);
             if (at + STEP < k1)
                 lookup(key_at(at + STEP));

@@ -5,9 +5,9 @@
 // The shared part is the wide kernel's (attn_wide_body.h: the group as one sequence of queries that see every key),
 // cut into chunks of keys; the own part is the mixed batch's (attn_mixed.hip).  All of them in one launch, for the former
 // is bound by the matrix cores and the latter by memory.  Measured (D = 128, 32 heads on 8, both kernels): 64 tokens behind 4096
-// keys, 1 to 1024 of their own, 47 us (3.3 TB/s of what has to be read), 256 of an e4m3 cache in four groups 80 us (2.8), 32 x 5 of
-// D = 64 behind 8192 and 6001 24 us, 128 tokens and a chunk of 1024 behind 8000 213 us (750 TFLOP/s), 8 tokens behind 1000 keys 14 us;
-// replayed in a graph 40, 75, 26, 237 and 14 us, where mlora_paged_attention takes 153, 193, 49, 592 and 17.  Bound by the own
+// keys, 1 to 1024 of their own, 47 us (3.3 TB/s of what has to be read), 256 of an e4m3 cache in four groups 80 us (2.8), 32 x 5
+// of D = 64 behind 8192 and 6001 24 us, 128 tokens and a chunk of 1024 behind 8000 211 to 213 us (750 TFLOP/s), 8 tokens behind
+// 1000 keys 14 us; replayed in a graph 40, 75, 26, 237 and 14 us, where mlora_paged_attention takes 153, 193, 49, 592 and 17.  Bound by the own
 // keys' reads and, as long as both run, by what the two kinds cost each other; the join is 4 to 11 us.
 #include "attn_decode_body.h"
 #include "attn_mixed.h"
@@ -147,8 +147,9 @@ __global__ __launch_bounds__(256) void attn_prefix_join_kernel(AttnArgs s, AttnA
         const int hi = w.causal ? min(L, L - n + t - q0 + 1) : L, from = keys & ~(AW_BN - 1);
         const int own = hi > keys ? (hi - 1 - from) / w.chunk + 1 : 1;
         for (int hd = h0 + lane / LPR; hd < end; hd += 64 / LPR)
-            join_row<D>(d, chunks + own, [&](int i) { return i < chunks ? row_slot(s, t, hd, i) : row_slot(w, t, hd, i - chunks); },
-                        t, hd, l);
+            join_row<D>(d, chunks + own, [&](int i) {
+                return i < chunks ? row_slot(s, t, hd, i) : row_slot(w, t, hd, i - chunks);
+            }, t, hd, l);
     }
 }
 
@@ -162,7 +163,8 @@ hipError_t launch_attn_prefix(const AttnArgs &s, const AttnArgs &w, const AttnAr
     if (blocks > 0x7fffffff)
         return hipErrorInvalidValue;
     const dim3 grid((unsigned)blocks);
-#define PRE(D, NQ, F, W) attn_prefix_kernel<D, NQ, F, W><<<grid, dim3(256), 0, stream>>>(s, w, d, (uint32_t)shared_x, (uint32_t)wide_x, (uint32_t)shares)
+    const uint32_t x[3] = {(uint32_t)shared_x, (uint32_t)wide_x, (uint32_t)shares};
+#define PRE(D, NQ, F, W) attn_prefix_kernel<D, NQ, F, W><<<grid, dim3(256), 0, stream>>>(s, w, d, x[0], x[1], x[2])
 #define PRE_W(D, F) (wide ? PRE(D, 1, F, true) : nq == 1 ? PRE(D, 1, F, false) : PRE(D, 2, F, false))
 #define PRE_F(D) (d.cache.fp8 ? PRE_W(D, true) : PRE_W(D, false))
     head_dim == 64 ? PRE_F(64) : PRE_F(128);

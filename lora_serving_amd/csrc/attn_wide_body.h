@@ -159,7 +159,8 @@ __device__ __forceinline__ bool aw_item(const AttnArgs &a, int item, int lane, W
 
 // tiles, scales, the join of halves, and (but for KEYS_PLAIN) which keys of two tiles hold an infinity or NaN in V
 template <int D, int SRC, int KG>
-constexpr int wide_tiles = KG * 4 * AW_BN * D * 2 + (SRC == AW_PAGES_E4M3 ? 4 * 2 * AW_BN * 4 : 0) + (KG > 1 ? 4 * 64 * 2 * 4 : 0);
+constexpr int wide_tiles = KG * 4 * AW_BN * D * 2 + (SRC == AW_PAGES_E4M3 ? 4 * 2 * AW_BN * 4 : 0) +
+                           (KG > 1 ? 4 * 64 * 2 * 4 : 0);
 template <int D, int SRC, int KG, int KEYS = KEYS_PLAIN>
 constexpr int wide_lds = wide_tiles<D, SRC, KG> + (KEYS == KEYS_PLAIN ? 0 : KG * 2 * 4 * 2);
 
@@ -216,7 +217,9 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
     const int row = rb * BM + wave * 32 + col;
     const int ri = min(row, rows - 1) / a.group, hd = h * a.group + min(row, rows - 1) - ri * a.group;
     const int pos = L - n + ri;
-    auto first_key = [&](int r) { return KEYS == KEYS_OWN ? own : a.window > 0 ? max(0, L - n + min(r, rows - 1) / a.group - a.window + 1) : 0; };
+    auto first_key = [&](int r) {
+        return KEYS == KEYS_OWN ? own : a.window > 0 ? max(0, L - n + min(r, rows - 1) / a.group - a.window + 1) : 0;
+    };
     auto end_key = [&](int r) { return KEYS != KEYS_SHARED && a.causal ? min(L, L - n + min(r, rows - 1) / a.group + 1) : L; };
     const int c0 = KEYS == KEYS_SINKS ? 0 : (own & ~(BN - 1)) + by * a.chunk;
     const int kmin = max(first_key(rb * BM), c0);
@@ -303,7 +306,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             } else {
 #pragma unroll
                 for (int i = 0; i < IPW; ++i)
-                    aw_dma(base, (uint32_t)min(RPI * i + crow, L - 1 - from) * (uint32_t)(2 * stride) + piece[i], to, RPI * i * D * 2);
+                    aw_dma(base, (uint32_t)min(RPI * i + crow, L - 1 - from) * (uint32_t)(2 * stride) + piece[i], to,
+                           RPI * i * D * 2);
             }
         } else if (SRC == AW_ROWS) {
             if (t * BN + BN <= L) {
@@ -521,8 +525,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             for (int d = 0; d < DB; ++d)
                 o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d)), as_bf16x8(pf[s]), o[d], 0, 0, 0);
     };
-    // Keys of a tile with an infinity or NaN in V: each wave looks at its own rows before the barrier, a quarter of the reads that it
-    // takes for each to look at all of them (KEYS_PLAIN)
+    // Keys of a tile with an infinity or NaN in V: each wave looks at its own rows before the barrier, a quarter of the reads
+    // that it takes for each to look at all of them (KEYS_PLAIN)
     constexpr bool SCAN = KEYS != KEYS_PLAIN;
     uint16_t *const flags = (uint16_t *)(smem + wide_tiles<D, SRC, KG>) + 8 * kg;
     auto scan = [&](int t) {
@@ -654,8 +658,8 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1)
                 bad |= __shfl_xor(bad, off, 64);
-        const uint64_t some = SCAN ? found
-                                   : ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)bad, 32) << 32) | (uint32_t)uniform((int)bad);
+        const uint64_t all = ((uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)bad, 32) << 32) | (uint32_t)uniform((int)bad);
+        const uint64_t some = SCAN ? found : all;
         for (uint64_t rest = some; rest; rest &= rest - 1) {
             const int bit = __ffsll((unsigned long long)rest) - 1, s = (bit & 31) >> 3, e = bit & 7;
             const bool see = sees(block_key(4 * t + s) + 8 * (e >> 2) + 4 * (bit >> 5) + (e & 3));
@@ -733,9 +737,9 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             phase_end();
         }
     }
-    // KEYS_SINKS: of a window's few tiles the one after those that all rows see is in the loop too (8 prompts of 2048, window 512:
-    // 183 us, so 180; one of 16384, window 4096: 900, so 888; e4m3 would spill 11 registers; with the one before them as well,
-    // looked at ahead of the loop, 188 and 916)
+    // KEYS_SINKS: of a window's few tiles the one after those that all rows see is in the loop too (8 prompts of 2048, window
+    // 512: 183 us, so 180; one of 16384, window 4096: 900, so 888; e4m3 would spill 11 registers; with the one before them as
+    // well, looked at ahead of the loop, 188 and 916)
     constexpr bool LAST = KEYS == KEYS_SINKS && !FP8;
     const int lead = f0 < f1 ? f0 : t1;
     for (; t < lead; ++t)
