@@ -489,10 +489,10 @@ mlora_status mlora_validate_pages_sinks(const mlora_cache *cache, const int32_t 
  *   max_prefix  host upper bound of prefix_len
  * page_table and kv_len are mlora_paged_attention's, with all tokens of every sequence; a sequence whose queries do not
  * all see the whole prefix (kv_len less its queries, if causal, is below prefix_len) is answered from its own pages.
- * A group's first sequence must hold the whole prefix.  Probabilities of shared keys are rounded to bf16 for the product
- * with V.  Sequences of more than 256 rows (queries x heads of a kv head's group) read the prefix for themselves, for
- * they fill the matrix cores without others.  Where less than about 32 MB of keys and values need not be read again
- * (sequences x shared tokens), mlora_paged_attention is faster, by 4 to 6 us.
+ * A group's first sequence must hold the whole prefix.  Probabilities of shared keys keep 2^-15.  Sequences of more than
+ * 256 rows (queries x heads of a kv head's group) read the prefix for themselves, for they fill the matrix cores without
+ * others, and with a chunk's precision.  Where less than about 32 MB of keys and values need not be read again (sequences x
+ * shared tokens), mlora_paged_attention is faster, by 4 to 6 us.
  *   ws  mlora_prefix_workspace_size() bytes for the same sizes, or for larger ones of the same heads; the size
  *       never falls as any of them rises (0 where the call would refuse them).  It holds fp32 parts of every row, at least
  *       2 T n_q_heads (4 head_dim + 8) bytes

@@ -208,9 +208,9 @@ size_t paged_room(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int32_t d,
 constexpr int32_t ALONE_ROWS = 256;
 
 // Chunks of keys for `items` row blocks of `keys` keys at the most, up to `limit`, in us: a tile takes 1.2 in a workgroup alone
-// on its CU and 1.95 in two, in rounds of 512, and a part of 128 rows 0.08 to write and to read again (whole: one chunk leaves
-// none).
-int64_t prefix_cuts(int64_t items, int64_t keys, int64_t limit, bool whole)
+// on its CU and 1.95 in two, in rounds of 512, and a part of 128 rows 0.08 to write and to read again.  shared: probabilities
+// are two bf16 parts there, a quarter more a tile, and one chunk leaves a part, too.
+int64_t prefix_cuts(int64_t items, int64_t keys, int64_t limit, bool shared)
 {
     const int64_t tiles = (keys + 63) / 64;
     int64_t best = 1;
@@ -218,7 +218,7 @@ int64_t prefix_cuts(int64_t items, int64_t keys, int64_t limit, bool whole)
     for (int64_t n = 1; n <= limit && (n == 1 || n * items <= 8 * CUS); ++n) {
         const int64_t groups = items * n, each = (tiles + n - 1) / n;
         const double tile_us = groups <= CUS ? 1.2 : 1.95 * ((groups + 2 * CUS - 1) / (2 * CUS));
-        const double us = tile_us * each + (whole && n == 1 ? 0. : 0.08 * groups);
+        const double us = tile_us * each * (shared ? 1.25 : 1.) + (shared || n > 1 ? 0.08 * groups : 0.);
         if (n == 1 || us < least) {
             best = n;
             least = us;
@@ -262,7 +262,7 @@ PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t hq, 
     const auto blocks = [&](int64_t rows) { return std::max<int64_t>(1, (rows + WIDE_ROWS - 1) / WIDE_ROWS) * hkv; };
     // (half of the groups' last row blocks are taken to be more)
     const int64_t shared = blocks(all - alone) + std::min<int64_t>(n_groups / 2, T) * hkv;
-    int64_t n = prefix_cuts(shared, max_prefix, most_prefix_cuts(items, max_prefix), false);
+    int64_t n = prefix_cuts(shared, max_prefix, most_prefix_cuts(items, max_prefix), true);
     if (getenv("PX_N")) n = std::min<int64_t>(atoi(getenv("PX_N")), most_prefix_cuts(items, max_prefix));
     p.chunk = ((max_prefix + n - 1) / n + 63) & ~INT64_C(63);
     p.chunks = (max_prefix + p.chunk - 1) / p.chunk;
@@ -278,7 +278,7 @@ PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t hq, 
     p.share_slots = 2 * 4 * (int64_t)p.own.shares * p.own.dec_rows;
     if (p.own.wide) {
         const int64_t keys = std::max<int64_t>(max_kv, 1);
-        n = prefix_cuts(blocks(alone > 0 ? alone : all), keys, most_prefix_cuts(items, keys), true);
+        n = prefix_cuts(blocks(alone > 0 ? alone : all), keys, most_prefix_cuts(items, keys), false);
         if (getenv("PX_WN")) n = std::min<int64_t>(atoi(getenv("PX_WN")), most_prefix_cuts(items, keys));
         p.own.wide_chunk = ((keys + n - 1) / n + 127) & ~INT64_C(127);
         p.own.wide_chunks = (keys + p.own.wide_chunk - 1) / p.own.wide_chunk;

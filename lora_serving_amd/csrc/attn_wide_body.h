@@ -398,7 +398,11 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         zero[i] = 0.f;
-    u32x4 pf[4];
+    // bf16 parts of a probability.  Shared keys: two, which keep 2^-15 of it, as for single tokens over pages of their own
+    // (with one, and with two and the chunks chosen for it: 8 tokens behind 1000 keys 13.9 and 14.1 us, 64 behind 4096 46.6 and
+    // 46.7, 256 of an e4m3 cache 79 and 82, 32 x 5 24 and 25.5, 128 and a chunk of 1024 211 and 217).
+    constexpr int PARTS = KEYS == KEYS_SHARED ? 2 : 1;
+    u32x4 pf[PARTS][4];
     // S^T: rows = keys 32 u + 8 (i / 4) + 4 hh + i % 4, column = query
     const uint32_t klane = kg * GROUP * 2 + col * D * 2 + 16 * (hh ^ aw_swz<D>(col));
     auto kfrag = [&](uint32_t at, int s, int u) {
@@ -496,7 +500,19 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             // (a masked key's scale may be anything)
             p[e] = !FP8 ? x : edge && s == -INFINITY ? 0.f : x * v2[e];
         }
-        pf[k >> 2][k & 3] = cvt_bf16x2(p[0], p[1]);
+        if (PARTS == 1) {
+            pf[0][k >> 2][k & 3] = cvt_bf16x2(p[0], p[1]);
+        } else {            // (as in attn_decode_body.h: both positive where p is)
+            uint32_t hi[2];
+            float lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                hi[e] = __builtin_elementwise_sub_sat(__float_as_uint(p[e]), 1u) & 0xffff0000u;
+                lo[e] = p[e] - __uint_as_float(hi[e]);
+            }
+            pf[0][k >> 2][k & 3] = hi[0] >> 16 | hi[1];
+            pf[PARTS - 1][k >> 2][k & 3] = cvt_bf16x2(lo[0], lo[1]);
+        }
     };
     auto all_powers = [&](int t, const f32x16 (&st)[2], auto edge) {
 #pragma unroll
@@ -522,8 +538,12 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
 #pragma unroll
         for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d)), as_bf16x8(pf[s]), o[d], 0, 0, 0);
+            for (int d = 0; d < DB; ++d) {
+                const bf16x8 f = as_bf16x8(vfrag(at, s, d));
+#pragma unroll
+                for (int w = 0; w < PARTS; ++w)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, as_bf16x8(pf[w][s]), o[d], 0, 0, 0);
+            }
     };
     // Keys of a tile with an infinity or NaN in V: each wave looks at its own rows before the barrier, a quarter of the reads
     // that it takes for each to look at all of them (KEYS_PLAIN)
@@ -588,7 +608,9 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
                 if (i < KS)
                     nx[e] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(qf[i < KS ? i : 0]), i ? nx[e] : zero, 0, 0, 0);
                 else
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(pf[i < KS ? 0 : s]), o[d], 0, 0, 0);
+#pragma unroll
+                    for (int w = 0; w < PARTS; ++w)
+                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, as_bf16x8(pf[w][i < KS ? 0 : s]), o[d], 0, 0, 0);
             }
             if (i + AHEAD < N)
                 read(i + AHEAD);
@@ -664,19 +686,24 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             const int bit = __ffsll((unsigned long long)rest) - 1, s = (bit & 31) >> 3, e = bit & 7;
             const bool see = sees(block_key(4 * t + s) + 8 * (e >> 2) + 4 * (bit >> 5) + (e & 3));
             const uint32_t half = hh != (bit >> 5) ? 0u : (e & 1) ? 0xffff0000u : 0xffffu;
-            u32x4 p;
+            u32x4 p[PARTS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t a0 = pf[0][i], a1 = pf[1][i], a2 = pf[2][i], a3 = pf[3][i];
-                p[i] = (s & 2) ? ((s & 1) ? a3 : a2) : ((s & 1) ? a1 : a0);
-            }
+            for (int w = 0; w < PARTS; ++w)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t a0 = pf[w][0][i], a1 = pf[w][1][i], a2 = pf[w][2][i], a3 = pf[w][3][i];
+                    p[w][i] = (s & 2) ? ((s & 1) ? a3 : a2) : ((s & 1) ? a1 : a0);
+                }
 #pragma unroll
             for (int d = 0; d < DB; ++d) {
                 u32x4 f = vfrag(at, s, d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     f[i] &= i == (e >> 1) ? half : 0u;
-                const f32x16 x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(p), o[d], 0, 0, 0);
+                f32x16 x = o[d];
+#pragma unroll
+                for (int w = 0; w < PARTS; ++w)
+                    x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(f), as_bf16x8(p[w]), x, 0, 0, 0);
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     o[d][i] = see ? x[i] : o[d][i];
@@ -691,9 +718,12 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
             for (int i = 0; i < 4; ++i)
                 keep[i] = ((mine >> (8 * s + 2 * i)) & 1 ? 0u : 0xffffu) | ((mine >> (8 * s + 2 * i + 1)) & 1 ? 0u : 0xffff0000u);
 #pragma unroll
-            for (int d = 0; d < DB; ++d)
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(as_bf16x8(vfrag(at, s, d) & keep), as_bf16x8(pf[s]), o[d],
-                                                               0, 0, 0);
+            for (int d = 0; d < DB; ++d) {
+                const bf16x8 f = as_bf16x8(vfrag(at, s, d) & keep);
+#pragma unroll
+                for (int w = 0; w < PARTS; ++w)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f, as_bf16x8(pf[w][s]), o[d], 0, 0, 0);
+            }
         }
     };
     // a tile on its own (K of it in place before; afterwards K of the next)

@@ -10,7 +10,7 @@ import pytest
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
-from tests.test_gpu_attention import check, check_lse, gen, randn, ref_attention  # noqa: E402
+from tests.test_gpu_attention import BF, check, check_lse, gen, randn, ref_attention  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -178,6 +178,53 @@ MANY = [
 @pytest.mark.parametrize("case", MANY, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-40:])
 def test_many_sequences(m, case):
     test_groups(m, case)
+
+
+FEW = [
+    ([after(5, (1, 1), (1, 3))], [], 4, 2, 128, 16, False),
+    ([after(130, (1, 2), (1, 60), (1, 200)), after(64, (1, 1), (1, 5))], [(1, 90)], 8, 2, 128, 32, False),
+    ([after(130, (1, 2), (1, 60), (1, 200)), after(64, (1, 1), (1, 5))], [(1, 90)], 16, 1, 64, 16, True),
+    ([after(300, (3, 60), (4, 130), (1, 20))], [], 8, 2, 64, 16, False),
+    ([after(40, *[(1, 1 + i % 30) for i in range(50)])], [], 4, 1, 128, 16, True),
+    ([after(90, (1, 70), (100, 300), (1, 4))], [], 6, 2, 128, 16, False),          # beside a chunk
+]
+
+
+@pytest.mark.parametrize("case", FEW, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-50:])
+def test_few_rows_round_only_the_result(m, case):
+    """Sequences of up to 16 rows (queries x heads of a group) keep a probability in two bf16 parts, of shared keys and of
+    their own: the second part is at most 2^-7 of it and rounded to bf16."""
+    groups, tail, hq, hkv, d, page, fp8 = case
+    b = Batch(m, gen(13 * hq + d), groups, hq, hkv, d, page, fp8, tail)
+    out = b.run()
+    at = 0
+    for (n, L), (k, v) in zip(b.seqs, b.vals):
+        if 0 < n * (hq // hkv) <= 16:
+            ref, _, mag, big = ref_attention(b.q[at:at + n].double(), k, v, True, 0, d ** -0.5)
+            err = (2 * 2.0 ** -23 * (big[..., None] + 16) * 4 + 2.0 ** -7 * BF) * mag
+            bad = ~((out[at:at + n].cpu().double() - ref).abs() <= BF * ref.abs() + (1 + BF) * err + 1e-30)
+            assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} at {(n, L)}"
+        at += n
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_an_infinite_value_stays_infinite(m, d):
+    """An infinity in V, of a shared token (of a whole tile and of the last one) or an own one, gives the same infinity."""
+    b = Batch(m, gen(d + 2), [after(150, (1, 5), (2, 40), (1, 100))], 4, 2, d, 16, False)
+    row_seq = [i for i, (n, _) in enumerate(b.seqs) for _ in range(n)]
+    pos = torch.tensor([L - n + i for n, L in b.seqs for i in range(n)])
+    for of, key in ((0, 3), (0, 70), (0, 143), (1, 160), (2, 249)):
+        pg, at = int(b.table[of, key // 16]), key % 16
+        holds = torch.tensor([int(b.table[s, key // 16]) == pg and b.seqs[s][1] > key for s in row_seq])
+        seen = holds & (pos >= key)
+        for value in (math.inf, -math.inf):
+            keep = b.cache.v[pg, :, at, 9].clone()
+            b.cache.v[pg, :, at, 9] = value
+            got = b.run().cpu()
+            b.cache.v[pg, :, at, 9] = keep
+            assert seen.any() and (got[seen][..., 9] == value).all()
+            assert got[~seen].isfinite().all()
+            assert got[..., [i for i in range(d) if i != 9]].isfinite().all()
 
 
 @pytest.mark.parametrize("seed", range(40))

@@ -10,7 +10,7 @@ import pytest
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
-from tests.test_gpu_attention import check, check_lse, gen, paged_batch, randn  # noqa: E402
+from tests.test_gpu_attention import BF, check, check_lse, gen, paged_batch, randn  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -210,6 +210,42 @@ def test_random_paged(m, seed):
     run_paged(m, seqs, hkv * group, hkv, r.choice([64, 128]), r.choice([16, 64, 256]), r.random() < 0.5, r.random() < 0.85,
               r.choice([1, 31, 32, 33, 96, 128, 300, r.randint(1, 1500)]),
               r.choice([1, 4, 31, 32, 33, 96, 127, 128, 129, r.randint(1, 700)]), r.random() < 0.5)
+
+
+FEW = [
+    # (queries, keys) of the sequences, hq, hkv, d, page, fp8, window, sinks
+    ([(1, 2), (1, 1), (1, 37), (1, 300), (1, 64)], 4, 2, 128, 16, False, 20, 3),
+    ([(1, 5), (1, 41), (1, 150), (1, 2000)], 8, 1, 64, 32, True, 70, 40),
+    ([(3, 60), (4, 130), (1, 20)], 8, 2, 64, 16, False, 9, 1),
+    ([(1, 140), (1, 8), (1, 900)], 16, 1, 128, 16, True, 100, 4),
+    ([(1, 70), (1, 300), (40, 900), (2, 33)], 4, 2, 128, 16, False, 50, 2),        # beside a chunk
+]
+
+
+@pytest.mark.parametrize("case", FEW, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-50:])
+def test_few_rows_round_only_the_result(m, case):
+    """Sequences of up to 16 rows (queries x heads of a group) keep a probability in two bf16 parts: the second part is at
+    most 2^-7 of it and rounded to bf16."""
+    seqs, hq, hkv, d, page, fp8, window, sinks = case
+    g = gen(5 * hq + d)
+    c, table, vals = paged_batch(m, g, seqs, hkv, d, page, fp8)
+    T = sum(n for n, _ in seqs)
+    q = randn(g, T, hq, d)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    mq, mk = max(n for n, _ in seqs), max(L for _, L in seqs)
+    out = torch.full((T, hq, d), 7.0, device="cuda", dtype=torch.bfloat16)
+    m.mlora_paged_attention(q.cuda(), c, table.cuda(), ints([sum(n for n, _ in seqs[:i]) for i in range(len(seqs) + 1)]),
+                            ints([L for _, L in seqs]), out, mq, mk, window=window, sinks=sinks,
+                            ws=m.paged_workspace(T, len(seqs), hq, hkv, d, mq, mk))
+    torch.cuda.synchronize()
+    at = 0
+    for (n, L), (k, v) in zip(seqs, vals):
+        if n * (hq // hkv) <= 16:
+            ref, _, mag, big = reference(q[at:at + n].double(), k, v, True, window, sinks, d ** -0.5)
+            err = (2 * 2.0 ** -23 * (big[..., None] + 16) * 4 + 2.0 ** -7 * BF) * mag
+            bad = ~((out[at:at + n].cpu().double() - ref).abs() <= BF * ref.abs() + (1 + BF) * err + 1e-30)
+            assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} at {(n, L)}"
+        at += n
 
 
 def test_no_sinks_gives_the_same_bits(m):
