@@ -96,6 +96,11 @@ constexpr int OWN_UNIT = 32;      // of KEYS_OWN, whose shares are a wave's
 constexpr int decode_slots(int head_dim, int nq) { return head_dim == 64 && nq == 1 ? 3 : 2; }
 hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream);
 hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream);
+// With a window of up to 64 keys a few keys share a row's weight, and the roundings of their probabilities even out the least
+// (up to 1.5 times the error of a result that is rounded alone): the wide kernel takes them in two bf16 parts.  Such calls are
+// short (8 prompts of 2048, windows of 32 and 64: 111 and 105 us, with two parts 121 and 116; one of 16384: 98 and 100, 107 and
+// 108).
+inline bool few_keys(const AttnArgs &a) { return a.sinks > 0 && a.window <= 64; }
 // Both kinds of sequences over pages in one launch: w as for launch_attn_wide, d as for launch_attn_decode (nq 1).
 hipError_t launch_attn_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int shares, hipStream_t stream);
 

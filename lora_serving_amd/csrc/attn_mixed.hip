@@ -17,7 +17,7 @@ namespace mlora {
 // 33 over 4000 66 (74), 100 over 200 and 128 over 2000 51 (54); but 200 over 1000 and 512 over 2000 228 (210), and of
 // 16 heads on 16 250 e4m3 ones over 2000 and 2048 over 8192 540 (486).  Where there cannot be more items the loop is
 // left out (a chunk of 2048 e4m3 tokens over 8192: 279 us, with it 286).
-template <int D, bool FP8, bool MORE, int KEYS>
+template <int D, bool FP8, bool MORE, int KEYS, int PARTS>
 __global__ __launch_bounds__(256, 2) void attn_mixed_kernel(AttnArgs w, AttnArgs d, uint32_t wide_x, uint32_t shares)
 {
     constexpr int SRC = FP8 ? AW_PAGES_E4M3 : AW_PAGES;
@@ -26,16 +26,16 @@ __global__ __launch_bounds__(256, 2) void attn_mixed_kernel(AttnArgs w, AttnArgs
     uint32_t i = blockIdx.x;
     const bool is_wide = mixed_place(wide_x * w.n_chunks, shares, &i);
     if (is_wide && MORE)
-        attn_wide_pages<D, SRC, KEYS>(w, (int)(i % wide_x), (int)(i / wide_x), (int)wide_x, smem);
+        attn_wide_pages<D, SRC, KEYS, PARTS>(w, (int)(i % wide_x), (int)(i / wide_x), (int)wide_x, smem);
     else if (is_wide)
-        attn_wide_body<D, SRC, 1, false, KEYS>(w, (int)(i % wide_x), (int)(i / wide_x), smem);
+        attn_wide_body<D, SRC, 1, false, KEYS, PARTS>(w, (int)(i % wide_x), (int)(i / wide_x), smem);
     else
         attn_decode_body<D, 1, FP8, KEYS>(d, i, shares, smem);
 }
 
 namespace {
 
-template <int KEYS>
+template <int KEYS, int PARTS>
 hipError_t launch_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int shares, hipStream_t stream)
 {
     const int64_t wide_x = wide_launched(w) * w.hkv, blocks = wide_x * w.n_chunks + shares;
@@ -43,7 +43,7 @@ hipError_t launch_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int 
         return hipErrorInvalidValue;
     const bool more = wide_launched(w) < wide_items(w);
     const dim3 grid((unsigned)blocks);
-#define MIX(D, F, M) attn_mixed_kernel<D, F, M, KEYS><<<grid, dim3(256), 0, stream>>>(w, d, (uint32_t)wide_x, (uint32_t)shares)
+#define MIX(D, F, M) attn_mixed_kernel<D, F, M, KEYS, PARTS><<<grid, dim3(256), 0, stream>>>(w, d, (uint32_t)wide_x, (uint32_t)shares)
 #define MIX_M(D, F) (more ? MIX(D, F, true) : MIX(D, F, false))
 #define MIX_F(D) (d.cache.fp8 ? MIX_M(D, true) : MIX_M(D, false))
     head_dim == 64 ? MIX_F(64) : MIX_F(128);
@@ -57,8 +57,9 @@ hipError_t launch_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int 
 
 hipError_t launch_attn_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int shares, hipStream_t stream)
 {
-    return w.sinks > 0 ? launch_mixed<KEYS_SINKS>(w, d, head_dim, shares, stream)
-                       : launch_mixed<KEYS_PLAIN>(w, d, head_dim, shares, stream);
+    return few_keys(w)   ? launch_mixed<KEYS_SINKS, 2>(w, d, head_dim, shares, stream)
+           : w.sinks > 0 ? launch_mixed<KEYS_SINKS, 1>(w, d, head_dim, shares, stream)
+                         : launch_mixed<KEYS_PLAIN, 1>(w, d, head_dim, shares, stream);
 }
 
 }  // namespace mlora

@@ -6,11 +6,11 @@
 
 namespace mlora {
 
-template <int D, int SRC, int KG, int KEYS>
+template <int D, int SRC, int KG, int KEYS, int PARTS>
 __global__ __launch_bounds__(KG * 256, 2) void attn_wide_kernel(AttnArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint8_t smem[wide_lds<D, SRC, KG, KEYS>];
-    attn_wide_body<D, SRC, KG, false, KEYS>(a, blockIdx.x, blockIdx.y, smem);
+    attn_wide_body<D, SRC, KG, false, KEYS, PARTS>(a, blockIdx.x, blockIdx.y, smem);
 }
 
 // One wave a (token, head): the chunks that hold keys it sees (KEYS_SINKS: all), joined.
@@ -47,7 +47,7 @@ __global__ __launch_bounds__(256) void attn_wide_combine_kernel(AttnArgs a)
 
 namespace {
 
-template <int KEYS>
+template <int KEYS, int PARTS>
 hipError_t launch_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream)
 {
     const int64_t items = wide_items(a);
@@ -59,7 +59,7 @@ hipError_t launch_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t 
     // against 145; 300 tokens of 32 heads: 13.5 against 13.0).  Pages are cut into chunks instead.
     const int64_t keys = a.cu_k ? a.Tk : a.max_q, span = a.window > 0 ? std::min<int64_t>(keys, a.window) : keys;
     const bool halves = items * a.hkv <= CUS && span >= 8 * AW_BN;
-#define AW(D, SRC, KG) attn_wide_kernel<D, SRC, KG, KEYS><<<grid, dim3(KG * 256), 0, stream>>>(a)
+#define AW(D, SRC, KG) attn_wide_kernel<D, SRC, KG, KEYS, PARTS><<<grid, dim3(KG * 256), 0, stream>>>(a)
 #define AW_R(D) (halves ? AW(D, AW_ROWS, 2) : AW(D, AW_ROWS, 1))
 #define AW_P(D) (a.cache.fp8 ? AW(D, AW_PAGES_E4M3, 1) : AW(D, AW_PAGES, 1))
 #define AW_S(D) (pages ? AW_P(D) : AW_R(D))
@@ -86,8 +86,9 @@ hipError_t launch_wide_combine(const AttnArgs &a, int head_dim, hipStream_t stre
 
 hipError_t launch_attn_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t stream)
 {
-    return a.sinks > 0 ? launch_wide<KEYS_SINKS>(a, head_dim, pages, stream)
-                       : launch_wide<KEYS_PLAIN>(a, head_dim, pages, stream);
+    return few_keys(a)   ? launch_wide<KEYS_SINKS, 2>(a, head_dim, pages, stream)
+           : a.sinks > 0 ? launch_wide<KEYS_SINKS, 1>(a, head_dim, pages, stream)
+                         : launch_wide<KEYS_PLAIN, 1>(a, head_dim, pages, stream);
 }
 
 hipError_t launch_attn_wide_combine(const AttnArgs &a, int head_dim, hipStream_t stream)

@@ -170,7 +170,11 @@ constexpr int wide_lds = wide_tiles<D, SRC, KG> + (KEYS == KEYS_PLAIN ? 0 : KG *
 // numbered through, without the blocks that no row of the workgroup sees between them, so that a few first keys cost a
 // quarter of a tile and the window's begins in the same one (8 prompts of 2048, window 512, 4 first keys: 230 us with whole tiles
 // of first keys, 193 with this and the look at V below).  Chunks are equal pieces of the tiles.
-template <int D, int SRC, int KG, bool MORE = false, int KEYS = KEYS_PLAIN>
+// PARTS: bf16 parts of a probability.  One rounds it to 2^-8, two keep 2^-15 of it, as the decode kernel does for single tokens.
+// KEYS_SHARED has two (with one, and with two and the chunks chosen for it: 8 tokens behind 1000 keys 13.9 and 14.1 us, 64
+// behind 4096 46.6 and 46.7, 256 of an e4m3 cache 79 and 82, 32 x 5 24 and 25.5, 128 and a chunk of 1024 211 and 217);
+// KEYS_SINKS where the window is short (few_keys).
+template <int D, int SRC, int KG, bool MORE = false, int KEYS = KEYS_PLAIN, int PARTS = KEYS == KEYS_SHARED ? 2 : 1>
 __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by, uint8_t *smem)
 {
     constexpr bool FP8 = SRC == AW_PAGES_E4M3;
@@ -398,10 +402,6 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         zero[i] = 0.f;
-    // bf16 parts of a probability.  Shared keys: two, which keep 2^-15 of it, as for single tokens over pages of their own
-    // (with one, and with two and the chunks chosen for it: 8 tokens behind 1000 keys 13.9 and 14.1 us, 64 behind 4096 46.6 and
-    // 46.7, 256 of an e4m3 cache 79 and 82, 32 x 5 24 and 25.5, 128 and a chunk of 1024 211 and 217).
-    constexpr int PARTS = KEYS == KEYS_SHARED ? 2 : 1;
     u32x4 pf[PARTS][4];
     // S^T: rows = keys 32 u + 8 (i / 4) + 4 hh + i % 4, column = query
     const uint32_t klane = kg * GROUP * 2 + col * D * 2 + 16 * (hh ^ aw_swz<D>(col));
@@ -882,11 +882,11 @@ __device__ __forceinline__ int attn_wide_body(const AttnArgs &a, int bx, int by,
 }
 
 // Over pages: item and kv head bx, and every wide_x-th after it (wide_x: a multiple of the kv heads).
-template <int D, int SRC, int KEYS = KEYS_PLAIN>
+template <int D, int SRC, int KEYS = KEYS_PLAIN, int PARTS = 1>
 __device__ __forceinline__ void attn_wide_pages(const AttnArgs &a, int bx, int by, int wide_x, uint8_t *smem)
 {
     for (int64_t x = bx;; x += wide_x) {
-        const int total = attn_wide_body<D, SRC, 1, true, KEYS>(a, (int)x, by, smem);
+        const int total = attn_wide_body<D, SRC, 1, true, KEYS, PARTS>(a, (int)x, by, smem);
         if (x + wide_x >= (int64_t)total * a.hkv)
             return;
         __syncthreads();

@@ -248,6 +248,33 @@ def test_few_rows_round_only_the_result(m, case):
         at += n
 
 
+@pytest.mark.parametrize("window,sinks", [(1, 1), (5, 2), (30, 1), (64, 4), (64, 70)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_windows_round_only_the_result(m, d, window, sinks):
+    """Windows of up to 64 keys: a probability is two bf16 parts in prompts and chunks, too (as above)."""
+    g = gen(window + sinks + d)
+    n, hq, hkv, page = 300, 4, 2, 16
+    q, k, v = randn(g, n, hq, d), randn(g, n, hkv, d), randn(g, n, hkv, d)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    out = torch.empty(n, hq, d, device="cuda", dtype=torch.bfloat16)
+    m.mlora_attention(q.cuda(), k.cuda(), v.cuda(), ints(0, n), out, window=window, sinks=sinks)
+    pages = (n + page - 1) // page
+    kc, vc = [torch.zeros(pages * page, hkv, d, dtype=torch.bfloat16) for _ in range(2)]
+    kc[:n], vc[:n] = k, v
+    c = m.Cache(*[x.view(pages, page, hkv, d).permute(0, 2, 1, 3).contiguous().cuda() for x in (kc, vc)])
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    w = 90
+    chunk = torch.empty(w, hq, d, device="cuda", dtype=torch.bfloat16)
+    m.mlora_paged_attention(q[n - w:].cuda(), c, table, ints(0, w), ints(n), chunk, w, n, window=window, sinks=sinks,
+                            ws=m.paged_workspace(w, 1, hq, hkv, d, w, n))
+    torch.cuda.synchronize()
+    ref, _, mag, big = reference(q.double(), k.double(), v.double(), True, window, sinks, d ** -0.5)
+    err = (2 * 2.0 ** -23 * (big[..., None] + 16) * 4 + 2.0 ** -7 * BF) * mag
+    tol = BF * ref.abs() + (1 + BF) * err + 1e-30
+    assert ((out.cpu().double() - ref).abs() <= tol).all()
+    assert ((chunk.cpu().double() - ref[n - w:]).abs() <= tol[n - w:]).all()
+
+
 def test_no_sinks_gives_the_same_bits(m):
     """sinks = 0, and sinks behind a window that reaches them, are the calls without them."""
     g = gen(5)
