@@ -151,6 +151,7 @@ CASES = [
     ([after(64 + i, (1, 1 + i % 5), (1, 3)) for i in range(90)], [], 4, 2, 64, 16, False, True),      # more than 64 groups
     ([after(64, *[(17, 20 + i) for i in range(70)])], [], 4, 2, 64, 16, False, True),  # many chunks
     ([after(256, (2, 2), (2, 2))], [], 32, 2, 128, 256, False, True),                 # 32 rows, whole pages
+    ([after(230, (1, 2), (1, 140), (1, 33))], [(1, 50)], 24, 1, 128, 16, True, True),  # single tokens of 24 rows
 ]
 
 

@@ -139,6 +139,10 @@ PAGED = [
     ([(1, 2000)] * 3, 48, 1, 64, 16, False, True, 300, 4),                      # a group of 48
     ([(1, 300), (2, 90)], 4, 2, 128, 16, False, True, 2 ** 31 - 1, 4),          # nothing is hidden
     ([(1, 700), (40, 90)], 4, 2, 128, 16, True, True, 30, 2 ** 31 - 1),         # every key is a first one
+    ([(1, 800), (1, 90)], 24, 1, 128, 16, False, True, 130, 4),                 # single tokens of 24 rows
+    ([(1, 700), (4, 333), (60, 900), (1, 9)], 4, 2, 128, 16, False, True, 50, 0),         # a window alone, its past given up
+    ([(1, 3000), (1, 2100)], 4, 2, 64, 16, True, True, 1500, 0),
+    ([(70, 1900)], 8, 2, 128, 16, True, False, 300, 0),
 ]
 
 
