@@ -327,7 +327,7 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
             }
         };
         int at = k0 + w32, kb = key_at(at);     // this wave's step, and its first key
-        if (OWN && b != seen) {
+        if (OWN && b != seen && L > 0) {         // (a table may have no columns)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
                 pgf[u] = table[min(((sq.lo & ~31) + 16 * u) >> ps, last)];

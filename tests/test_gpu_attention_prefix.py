@@ -269,6 +269,22 @@ def test_bounds_above_the_sizes(m):
     b.check(out)
 
 
+def test_no_keys_and_no_table(m):
+    """A batch whose sequences hold nothing yet, with a table of no columns: zeros and -inf."""
+    k, v = [torch.zeros(2, 2, 16, 64, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    for n, w in ((3, 1), (2, 70)):
+        T = n * w
+        q = randn(gen(n), T, 4, 64).cuda()
+        out, lse = torch.full_like(q, 7.0), torch.full((T, 4), 7.0, device="cuda")
+        table = torch.empty(n, 0, device="cuda", dtype=torch.int32)
+        for causal in (True, False):
+            m.mlora_prefix_attention(q, m.Cache(k, v), table, ints(*range(0, T + 1, w)), ints(*[0] * n), ints(0, n), ints(40), out,
+                                     w, 100, 60, causal=causal, lse=lse, ws=m.prefix_workspace(T, n, 1, 4, 2, 64, w, 100, 60))
+            torch.cuda.synchronize()
+            assert (out == 0).all() and (lse == -math.inf).all()
+            out.fill_(7.0)
+
+
 def test_unanswered_and_padding_rows_are_left(m):
     """Sequences of more queries than max_q and rows past the last sequence keep what was there."""
     b = Batch(m, gen(4), [after(200, (1, 4), (9, 30), (1, 1))], 4, 2, 64, 16, False)
