@@ -263,7 +263,6 @@ PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t hq, 
     // (half of the groups' last row blocks are taken to be more)
     const int64_t shared = blocks(all - alone) + std::min<int64_t>(n_groups / 2, T) * hkv;
     int64_t n = prefix_cuts(shared, max_prefix, most_prefix_cuts(items, max_prefix), true);
-    if (getenv("PX_N")) n = std::min<int64_t>(atoi(getenv("PX_N")), most_prefix_cuts(items, max_prefix));
     p.chunk = ((max_prefix + n - 1) / n + 63) & ~INT64_C(63);
     p.chunks = (max_prefix + p.chunk - 1) / p.chunk;
     // The card holds 512 workgroups: those of the shares start beside the others', one of which a CU has at the most.  Where a
@@ -279,7 +278,6 @@ PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t hq, 
     if (p.own.wide) {
         const int64_t keys = std::max<int64_t>(max_kv, 1);
         n = prefix_cuts(blocks(alone > 0 ? alone : all), keys, most_prefix_cuts(items, keys), false);
-        if (getenv("PX_WN")) n = std::min<int64_t>(atoi(getenv("PX_WN")), most_prefix_cuts(items, keys));
         p.own.wide_chunk = ((keys + n - 1) / n + 127) & ~INT64_C(127);
         p.own.wide_chunks = (keys + p.own.wide_chunk - 1) / p.own.wide_chunk;
     }
