@@ -497,6 +497,8 @@ mlora_status mlora_validate_pages_sinks(const mlora_cache *cache, const int32_t 
  *   ws  mlora_prefix_workspace_size() bytes for the same sizes, or for larger ones of the same heads; the size
  *       never falls as any of them rises (0 where the call would refuse them).  It holds fp32 parts of every row, at least
  *       2 T n_q_heads (4 head_dim + 8) bytes
+ * n_groups and max_prefix are below 2^30, n_seqs * n_kv_heads * (max_kv / 32 + 1) below 2^31, other sizes as in
+ * mlora_paged_attention.
  * mlora_validate_prefixes checks the groups on the host (all pointers host): group_start, 0 <= prefix_len <= max_prefix,
  * and that the table and each first sequence's kv_len reach that far; MLORA_ERR_SHAPE and the value where not.
  */

@@ -71,10 +71,10 @@ bool paged_sizes_ok(int64_t T, int32_t n_seqs, int32_t hq, int32_t hkv, int64_t 
            (int64_t)n_seqs * hkv * (max_kv / DECODE_UNIT + 1) < MAX_ROWS;
 }
 
-// And of a call over shared prefixes, whose shares are made of smaller units.
-bool prefix_sizes_ok(int32_t n_seqs, int32_t hkv, int64_t max_kv, int64_t max_prefix)
+// And of a call over shared prefixes, whose shares are made of smaller units (64 lanes count the groups in equal runs).
+bool prefix_sizes_ok(int32_t n_seqs, int32_t n_groups, int32_t hkv, int64_t max_kv, int64_t max_prefix)
 {
-    return max_prefix < MAX_KEYS && (int64_t)n_seqs * hkv * (max_kv / OWN_UNIT + 1) < MAX_ROWS;
+    return max_prefix < MAX_KEYS && n_groups < MAX_KEYS && (int64_t)n_seqs * hkv * (max_kv / OWN_UNIT + 1) < MAX_ROWS;
 }
 
 bool rows_ok(int64_t stride, int64_t width) { return stride >= width && stride % 8 == 0; }
@@ -690,7 +690,7 @@ size_t mlora_prefix_workspace_size(int64_t T, int32_t n_seqs, int32_t n_groups, 
     if (n_groups < 0 || max_prefix < 0)
         return 0;
     const size_t paged = mlora_paged_workspace_size(T, n_seqs, n_q_heads, n_kv_heads, head_dim, max_q, max_kv);
-    if (paged > 0 && !prefix_sizes_ok(n_seqs, n_kv_heads, max_kv, max_prefix))
+    if (paged > 0 && !prefix_sizes_ok(n_seqs, n_groups, n_kv_heads, max_kv, max_prefix))
         return 0;
     if (paged == 0 || n_groups == 0 || max_prefix == 0)
         return paged;
@@ -711,7 +711,7 @@ mlora_status mlora_prefix_attention(const void *q, int64_t q_stride, int64_t T, 
                                        max_q, max_kv, causal, 0, 0, scale, out, out_stride, lse);
     if (st != MLORA_OK)
         return st;
-    if (!prefix_sizes_ok(n_seqs, c.a.hkv, max_kv, max_prefix))
+    if (!prefix_sizes_ok(n_seqs, n_groups, c.a.hkv, max_kv, max_prefix))
         return MLORA_ERR_UNSUPPORTED;
     if (c.nothing)
         return MLORA_OK;
