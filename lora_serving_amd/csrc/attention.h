@@ -97,9 +97,10 @@ constexpr int decode_slots(int head_dim, int nq) { return head_dim == 64 && nq =
 hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream);
 hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream);
 // With a window of up to 64 keys a few keys share a row's weight, and the roundings of their probabilities even out the least
-// (up to 1.5 times the error of a result that is rounded alone): the wide kernel takes them in two bf16 parts.  Such calls are
+// (up to 1.5 times the error of a result that is rounded alone): both kernels take them in two bf16 parts.  Such calls are
 // short (8 prompts of 2048, windows of 32 and 64: 111 and 105 us, with two parts 121 and 116; one of 16384: 98 and 100, 107 and
-// 108).
+// 108).  The decode kernel's two column tiles spill 56 registers for them at D = 128 (27 with one part; 32 x 5 tokens, window 64:
+// 14.6 us, with two parts 17.9, e4m3 11.9 and 13.6, D = 64 7.5 and 7.8; 256 x 8 81 and 101).
 inline bool few_keys(const AttnArgs &a) { return a.sinks > 0 && a.window <= 64; }
 // Both kinds of sequences over pages in one launch: w as for launch_attn_wide, d as for launch_attn_decode (nq 1).
 hipError_t launch_attn_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int shares, hipStream_t stream);

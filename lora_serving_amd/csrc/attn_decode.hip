@@ -4,11 +4,11 @@
 
 namespace mlora {
 
-template <int D, int NQ, bool FP8, int KEYS>
+template <int D, int NQ, bool FP8, int KEYS, int PARTS>
 __global__ __launch_bounds__(256, decode_slots(D, NQ)) void attn_decode_kernel(AttnArgs a)
 {
     __shared__ __attribute__((aligned(16))) uint8_t smem[decode_lds<D, NQ>];
-    attn_decode_body<D, NQ, FP8, KEYS>(a, blockIdx.x, gridDim.x, smem);
+    attn_decode_body<D, NQ, FP8, KEYS, PARTS>(a, blockIdx.x, gridDim.x, smem);
 }
 
 // The join, a workgroup a cut between shares: the first cut within a sequence and head joins its parts, one wave a
@@ -36,11 +36,12 @@ __global__ __launch_bounds__(256) void attn_combine_kernel(AttnArgs a, int share
 
 namespace {
 
-template <int KEYS>
+// (PARTS: of two column tiles)
+template <int KEYS, int PARTS>
 hipError_t launch_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream)
 {
     const dim3 grid((unsigned)shares);
-#define DEC(D, NQ, F) attn_decode_kernel<D, NQ, F, KEYS><<<grid, dim3(256), 0, stream>>>(a)
+#define DEC(D, NQ, F) attn_decode_kernel<D, NQ, F, KEYS, NQ == 1 ? 2 : PARTS><<<grid, dim3(256), 0, stream>>>(a)
 #define DEC_F(D, NQ) (a.cache.fp8 ? DEC(D, NQ, true) : DEC(D, NQ, false))
 #define DEC_Q(D) (nq == 1 ? DEC_F(D, 1) : DEC_F(D, 2))
     head_dim == 64 ? DEC_Q(64) : DEC_Q(128);
@@ -67,8 +68,9 @@ hipError_t launch_combine(const AttnArgs &a, int head_dim, int shares, hipStream
 
 hipError_t launch_attn_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream)
 {
-    return a.sinks > 0 ? launch_decode<KEYS_SINKS>(a, head_dim, nq, shares, stream)
-                       : launch_decode<KEYS_PLAIN>(a, head_dim, nq, shares, stream);
+    return few_keys(a)   ? launch_decode<KEYS_SINKS, 2>(a, head_dim, nq, shares, stream)
+           : a.sinks > 0 ? launch_decode<KEYS_SINKS, 1>(a, head_dim, nq, shares, stream)
+                         : launch_decode<KEYS_PLAIN, 1>(a, head_dim, nq, shares, stream);
 }
 
 hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipStream_t stream)

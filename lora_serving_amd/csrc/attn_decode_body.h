@@ -173,14 +173,14 @@ constexpr int decode_lds = KEYS == KEYS_OWN ? 4 * 2 * 32 * D + (NQ > 1 ? 4 * 16 
 // by itself: no barrier, so that the start of one wave's sequence, a chain of loads, hides behind the others' keys.  What
 // comes after a shared prefix is short, and the waves of a workgroup waited for each start together (256 of an e4m3 cache
 // behind four prefixes, 1 to 700 keys each: the kernel 97 us, with this and fewer chunks of the prefixes 77).
-template <int D, int NQ, bool FP8, int KEYS = KEYS_PLAIN>
+// PARTS: bf16 parts of a probability (see below).
+template <int D, int NQ, bool FP8, int KEYS = KEYS_PLAIN, int PARTS = NQ == 1 ? 2 : 1>
 __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t share, uint32_t shares, uint8_t *smem)
 {
     constexpr int ESZ = FP8 ? 1 : 2;
     constexpr int KS = D / 32;          // k-steps of the first product
     constexpr int DB = D / 16;          // row blocks of the second
     constexpr int LD = FP8 ? D / 64 : D / 32;   // 16-byte loads per lane and 16-key block
-    constexpr int PARTS = NQ == 1 ? 2 : 1;      // bf16 parts of a probability
     constexpr int OS = D + 4;           // row stride of the joined accumulators in LDS
     constexpr int VW = 32 * D;          // a wave's V rows in LDS
     constexpr bool OWN = KEYS == KEYS_OWN;
@@ -507,7 +507,8 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                 // the time for (48 batches: 0.6% slower at the median, long ones 2% at most), the first cut off below p (a step
                 // of 2^-7), the rest rounded (2^-15 of p); both are positive where p is, so an infinite V stays that
                 // infinity.  Two tiles: rounded to bf16 (half a step: 2^-8 relative), for two parts take registers and
-                // products that are not there (32 x 8 tokens over 4096 keys 156 us, so 137; e4m3 75 and 70).
+                // products that are not there (32 x 8 tokens over 4096 keys 156 us, so 137; e4m3 75 and 70), but two parts
+                // where a window is short (few_keys).
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (PARTS == 1) {

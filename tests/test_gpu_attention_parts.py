@@ -1,0 +1,48 @@
+"""Where a probability is kept in two bf16 parts with a window and first tokens, and over shared prefixes: nothing but the
+result is rounded to bf16 then.
+
+Tolerance as in test_gpu_attention_few_rows: scores, exponentials and sums in fp32; a probability (over an e4m3 cache: times
+its value's scale, as the matrix cores take it) is a part and a rest of at most 2^-7 of it, which is rounded to bf16; then
+the result's rounding.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+from tests.test_gpu_attention import BF, gen, m, paged_batch, randn, ref_attention  # noqa: E402, F401  (m: a fixture)
+from tests.test_gpu_attention_prefix import Batch, after  # noqa: E402
+from tests.test_gpu_attention_sinks import reference  # noqa: E402
+
+
+def check(got, ref, mag, big, what):
+    err = (2 * 2.0 ** -23 * (big[..., None] + 16) * 4 + 2.0 ** -7 * BF) * mag
+    bad = ~((got.cpu().double() - ref).abs() <= BF * ref.abs() + (1 + BF) * err + 1e-30)
+    assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} at {what}"
+
+
+def windowed(m, seqs, hq, hkv, d, page, fp8, window, sinks):  # noqa: F811
+    g = gen(3 * hq + d + window)
+    c, table, vals = paged_batch(m, g, seqs, hkv, d, page, fp8)
+    T = sum(n for n, _ in seqs)
+    q = randn(g, T, hq, d)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    mq, mk = max(n for n, _ in seqs), max(L for _, L in seqs)
+    out = torch.full((T, hq, d), 7.0, device="cuda", dtype=torch.bfloat16)
+    m.mlora_paged_attention(q.cuda(), c, table.cuda(), ints([sum(n for n, _ in seqs[:i]) for i in range(len(seqs) + 1)]),
+                            ints([L for _, L in seqs]), out, mq, mk, window=window, sinks=sinks,
+                            ws=m.paged_workspace(T, len(seqs), hq, hkv, d, mq, mk))
+    torch.cuda.synchronize()
+    at = 0
+    for (n, L), (k, v) in zip(seqs, vals):
+        ref, _, mag, big = reference(q[at:at + n].double(), k, v, True, window, sinks, d ** -0.5)
+        check(out[at:at + n], ref, mag, big, (n, L))
+        at += n
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("window,sinks", [(1, 1), (5, 2), (30, 1), (64, 4), (64, 70)])
+def test_short_windows_of_a_few_tokens_a_sequence(m, d, window, sinks, fp8):  # noqa: F811
+    """Windows of up to 64 keys where max_q gives 17 to 32 rows (queries x heads of a kv head's group)."""
+    windowed(m, [(5, 300), (5, 5), (1, 40), (8, 1500), (3, 90)], 8, 2, d, 16, fp8, window, sinks)
