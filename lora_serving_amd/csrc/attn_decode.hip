@@ -41,7 +41,8 @@ template <int KEYS, int PARTS>
 hipError_t launch_decode(const AttnArgs &a, int head_dim, int nq, int shares, hipStream_t stream)
 {
     const dim3 grid((unsigned)shares);
-#define DEC(D, NQ, F) attn_decode_kernel<D, NQ, F, KEYS, NQ == 1 ? 2 : PARTS><<<grid, dim3(256), 0, stream>>>(a)
+#define DEC(D, NQ, F) \
+    attn_decode_kernel<D, NQ, F, KEYS, NQ == 1 ? 2 : key_parts<KEYS, F, PARTS>><<<grid, dim3(256), 0, stream>>>(a)
 #define DEC_F(D, NQ) (a.cache.fp8 ? DEC(D, NQ, true) : DEC(D, NQ, false))
 #define DEC_Q(D) (nq == 1 ? DEC_F(D, 1) : DEC_F(D, 2))
     head_dim == 64 ? DEC_Q(64) : DEC_Q(128);

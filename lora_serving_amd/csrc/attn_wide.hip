@@ -59,7 +59,8 @@ hipError_t launch_wide(const AttnArgs &a, int head_dim, bool pages, hipStream_t 
     // against 145; 300 tokens of 32 heads: 13.5 against 13.0).  Pages are cut into chunks instead.
     const int64_t keys = a.cu_k ? a.Tk : a.max_q, span = a.window > 0 ? std::min<int64_t>(keys, a.window) : keys;
     const bool halves = items * a.hkv <= CUS && span >= 8 * AW_BN;
-#define AW(D, SRC, KG) attn_wide_kernel<D, SRC, KG, KEYS, PARTS><<<grid, dim3(KG * 256), 0, stream>>>(a)
+#define AW(D, SRC, KG) \
+    attn_wide_kernel<D, SRC, KG, KEYS, key_parts<KEYS, SRC == AW_PAGES_E4M3, PARTS>><<<grid, dim3(KG * 256), 0, stream>>>(a)
 #define AW_R(D) (halves ? AW(D, AW_ROWS, 2) : AW(D, AW_ROWS, 1))
 #define AW_P(D) (a.cache.fp8 ? AW(D, AW_PAGES_E4M3, 1) : AW(D, AW_PAGES, 1))
 #define AW_S(D) (pages ? AW_P(D) : AW_R(D))

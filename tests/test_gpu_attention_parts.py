@@ -46,3 +46,23 @@ def windowed(m, seqs, hq, hkv, d, page, fp8, window, sinks):  # noqa: F811
 def test_short_windows_of_a_few_tokens_a_sequence(m, d, window, sinks, fp8):  # noqa: F811
     """Windows of up to 64 keys where max_q gives 17 to 32 rows (queries x heads of a kv head's group)."""
     windowed(m, [(5, 300), (5, 5), (1, 40), (8, 1500), (3, 90)], 8, 2, d, 16, fp8, window, sinks)
+
+
+E4M3 = [
+    # (queries, keys) of the sequences, hq, hkv, d, page, window, sinks
+    ([(5, 700), (5, 5), (1, 300), (8, 1500)], 8, 2, 128, 32, 300, 4),                  # 17 to 32 rows
+    ([(5, 700), (2, 130), (4, 65)], 12, 2, 64, 16, 70, 1),
+    ([(300, 900)], 4, 2, 128, 32, 300, 1),                                             # a chunk, cut into pieces
+    ([(70, 70), (90, 400)], 8, 2, 64, 16, 100, 2),
+    ([(1, 700), (70, 300), (1, 20), (2, 90)], 4, 2, 128, 16, 65, 4),                   # single tokens beside chunks
+    ([(1, 50 + 7 * i) for i in range(40)] + [(200, 600)], 8, 2, 64, 64, 200, 130),
+    ([(40, 60 + 9 * i) for i in range(70)] + [(1, 9)], 4, 1, 64, 16, 90, 3),           # more row blocks than workgroups at first
+]
+
+
+@pytest.mark.parametrize("case", E4M3, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-50:])
+def test_first_tokens_over_an_e4m3_cache(m, case):  # noqa: F811
+    """The matrix cores take a probability times its value's scale: of few keys with most of the weight one rounding to bf16
+    would be in all of a row's results."""
+    seqs, hq, hkv, d, page, window, sinks = case
+    windowed(m, seqs, hq, hkv, d, page, True, window, sinks)
