@@ -490,7 +490,9 @@ mlora_status mlora_validate_pages_sinks(const mlora_cache *cache, const int32_t 
  *   max_prefix  host upper bound of prefix_len
  * page_table and kv_len are mlora_paged_attention's, with all tokens of every sequence; a sequence whose queries do not
  * all see the whole prefix (kv_len less its queries, if causal, is below prefix_len) is answered from its own pages.
- * A group's first sequence must hold the whole prefix.  Probabilities of shared keys keep 2^-15.  Sequences of more than
+ * A group's first sequence must hold the whole prefix.  Probabilities of shared keys keep 2^-15, and so do those of other keys
+ * of sequences of up to 16 rows, or 32 where max_q gives no more; else 2^-8 (and as in
+ * mlora_paged_attention, which answers the call, where n_groups or max_prefix is 0).  Sequences of more than
  * 256 rows (queries x heads of a kv head's group) read the prefix for themselves, for they fill the matrix cores without
  * others, and with a chunk's precision.  Where less than about 32 MB of keys and values need not be read again (sequences x
  * shared tokens), mlora_paged_attention is faster, by 4 to 6 us.

@@ -174,7 +174,7 @@ constexpr int decode_lds = KEYS == KEYS_OWN ? 4 * 2 * 32 * D + (NQ > 1 ? 4 * 16 
 // comes after a shared prefix is short, and the waves of a workgroup waited for each start together (256 of an e4m3 cache
 // behind four prefixes, 1 to 700 keys each: the kernel 97 us, with this and fewer chunks of the prefixes 77).
 // PARTS: bf16 parts of a probability (see below).
-template <int D, int NQ, bool FP8, int KEYS = KEYS_PLAIN, int PARTS = NQ == 1 ? 2 : 1>
+template <int D, int NQ, bool FP8, int KEYS = KEYS_PLAIN, int PARTS = NQ == 1 || KEYS == KEYS_OWN ? 2 : 1>
 __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t share, uint32_t shares, uint8_t *smem)
 {
     constexpr int ESZ = FP8 ? 1 : 2;
@@ -508,7 +508,10 @@ __device__ __forceinline__ void attn_decode_body(const AttnArgs &a, uint32_t sha
                 // of 2^-7), the rest rounded (2^-15 of p); both are positive where p is, so an infinite V stays that
                 // infinity.  Two tiles: rounded to bf16 (half a step: 2^-8 relative), for two parts take registers and
                 // products that are not there (32 x 8 tokens over 4096 keys 156 us, so 137; e4m3 75 and 70), but two parts
-                // where a window is short (few_keys).
+                // where a window is short (few_keys), over an e4m3 cache with sinks (key_parts), and behind a prefix, which
+                // leaves a sequence few keys (own keys of up to 400, rms error of a result that is rounded alone 1: 1.25,
+                // e4m3 1.4, two parts 1.0; 32 x 5 tokens, up to 600 own keys: 64 and 65 us, e4m3 72 and 74, D = 64 27 and
+                // 27, up to 4000: 85 and 90, e4m3 67 and 73).
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     if (PARTS == 1) {

@@ -66,3 +66,27 @@ def test_first_tokens_over_an_e4m3_cache(m, case):  # noqa: F811
     would be in all of a row's results."""
     seqs, hq, hkv, d, page, window, sinks = case
     windowed(m, seqs, hq, hkv, d, page, True, window, sinks)
+
+
+FEW = [
+    # groups, sequences of no group, hq, hkv, d, page, fp8: 17 to 32 rows a sequence, and fewer
+    ([after(20, (5, 5), (5, 80), (2, 300), (5, 33))], [], 8, 2, 128, 16, False),
+    ([after(20, (5, 5), (5, 80), (2, 300), (5, 33))], [], 8, 2, 64, 32, True),
+    ([after(600, (5, 5), (5, 80), (2, 700), (1, 3))], [(5, 40)], 12, 2, 128, 32, True),
+    ([after(65, (3, 3), (3, 1500)), after(130, (3, 20), (2, 9), (1, 1))], [(3, 400), (3, 2)], 10, 1, 64, 16, False),
+    ([after(90, (8, 8), (8, 300)), (0, [(8, 70)])], [(8, 8)], 4, 1, 128, 16, False),
+    ([after(40, *[(5, 5 + 7 * i % 90) for i in range(70)])], [], 8, 2, 128, 16, True),
+]
+
+
+@pytest.mark.parametrize("case", FEW, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-50:])
+def test_a_few_tokens_a_sequence_behind_prefixes(m, case):  # noqa: F811
+    """Where max_q gives 17 to 32 rows, of shared keys and of their own."""
+    groups, tail, hq, hkv, d, page, fp8 = case
+    b = Batch(m, gen(17 * hq + d), groups, hq, hkv, d, page, fp8, tail)
+    out = b.run()
+    at = 0
+    for (n, L), (k, v) in zip(b.seqs, b.vals):
+        ref, _, mag, big = ref_attention(b.q[at:at + n].double(), k, v, True, 0, d ** -0.5)
+        check(out[at:at + n], ref, mag, big, (n, L))
+        at += n
