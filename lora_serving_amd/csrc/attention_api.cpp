@@ -265,10 +265,13 @@ PrefixPlan prefix_plan(int64_t T, int32_t n_seqs, int32_t n_groups, int32_t hq, 
     int64_t n = prefix_cuts(shared, max_prefix, most_prefix_cuts(items, max_prefix), true);
     p.chunk = ((max_prefix + n - 1) / n + 63) & ~INT64_C(63);
     p.chunks = (max_prefix + p.chunk - 1) / p.chunk;
-    // The card holds 512 workgroups: those of the shares start beside the others', one of which a CU has at the most.  Where a
-    // sequence may have more than 1536 keys of its own, they outlast the others, and as many on every CU are faster than a second
-    // one on some (128 tokens behind 4000 keys, 500 to 3000 of their own: 384 209 us, 256 182; 64 behind 4096, 1 to 1024: 384 39,
-    // 256 45).
+    // The card holds 512 workgroups: those of the shares start beside the others', one of which a CU has at the most.  Where
+    // sequences have many keys of their own, they outlast the others, and as many on every CU are faster than a second one on
+    // some (128 tokens behind 4000 keys, 500 to 3000 of their own: 384 209 us, 256 182; 64 behind 4096, 1 to 1024: 384 39, 256
+    // 45).  The host knows bounds alone: their difference is what a sequence of the longest prefix may have, more than 1536
+    // keys here, but sequences of no group or of a shorter prefix may have more (8 of 1 to 9200 beside 64 behind 8192: both 84
+    // us; 64 of 1 to 9000 beside 128 behind 8000: 362, with 256 301), and one long one may stand for none of the others (one
+    // of 8000 beside 64 behind 2000: 384 43, 256 45; beside 128: 90 and 82).
     const int64_t beside = std::min(shared * p.chunks, CUS);
     int64_t groups = 2 * CUS - beside;
     if (max_kv - max_prefix > 1536)

@@ -5,10 +5,11 @@
 // The shared part is the wide kernel's (attn_wide_body.h: the group as one sequence of queries that see every key),
 // cut into chunks of keys; the own part is the mixed batch's (attn_mixed.hip).  All of them in one launch, for the former
 // is bound by the matrix cores and the latter by memory.  Measured (D = 128, 32 heads on 8, both kernels): 64 tokens behind 4096
-// keys, 1 to 1024 of their own, 47 us (3.3 TB/s of what has to be read), 256 of an e4m3 cache in four groups 82 us (2.8), 32 x 5
-// of D = 64 behind 8192 and 6001 25.5 us, 128 tokens and a chunk of 1024 behind 8000 217 us (740 TFLOP/s), 8 tokens behind 1000
-// keys 14 us; replayed in a graph 40, 80, 28, 238 and 14 us, where mlora_paged_attention takes 152, 186, 48, 588 and 17.  Bound
-// by the own keys' reads and, as long as both run, by what the two kinds cost each other; the join is 5 to 11 us.
+// keys, 1 to 1024 of their own, 46 to 47 us (3.3 TB/s of what has to be read), 256 of an e4m3 cache in four groups 82 us (2.8),
+// 32 x 5 of D = 64 behind 8192 and 6001 25.5 us, 128 tokens and a chunk of 1024 behind 8000 215 to 217 us (745 TFLOP/s), 8 tokens
+// behind 1000 keys 14 us; in a graph of calls on three inputs 48, 84, 29, 216 and 16 us, where mlora_paged_attention takes 155,
+// 196, 51, 586 and 19.  Bound by the own keys' reads and, as long as both run, by what the two kinds cost each other; the join
+// is 5 to 11 us.
 #include "attn_decode_body.h"
 #include "attn_mixed.h"
 #include "attn_wide_body.h"
