@@ -404,8 +404,8 @@ mlora_status mlora_attention(const void *q, int64_t q_stride, const void *k, int
 /*
  * mlora_attention with a few first keys of each sequence that stay visible behind the window: with window > 0, query i
  * sees key j when j < L, j <= p (if causal) and j > p - window or j < sinks.  sinks >= 0; without a window it hides and
- * shows nothing.  All else as mlora_attention, which is sinks = 0 (but where the window is of up to 64 keys, and over an
- * e4m3 cache, 2^-15 of a probability is kept).
+ * shows nothing.  All else as mlora_attention, which answers calls with sinks = 0 or a window of T_k (over pages: max_kv) or
+ * more; in others a window of up to 64 keys, or any over an e4m3 cache, keeps 2^-15 of a probability.
  */
 mlora_status mlora_attention_sinks(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                                    const void *v, int64_t v_stride, int64_t T_q, int64_t T_k,
