@@ -490,14 +490,14 @@ mlora_status mlora_validate_pages_sinks(const mlora_cache *cache, const int32_t 
  *   max_prefix  host upper bound of prefix_len
  * page_table and kv_len are mlora_paged_attention's, with all tokens of every sequence; a sequence whose queries do not
  * all see the whole prefix (kv_len less its queries, if causal, is below prefix_len) is answered from its own pages.
- * A group's first sequence must hold the whole prefix.  Probabilities of shared keys keep 2^-15, and so do those of other keys
- * of sequences of up to 16 rows, or 32 where max_q gives no more; else 2^-8 (and as in
- * mlora_paged_attention, which answers the call, where n_groups or max_prefix is 0).  Sequences of more than
- * 256 rows (queries x heads of a kv head's group) read the prefix for themselves, for they fill the matrix cores without
- * others, and with a chunk's precision.  It pays where enough keys and values need not be read again (sequences x shared tokens x
- * a token's bytes): over a bf16 cache from 16 to 50 MB on for up to 16 sequences, from 30 to 130 MB on for more (64 sequences of
- * 32 heads on 8, head_dim 128: 370 tokens); over an e4m3 cache from 40 to 130 MB on, for fewer than 16 sequences from 100 MB on
- * or not at all.  With less mlora_paged_attention is faster, by up to 10 us.
+ * A group's first sequence must hold the whole prefix.  Probabilities of shared keys keep 2^-15, and so do those of other
+ * keys of sequences of up to 16 rows, or 32 where max_q gives no more, and of all over an e4m3 cache; else 2^-8 (and as in
+ * mlora_paged_attention, which answers the call, where n_groups or max_prefix is 0).  Sequences of more than 256 rows
+ * (queries x heads of a kv head's group) read the prefix for themselves, for they fill the matrix cores without others.  It
+ * pays where enough keys and values need not be read again (sequences x shared tokens x a token's bytes): over a bf16 cache
+ * from 16 to 50 MB on for up to 16 sequences, from 30 to 130 MB on for more (64 sequences of 32 heads on 8, head_dim 128:
+ * 370 tokens); over an e4m3 cache from 40 to 130 MB on, for fewer than 16 sequences from 100 MB on or not at all.  With less
+ * mlora_paged_attention is faster, by up to 10 us.
  *   ws  mlora_prefix_workspace_size() bytes for the same sizes, or for larger ones of the same heads; the size
  *       never falls as any of them rises (0 where the call would refuse them).  It holds fp32 parts of every row, at least
  *       2 T n_q_heads (4 head_dim + 8) bytes, rows of long chunks too, though few calls write those (16384 tokens of 32 heads,

@@ -102,12 +102,14 @@ hipError_t launch_attn_combine(const AttnArgs &a, int head_dim, int shares, hipS
 // 108).  The decode kernel's two column tiles spill 56 registers for them at D = 128 (27 with one part; 32 x 5 tokens, window 64:
 // 14.6 us, with two parts 17.9, e4m3 11.9 and 13.6, D = 64 7.5 and 7.8; 256 x 8 81 and 101).
 inline bool few_keys(const AttnArgs &a) { return a.sinks > 0 && a.window <= 64; }
-// And over an e4m3 cache, whatever the window: there the matrix cores take a probability times its value's scale, so that the
-// largest one, exactly 1, is rounded as well, and where a few first keys hold most of the weight one rounding is in all of a
-// row's results (windows of 70 to 300: up to 2.1 times the rms error of a result that is rounded alone, with two parts 1.0; in
-// bf16 1.1 at the most).  D = 128: a chunk of 2048 over 8048 keys, window 2048, 101 us, with two parts 127; beside 256 tokens 256
-// and 268; 32 x 5 tokens, window 2048, 57 and 62; 256 x 5, window 1024, 188 and 207; a chunk of D = 64 52 and 58.
-template <int KEYS, bool FP8, int PARTS> constexpr int key_parts = KEYS == KEYS_SINKS && FP8 ? 2 : PARTS;
+// And over an e4m3 cache, whatever the window, and behind shared prefixes: there the matrix cores take a probability times its
+// value's scale, so that the largest one, exactly 1, is rounded as well, and where a few first keys hold most of the weight one
+// rounding is in all of a row's results (windows of 70 to 300: up to 2.1 times the rms error of a result that is rounded alone,
+// with two parts 1.0; in bf16 1.1 at the most).  D = 128: a chunk of 2048 over 8048 keys, window 2048, 101 us, with two parts
+// 127; beside 256 tokens 256 and 268; 32 x 5 tokens, window 2048, 57 and 62; 256 x 5, window 1024, 188 and 207; a chunk of D =
+// 64 52 and 58.  Chunks behind a prefix: 2.05 times that error; 128 tokens and a chunk of 1024 behind 8000 keys 277 and 322, 32
+// and 300 behind 4000 82 and 99.
+template <int KEYS, bool FP8, int PARTS> constexpr int key_parts = KEYS != KEYS_PLAIN && FP8 ? 2 : PARTS;
 // Both kinds of sequences over pages in one launch: w as for launch_attn_wide, d as for launch_attn_decode (nq 1).
 hipError_t launch_attn_mixed(const AttnArgs &w, const AttnArgs &d, int head_dim, int shares, hipStream_t stream);
 

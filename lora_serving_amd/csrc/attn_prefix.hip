@@ -28,10 +28,11 @@ __global__ __launch_bounds__(256, 2) void attn_prefix_kernel(AttnArgs s, AttnArg
     if (!mixed_place(shared + (WIDE ? wide_x * w.n_chunks : 0), shares, &i)) {
         attn_decode_body<D, NQ, FP8, KEYS_OWN>(d, i, shares, smem);
     } else if (WIDE && i < wide_x * w.n_chunks) {
-        // (the longer ones: one bf16 part of a probability, as in chunks of mlora_paged_attention.  Of up to 1.36 times the rms
-        // error of a result that is rounded alone, e4m3 1.45; two parts 1.0, but 128 tokens and a chunk of 1024 behind 8000
-        // keys 272 us, so 227, e4m3 325 and 277)
-        attn_wide_pages<D, SRC, KEYS_OWN>(w, (int)(i % wide_x), (int)(i / wide_x), (int)wide_x, smem);
+        // (the longer ones: over a bf16 cache one bf16 part of a probability, as in chunks of mlora_paged_attention: up to 1.36
+        // times the rms error of a result that is rounded alone; two parts 1.0, but 128 tokens and a chunk of 1024 behind 8000
+        // keys 272 us, so 227.  e4m3: see key_parts; 277 us with one part, with two 322)
+        attn_wide_pages<D, SRC, KEYS_OWN, key_parts<KEYS_OWN, FP8, 1>>(w, (int)(i % wide_x), (int)(i / wide_x), (int)wide_x,
+                                                                       smem);
     } else {
         if (WIDE)
             i -= wide_x * w.n_chunks;

@@ -90,3 +90,23 @@ def test_a_few_tokens_a_sequence_behind_prefixes(m, case):  # noqa: F811
         ref, _, mag, big = ref_attention(b.q[at:at + n].double(), k, v, True, 0, d ** -0.5)
         check(out[at:at + n], ref, mag, big, (n, L))
         at += n
+
+
+CHUNKS = [
+    # groups, sequences of no group, hq, hkv, d, page: chunks of up to 256 rows, which share, and of more, which do not
+    ([after(200, (100, 300), (1, 5), (60, 60))], [(33, 900)], 8, 2, 128, 16),
+    ([after(65, (64, 64), (40, 700), (2, 2)), after(300, (1, 9), (90, 90))], [(70, 70)], 4, 1, 64, 32),
+    ([after(130, *[(40, 40 + 9 * i) for i in range(40)])], [(1, 300)], 4, 2, 64, 16),    # more row blocks than workgroups
+]
+
+
+@pytest.mark.parametrize("case", CHUNKS, ids=lambda c: "-".join(str(v) for v in c).replace(" ", "")[-50:])
+def test_chunks_behind_prefixes_of_an_e4m3_cache(m, case):  # noqa: F811
+    groups, tail, hq, hkv, d, page = case
+    b = Batch(m, gen(19 * hq + d), groups, hq, hkv, d, page, True, tail)
+    out = b.run()
+    at = 0
+    for (n, L), (k, v) in zip(b.seqs, b.vals):
+        ref, _, mag, big = ref_attention(b.q[at:at + n].double(), k, v, True, 0, d ** -0.5)
+        check(out[at:at + n], ref, mag, big, (n, L))
+        at += n
