@@ -40,7 +40,8 @@ __global__ __launch_bounds__(256, 2) void attn_prefix_kernel(AttnArgs s, AttnArg
     }
 }
 
-// The parts of a row, joined by D / 4 lanes (`lane` of them; a row's lanes are in step): parts [0, n) at slot(c).
+// The parts of a row, joined by D / 4 lanes (`lane` of them; a row's lanes are in step): parts [0, n) at slot(c).  (join_parts
+// takes a wave a row; here every row has parts, and a wave's loads of 16 bytes a lane serve 2 or 4 rows.)
 template <int D, class Slot>
 __device__ __forceinline__ void join_row(const AttnArgs &a, int n, Slot slot, int64_t t, int hd, int lane)
 {
